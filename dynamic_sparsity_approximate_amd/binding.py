@@ -60,6 +60,24 @@ class effort_desc(ctypes.Structure):
         return d
 
 
+EFFORT_F32, EFFORT_F16, EFFORT_BF16 = 0, 1, 2
+EFFORT_KV_E4M3, EFFORT_KV_I8 = 0, 1
+EFFORT_KV_MIN_EXP = -64
+EFFORT_KV_MAX_SEQS = 1024
+
+
+class effort_kv_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class effort_kv_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError("libeffort.so is not built (python dynamic_sparsity_approximate_amd/build.py)")
 # One HIP runtime per process: torch ships its own libamdhip64 (soname
@@ -74,6 +92,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 _p, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _D = ctypes.POINTER(effort_desc)
+_KC, _KB, _f64 = ctypes.POINTER(effort_kv_cache), ctypes.POINTER(effort_kv_batch), ctypes.c_double
 _PROTOS = {
     "effort_strerror": ([ctypes.c_int], ctypes.c_char_p),
     "effort_last_hip_error": ([], ctypes.c_char_p),
@@ -105,6 +124,14 @@ _PROTOS = {
     "dense_gemm_small": ([_p, _p, _i32, _i64, _i64, _p, _p], ctypes.c_int),
     "effort_silu_mul": ([_p, _p, _i64, _p, _p], ctypes.c_int),
     "effort_axpby": ([_p, _f32, _p, _f32, _i64, _p, _p], ctypes.c_int),
+    "effort_rope_table": ([_f64, _i64, _i32, _p, _p], ctypes.c_int),
+    "effort_kv_append": ([_KC, _KB, _i32, _p, _i64, _i32, _i32, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64,
+                          _p], ctypes.c_int),
+    "effort_kv_workspace_bytes": ([_KC, _i32, _i64, _i32, ctypes.POINTER(_u64)], ctypes.c_int),
+    "effort_kv_attention": ([_KC, _KB, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
+                            ctypes.c_int),
+    "effort_norm_residual": ([_i32, _i64, _i64, _p, _i64, _i32, _p, _i64, _p, _p, _i64, _f32, _p, _f32, _p,
+                              _i64, _p, _i64, _p], ctypes.c_int),
     "effort_event_create": ([ctypes.POINTER(_p)], ctypes.c_int),
     "effort_event_record": ([_p, _p], ctypes.c_int),
     "effort_event_elapsed_ms": ([_p, _p, ctypes.POINTER(_f32)], ctypes.c_int),
@@ -375,6 +402,41 @@ def effort_silu_mul(h1, h3, n: int, out, stream=None):
 
 def effort_axpby(a, ga: float, b, gb: float, n: int, out, stream=None):
     _check(_lib.effort_axpby(_ptr(a), ga, _ptr(b), gb, n, _ptr(out), _stream(stream)), "effort_axpby")
+
+
+def effort_rope_table(base: float, rows: int, rot_dim: int, table, stream=None):
+    _check(_lib.effort_rope_table(base, rows, rot_dim, _ptr(table), _stream(stream)), "effort_rope_table")
+
+
+def effort_kv_append(cache, batch, dtype: int, rope, rope_rows: int, rot_dim: int, interleaved: int, q,
+                     q_stride: int, q_heads: int, q_out, q_out_stride: int, k, k_stride: int, v, v_stride: int,
+                     stream=None):
+    _check(_lib.effort_kv_append(ctypes.byref(cache), ctypes.byref(batch), dtype, _ptr(rope), rope_rows, rot_dim,
+                                 interleaved, _ptr(q), q_stride, q_heads, _ptr(q_out), q_out_stride, _ptr(k),
+                                 k_stride, _ptr(v), v_stride, _stream(stream)), "effort_kv_append")
+
+
+def effort_kv_workspace_bytes(cache, seqs: int, tokens: int, q_heads: int) -> int:
+    b = _u64()
+    _check(_lib.effort_kv_workspace_bytes(ctypes.byref(cache), seqs, tokens, q_heads, ctypes.byref(b)),
+           "effort_kv_workspace_bytes")
+    return int(b.value)
+
+
+def effort_kv_attention(cache, batch, dtype: int, q, q_stride: int, q_heads: int, scale: float, window: int, out,
+                        out_stride: int, ws, ws_bytes: int, stream=None):
+    _check(_lib.effort_kv_attention(ctypes.byref(cache), ctypes.byref(batch), dtype, _ptr(q), q_stride, q_heads,
+                                    scale, window, _ptr(out), out_stride, _ptr(ws), ws_bytes, _stream(stream)),
+           "effort_kv_attention")
+
+
+def effort_norm_residual(dtype: int, rows: int, n: int, x, x_stride: int, resid_dtype: int, resid,
+                         resid_stride: int, post_w, gate, gate_stride: int, scale: float, pre_w, eps: float,
+                         resid_out, resid_out_stride: int, out, out_stride: int, stream=None):
+    _check(_lib.effort_norm_residual(dtype, rows, n, _ptr(x), x_stride, resid_dtype, _ptr(resid), resid_stride,
+                                     _ptr(post_w), _ptr(gate), gate_stride, scale, _ptr(pre_w), eps,
+                                     _ptr(resid_out), resid_out_stride, _ptr(out), out_stride, _stream(stream)),
+           "effort_norm_residual")
 
 
 def effort_event_create() -> int:

@@ -34,7 +34,11 @@ DEVICE = ["--offload-arch=" + ARCH, "-munsafe-fp-atomics", "-fno-gpu-flush-denor
 
 SOURCES = [
     ("kernels.hip", DEVICE + ["-x", "hip"]),
+    ("kv_append.hip", DEVICE + ["-x", "hip"]),
+    ("kv_attend.hip", DEVICE + ["-x", "hip"]),
+    ("norm.hip", DEVICE + ["-x", "hip"]),
     ("api.cpp", ["-D__HIP_PLATFORM_AMD__"]),
+    ("layer_api.cpp", ["-D__HIP_PLATFORM_AMD__"]),
     ("convert.cpp", []),
 ]
 
@@ -50,7 +54,7 @@ def _compile(src, extra):
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=3) as ex:
+    with ThreadPoolExecutor(max_workers=6) as ex:
         objs = list(ex.map(lambda s: _compile(*s), SOURCES))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + ["-lpthread"]

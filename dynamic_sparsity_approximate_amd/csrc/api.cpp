@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "effort.h"
+#include "host.hpp"
 #include "kernels.hpp"
 #include "layout.hpp"
 
@@ -25,16 +26,21 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 thread_local hipError_t t_last_hip_error = hipSuccess;  // what effort_last_hip_error() reports
+// Device property cache (immutable per device; threads may fill it concurrently
+// with the same value).
+std::atomic<int> g_cu_count[kMaxDevices];
 
-// Records a failed HIP status for effort_last_hip_error().
+}  // namespace
+
+namespace effort {
+
 bool hip_failed(hipError_t e) {
   if (e == hipSuccess) return false;
   t_last_hip_error = e;
   return true;
 }
-// Device property cache (immutable per device; threads may fill it concurrently
-// with the same value).
-std::atomic<int> g_cu_count[kMaxDevices];
+
+int status_of(hipError_t e) { return hip_failed(e) ? EFFORT_EHIP : EFFORT_OK; }
 
 int cu_count() {
   int dev = 0;
@@ -50,14 +56,14 @@ int cu_count() {
   return cus;
 }
 
-int status_of(hipError_t e) { return hip_failed(e) ? EFFORT_EHIP : EFFORT_OK; }
+}  // namespace effort
+
+namespace {
 
 bool stream_capturing(hipStream_t s) {
   hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
   return hipStreamIsCapturing(s, &st) == hipSuccess && st != hipStreamCaptureStatusNone;
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_desc(const effort_desc* d, Geometry* g) {
   if (!d) return EFFORT_EINVAL;

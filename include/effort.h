@@ -339,6 +339,145 @@ int effort_silu_mul(const float* h1_dev, const float* h3_dev, int64_t n, float* 
 int effort_axpby(const float* a_dev, float ga, const float* b_dev, float gb, int64_t n,
                  float* out_dev, void* stream);
 
+/* ---------------------------------------------------------------- between the matvecs of a decoder layer */
+
+/* What a decoder layer needs between its matvecs: the rotation of queries and
+   keys by their positions, a paged cache of keys and values held in 8 bits,
+   causal attention over that cache, and the sum into the residual with the
+   norms around it.  Nothing in this section needs a zeroed workspace, and no
+   call leaves state in one: a workspace is free again when the call's work on
+   the stream has run. */
+
+/* Types of q, k, v, out and of a norm's rows (`dtype` arguments). */
+#define EFFORT_F32 0
+#define EFFORT_F16 1
+#define EFFORT_BF16 2
+
+/* Formats of a cache: one byte per element, times its page's scale. */
+#define EFFORT_KV_E4M3 0 /* 1 sign, 4 exponent (bias 7), 3 fraction bits; largest 448; no infinities */
+#define EFFORT_KV_I8 1   /* two's complement, used from -127 to 127 */
+
+#define EFFORT_KV_MIN_EXP (-64)   /* least exponent of a scale that effort_kv_append writes */
+#define EFFORT_KV_MAX_SEQS 1024   /* sequences of one call */
+
+/* A paged cache.  Element (page, head, slot, i) of the keys stands for
+   k[((page * kv_heads + head) * page_tokens + slot) * head_dim + i], decoded,
+   times k_scale[page * kv_heads + head]; values alike.  Scales are
+   non-negative; a scale that is a NaN or infinite marks its page and head as
+   poisoned: every row that sees a token of it becomes NaN.  Codes behind a
+   sequence's end, and scales of pages no sequence uses, may hold anything;
+   the e4m3 codes 0x7F and 0xFF (NaN) must not occur in a sequence's tokens
+   (effort_kv_append writes none). */
+typedef struct effort_kv_cache {
+  int32_t format;      /* EFFORT_KV_* */
+  int32_t kv_heads;    /* 1..256 */
+  int32_t head_dim;    /* 64 or 128 */
+  int32_t page_tokens; /* 16, 32, 64 or 128: the tokens that share a scale */
+  int64_t pages;       /* 1..2^31 - 1 */
+  uint8_t* k;          /* device [pages][kv_heads][page_tokens][head_dim], 16-byte aligned */
+  uint8_t* v;
+  float* k_scale; /* device [pages][kv_heads] */
+  float* v_scale;
+} effort_kv_cache;
+
+/* The new tokens of a call and where they belong.  Rows q_starts[s] ..
+   q_starts[s + 1] - 1 of q, k, v and out are sequence s's new tokens, its last
+   ones: with n of them, token i has position kv_lens[s] - n + i, in slot
+   (position mod page_tokens) of page page_table[s][position / page_tokens].
+   All three arrays are read by the kernels alone, so a captured call follows
+   their contents; the kernels check what they read:
+    - a token at a negative position, or behind the last page of the table, is
+      in no page: it is not stored, its q row is not written, and it sees only
+      what is in the table (nothing, at a negative position);
+    - a page id outside [0, pages) holds nothing: not stored to, not seen;
+    - q_starts is cut to [0, tokens]; rows that no sequence has stay as they were.
+   A page may stand in several sequences' tables (a shared prefix), but a page
+   that receives new tokens must stand in the table once. */
+typedef struct effort_kv_batch {
+  int32_t seqs;              /* 0..EFFORT_KV_MAX_SEQS */
+  int32_t max_pages;         /* columns of the page table; max_pages * page_tokens < 2^31 */
+  int64_t tokens;            /* rows of q, k, v, out; 0..2^24 */
+  int64_t table_stride;      /* elements between the rows of the page table, >= max_pages */
+  const int32_t* page_table; /* device [seqs][max_pages] */
+  const int32_t* kv_lens;    /* device [seqs]: tokens of each sequence, the new ones included */
+  const int32_t* q_starts;   /* device [seqs + 1], not decreasing */
+} effort_kv_batch;
+
+/* table_dev[row][pair] = (cos, sin) of row * base^(-2 pair / rot_dim), pair <
+   rot_dim / 2, computed in double and rounded once.  rows in 1..2^31 - 1,
+   rot_dim a multiple of 8 in 8..128, base > 1 and finite, else EINVAL. */
+int effort_rope_table(double base, int64_t rows, int32_t rot_dim, float* table_dev, void* stream);
+
+/* Rotates the new tokens' queries and keys, and appends keys and values to the
+   cache, in one launch.
+   Rotation: of a head's first rot_dim elements, pair j is (j, j + rot_dim / 2),
+   or (2j, 2j + 1) when `interleaved`; with (c, s) = rope_dev[position][j] it
+   becomes (a c - b s, b c + a s).  rope_dev: [rope_rows][rot_dim / 2][2]
+   floats, 8-byte aligned, rope_rows >= max_pages * page_tokens; rot_dim a
+   multiple of 8 in 8..head_dim, or 0 for no rotation (rope_dev unused).
+   q_out_dev may be q_dev (in place); it must not overlap q_dev in another way,
+   nor k_dev or v_dev.  q_dev NULL: keys and values only.
+   Scales: for each (page, head) that receives tokens, e is the least integer,
+   at least EFFORT_KV_MIN_EXP, for which the new elements' largest magnitude is
+   at most 2^e times the format's largest code.  A page whose slot 0 is new
+   takes the scale 2^e.  Another page keeps its scale s unless 2^e is larger;
+   then its older tokens become the nearest codes to code * s / 2^e (ties to
+   even) and its scale 2^e.  New elements become the nearest code to x / scale
+   (ties to even), with x rotated in double and not rounded before that: the
+   codes are the exact ones.  For e4m3 a larger scale loses nothing of the
+   older codes but what falls under its least exponent.
+   A new element that is a NaN or infinite poisons its page and head: the scale
+   becomes a NaN until the page is started anew, its new codes are 0.
+   Strides are in elements between tokens; a token's heads are contiguous.
+   EINVAL: null or misaligned pointers, sizes outside the stated ranges, a
+   stride below its row. */
+int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
+                     const float* rope_dev, int64_t rope_rows, int32_t rot_dim, int32_t interleaved,
+                     const void* q_dev, int64_t q_stride, int32_t q_heads, void* q_out_dev,
+                     int64_t q_out_stride, const void* k_dev, int64_t k_stride, const void* v_dev,
+                     int64_t v_stride, void* stream);
+
+/* Workspace bytes of effort_kv_attention for `seqs` sequences and `tokens` new
+   tokens of q_heads query heads (a multiple of kv_heads, at most 64 times it). */
+int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
+                              int32_t q_heads, uint64_t* bytes);
+
+/* Causal attention of the new tokens over the cache: query head h reads head
+   h / (q_heads / kv_heads) of the cache; the token at position p sees the
+   positions t <= p of its sequence, with window > 0 only those > p - window;
+     out = sum_t w_t value_t / sum_t w_t,  w_t = exp(scale * q . key_t).
+   A row that sees nothing becomes 0.  q and out: [tokens][q_heads][head_dim]
+   of `dtype`, strides in elements between tokens, heads contiguous; out must
+   not overlap q.  scale: finite.  Scores, weights and sums are held in 32
+   bits; with EFFORT_F32 the products keep 22 bits or more of q and of the
+   weights, with the 16-bit types 11 of the weights and all of q.
+   ws_dev: 256-byte aligned, of effort_kv_workspace_bytes; its contents do not
+   matter.  Calls that may overlap need one each. */
+int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
+                        const void* q_dev, int64_t q_stride, int32_t q_heads, float scale,
+                        int32_t window, void* out_dev, int64_t out_stride, void* ws_dev,
+                        uint64_t ws_bytes, void* stream);
+
+/* The end of one block and the start of the next, for rows x[rows][n]:
+     t = x / rms(x) * post_w     (post_w NULL: t = x)
+     r = resid + scale * gate * t  (resid NULL: no sum; gate NULL: 1)
+     out = r / rms(r) * pre_w
+   with rms(u) = sqrt(mean(u^2) + eps).  resid_out gets r in resid_dtype (NULL:
+   not stored), out gets the last line in dtype (NULL: not computed, pre_w is
+   then unused; NULL pre_w: no weight); at least one of the two is given.  The
+   sums and the values between the lines are held in 32 bits; `out` comes from
+   r before it is rounded.  gate: [n], or one row per row of x when gate_stride
+   > 0 (0: shared).  x, post_w, gate, pre_w and out are of `dtype`; resid and
+   resid_out of resid_dtype, which is `dtype` or EFFORT_F32.  Strides are in
+   elements between rows.  resid_out may be resid, and out may be x, with the
+   same stride; no other overlap of an output is allowed.
+   EINVAL also: rows < 0, n outside 1..2^20, eps negative or not finite. */
+int effort_norm_residual(int32_t dtype, int64_t rows, int64_t n, const void* x_dev, int64_t x_stride,
+                         int32_t resid_dtype, const void* resid_dev, int64_t resid_stride,
+                         const void* post_w_dev, const void* gate_dev, int64_t gate_stride,
+                         float scale, const void* pre_w_dev, float eps, void* resid_out_dev,
+                         int64_t resid_out_stride, void* out_dev, int64_t out_stride, void* stream);
+
 /* ---------------------------------------------------------------- measurement helpers */
 
 int effort_event_create(void** event_out);            /* hipEvent_t with timing */

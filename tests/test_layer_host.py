@@ -1,0 +1,171 @@
+"""Refusals of the operators between a decoder layer's matvecs: every check runs
+on the host before any device work, so none needs a GPU (the addresses given
+here are never read)."""
+import ctypes
+import math
+
+import pytest
+
+import dynamic_sparsity_approximate_amd as E
+from dynamic_sparsity_approximate_amd import binding as B
+
+A = 4096  # an address, aligned and never read
+
+
+def cache(**kw):
+    d = dict(format=E.EFFORT_KV_E4M3, kv_heads=8, head_dim=128, page_tokens=64, pages=10, k=A, v=A, k_scale=A,
+             v_scale=A)
+    d.update(kw)
+    return E.effort_kv_cache(**d)
+
+
+def batch(**kw):
+    d = dict(seqs=2, max_pages=4, tokens=3, table_stride=4, page_table=A, kv_lens=A, q_starts=A)
+    d.update(kw)
+    return E.effort_kv_batch(**d)
+
+
+APPEND = dict(cache=None, batch=None, dtype=E.EFFORT_F32, rope=A, rope_rows=256, rot_dim=128, interleaved=0, q=A,
+              q_stride=4096, q_heads=32, q_out=2 * A, q_out_stride=4096, k=A, k_stride=1024, v=A, v_stride=1024)
+ATTEND = dict(cache=None, batch=None, dtype=E.EFFORT_F32, q=A, q_stride=4096, q_heads=32, scale=0.1, window=0,
+              out=2 * A, out_stride=4096, ws=A, ws_bytes=1 << 40)
+NORM = dict(dtype=E.EFFORT_F32, rows=3, n=64, x=A, x_stride=64, resid_dtype=E.EFFORT_F32, resid=2 * A,
+            resid_stride=64, post_w=A, gate=A, gate_stride=0, scale=1.0, pre_w=A, eps=1e-5, resid_out=3 * A,
+            resid_out_stride=64, out=4 * A, out_stride=64)
+
+
+def call(fn, base, c=None, b=None, **kw):
+    args = dict(base, **kw)
+    if "cache" in args:
+        args["cache"], args["batch"] = c or cache(), b or batch()
+    return fn(*args.values(), stream=0)
+
+
+def refused(code, fn, base, **kw):
+    with pytest.raises(E.EffortError) as e:
+        call(fn, base, **kw)
+    assert e.value.code == code, e.value
+
+
+BAD_CACHE = [dict(format=2), dict(format=-1), dict(kv_heads=0), dict(kv_heads=257), dict(head_dim=96),
+             dict(page_tokens=8), dict(page_tokens=48), dict(pages=0), dict(pages=1 << 31), dict(k=None),
+             dict(v=A + 8), dict(k_scale=None), dict(v_scale=A + 2)]
+BAD_BATCH = [dict(seqs=-1), dict(seqs=1025), dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(max_pages=0),
+             dict(max_pages=1 << 25, table_stride=1 << 25), dict(table_stride=3), dict(page_table=None),
+             dict(kv_lens=A + 2), dict(q_starts=None)]
+
+
+@pytest.mark.parametrize("bad", BAD_CACHE)
+def test_bad_caches(bad):
+    refused(B.EFFORT_EINVAL, E.effort_kv_append, APPEND, c=cache(**bad))
+    refused(B.EFFORT_EINVAL, E.effort_kv_attention, ATTEND, c=cache(**bad))
+
+
+@pytest.mark.parametrize("bad", BAD_BATCH)
+def test_bad_batches(bad):
+    refused(B.EFFORT_EINVAL, E.effort_kv_append, APPEND, b=batch(**bad))
+    refused(B.EFFORT_EINVAL, E.effort_kv_attention, ATTEND, b=batch(**bad))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=3), dict(dtype=-1), dict(interleaved=2), dict(rot_dim=4), dict(rot_dim=136), dict(rot_dim=-8),
+    dict(rope=None), dict(rope=A + 4), dict(rope_rows=255), dict(q_heads=12), dict(q_heads=0),
+    dict(q_heads=8 * 65, q_stride=1 << 20, q_out_stride=1 << 20), dict(q_stride=4095), dict(q_out=None),
+    dict(q_out_stride=4095), dict(k=None), dict(k=A + 2), dict(k_stride=1023), dict(v=None), dict(v_stride=1023),
+    dict(q_out=A, q_out_stride=5000), dict(dtype=E.EFFORT_F16, v=A + 1)])
+def test_append_refuses(bad):
+    refused(B.EFFORT_EINVAL, E.effort_kv_append, APPEND, **bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=7), dict(q=None), dict(q=A + 2), dict(q_stride=4095), dict(q_heads=33), dict(scale=math.nan),
+    dict(scale=math.inf), dict(window=-1), dict(out=None), dict(out_stride=100), dict(out=A)])
+def test_attention_refuses(bad):
+    refused(B.EFFORT_EINVAL, E.effort_kv_attention, ATTEND, **bad)
+
+
+def test_attention_workspace():
+    need = E.effort_kv_workspace_bytes(cache(), 2, 3, 32)
+    if need:
+        refused(B.EFFORT_ENOSPACE, E.effort_kv_attention, ATTEND, ws_bytes=need - 1)
+        refused(B.EFFORT_EINVAL, E.effort_kv_attention, ATTEND, ws=None)
+        refused(B.EFFORT_EINVAL, E.effort_kv_attention, ATTEND, ws=A + 64)
+    for args in ((cache(), -1, 3, 32), (cache(), 2, -1, 32), (cache(), 2, 3, 31), (cache(head_dim=32), 2, 3, 32),
+                 (cache(), 1025, 3, 32)):
+        with pytest.raises(E.EffortError) as e:
+            E.effort_kv_workspace_bytes(*args)
+        assert e.value.code == B.EFFORT_EINVAL
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=5), dict(resid_dtype=E.EFFORT_F16), dict(rows=-1), dict(rows=1 << 31), dict(n=0),
+    dict(n=(1 << 20) + 1), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(x=None), dict(x=A + 2),
+    dict(x_stride=63), dict(resid=A + 2), dict(resid_stride=63), dict(gate_stride=63), dict(gate=A + 1),
+    dict(post_w=A + 2), dict(pre_w=A + 2), dict(resid_out=None, out=None), dict(out_stride=63),
+    dict(resid_out_stride=63), dict(resid_out=2 * A, resid_out_stride=70), dict(out=A, out_stride=70),
+    dict(out=2 * A), dict(out=3 * A), dict(resid_out=A)])
+def test_norm_refuses(bad):
+    refused(B.EFFORT_EINVAL, E.effort_norm_residual, NORM, **bad)
+
+
+@pytest.mark.parametrize("bad", [(1.0, 4, 64), (math.inf, 4, 64), (math.nan, 4, 64), (1e4, 0, 64), (1e4, 4, 0),
+                                 (1e4, 4, 12), (1e4, 4, 136)])
+def test_rope_table_refuses(bad):
+    with pytest.raises(E.EffortError) as e:
+        E.effort_rope_table(*bad, A, stream=0)
+    assert e.value.code == B.EFFORT_EINVAL
+    with pytest.raises(E.EffortError):
+        E.effort_rope_table(1e4, 4, 64, A + 4, stream=0)
+
+
+def test_nothing_to_do_needs_no_device():
+    for b in (batch(seqs=0, page_table=None, kv_lens=None, q_starts=None), batch(tokens=0)):
+        call(E.effort_kv_append, APPEND, b=b)
+        call(E.effort_kv_attention, ATTEND, b=b)
+    call(E.effort_norm_residual, NORM, rows=0)
+
+
+def test_struct_sizes_match_the_header():
+    assert ctypes.sizeof(E.effort_kv_cache) == 4 * 4 + 8 + 4 * 8
+    assert ctypes.sizeof(E.effort_kv_batch) == 2 * 4 + 2 * 8 + 3 * 8
+
+
+def test_python_layer_refuses():
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    k, s = z(4, 2, 16, 64, dtype=torch.uint8), z(4, 2)
+    ok = E.KVCache.wrap(k, k.clone(), s, s.clone())
+    for bad in ((k.float(), k, s, s), (k, k[:3], s, s), (k, k, s.double(), s), (k, k, s[:, :1], s),
+                (k.transpose(0, 1), k.transpose(0, 1), s.t(), s.t())):
+        with pytest.raises(ValueError):
+            E.KVCache.wrap(*bad)
+    i32 = dict(dtype=torch.int32)
+    b = E.KVBatch(z(3, 5, **i32), z(3, **i32), z(4, **i32))
+    for bad in ((z(3, 5), z(3, **i32), z(4, **i32)), (z(3, 5, **i32), z(2, **i32), z(4, **i32)),
+                (z(3, 5, **i32), z(3, **i32), z(3, **i32)), (z(5, 3, **i32).t(), z(3, **i32), z(4, **i32)),
+                (z(3, 5, **i32), z(6, **i32)[::2], z(4, **i32))):
+        with pytest.raises(ValueError):
+            E.KVBatch(*bad)
+    q, kv = z(2, 4, 64), z(2, 2, 64)
+    with pytest.raises(TypeError):
+        ok.attend(b, q.double())
+    for bad in (z(2, 4, 32), z(2, 256), z(2, 8, 64)[:, ::2]):
+        with pytest.raises(ValueError):
+            ok.attend(b, bad)
+    for bad in ((z(2, 3, 64), kv), (kv, z(3, 2, 64)), (kv, kv.half())):
+        with pytest.raises(ValueError):
+            ok.append(b, *bad)
+    with pytest.raises(ValueError):  # everything is right but the device
+        ok.attend(b, q)
+    with pytest.raises(ValueError):
+        ok.append(b, kv, kv, rope=z(3, 8))
+    with pytest.raises(ValueError):
+        E.norm_residual(z(2, 3, 4))
+    with pytest.raises(ValueError):
+        E.norm_residual(z(2, 4), z(2, 5))
+    with pytest.raises(TypeError):
+        E.norm_residual(z(2, 4), z(2, 4).half())
+    with pytest.raises(ValueError):
+        E.norm_residual(z(2, 4), pre_w=z(5))
+    with pytest.raises(ValueError):
+        E.norm_residual(z(2, 4), gate=z(3, 4))
