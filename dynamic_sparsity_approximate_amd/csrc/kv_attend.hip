@@ -1,104 +1,587 @@
 // kv_attend.hip -- causal attention over the paged 8-bit cache.
+//
+// For one sequence and one head of the cache, the rows of the products are the
+// (new token, query head of the group) pairs, token by token: row = token *
+// group + query head.  A wave multiplies 16 rows with 32 tokens at a time:
+//   S^T[token][row] = K Q^T, two 16x16x32 products per 32 elements of a head,
+//   O^T[element][row] += V^T P^T, one product per 16 elements of a head.
+// In S^T a lane holds its row (lane mod 16) at tokens (lane / 16) * 4 + 0..3 of
+// both 16-token halves: exactly the eight tokens that it has to supply of P^T
+// when the second product counts its tokens in that order, so the weights never
+// leave their lane, and a row's maximum, sum and rescaling are the lane's own
+// but for two exchanges across the four lanes of a row.
+// Codes become fp16 exactly (8 bits fit its 11); q is scaled per row by a power
+// of two into fp16's upper range.  With fp32 rows, q and the weights are taken
+// as two fp16 parts each (22 bits) and the products run twice.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
+#include "host.hpp"
 #include "layer.hpp"
 
 namespace effort {
 
-constexpr int AT_T = 64;
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 
-// One wave per (new token, query head), in one pass over the visible tokens,
-// 64 at a time: lane t's score of token t, the running maximum and sum, then
-// each lane its elements of the weighted sum of values.
-template <int DT, int FMT, int D>
-__global__ __launch_bounds__(AT_T) void k_attend_rows(AttendArgs a) {
-  typedef typename ElemOf<DT>::T T;
-  const int lane = (int)threadIdx.x;
-  const int32_t tok = (int32_t)blockIdx.x, head = (int32_t)blockIdx.y;
-  int lo = 0, hi = a.b.seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start_of(a.b, mid) <= tok) lo = mid; else hi = mid;
-  }
-  const int32_t s0 = start_of(a.b, lo), s1 = start_of(a.b, lo + 1);
-  if (tok < s0 || tok >= s1) return;
-  const int64_t len = a.b.lens[lo], pos = len - (s1 - s0) + (tok - s0);
-  const int64_t cap = (int64_t)a.b.max_pages * a.page_tokens;
-  const int64_t first = a.window && pos + 1 > a.window ? pos + 1 - a.window : 0;
-  const int64_t end = pos + 1 < cap ? pos + 1 : cap;
-  const int kvh = head / (a.q_heads / a.kv_heads);
-  __shared__ float q[D];
-  __shared__ float p[AT_T];
-  __shared__ int64_t base[AT_T];
-  __shared__ float vscale[AT_T];
-  const T* row = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * D;
-  for (int i = lane; i < D; i += AT_T) q[i] = (float)row[i];
-  __syncthreads();
-  float m = -INFINITY, l = 0.0f, acc[D / AT_T];
-#pragma unroll
-  for (int i = 0; i < D / AT_T; ++i) acc[i] = 0.0f;
-  for (int64_t t0 = first; t0 < end; t0 += AT_T) {
-    const int64_t t = t0 + lane;
-    float s = -INFINITY;
-    int64_t at = -1;
-    if (t < end) {
-      const int32_t page = a.b.table[lo * a.b.table_stride + t / a.page_tokens];
-      if (page >= 0 && page < a.b.pages) {
-        const int64_t ph = (int64_t)page * a.kv_heads + kvh;
-        at = (ph * a.page_tokens + t % a.page_tokens) * D;
-        float dot = 0.0f;
-        for (int i = 0; i < D; ++i) dot = __builtin_fmaf(q[i], decode<FMT>(a.kc[at + i]), dot);
-        const float ks = a.ks[ph], vs = a.vs[ph];
-        s = dot * ks * a.scale;
-        const bool bad = !(fabsf(ks) < INFINITY) || !(fabsf(vs) < INFINITY);
-        if (bad) s = __uint_as_float(0x7FC00000u);
-        vscale[lane] = bad ? 1.0f : vs;
-      }
-    }
-    base[lane] = at;
-    float top = at >= 0 ? s : -INFINITY;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float mn = fmaxf(m, top);
-    // mn is -inf where nothing but NaN scores has been seen: they stay NaN
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float w = at >= 0 ? expf(s - ref) : 0.0f;
-    p[lane] = w;
-    __syncthreads();
-    const float alpha = expf(m - ref);
-    m = mn;
-    float sum = w;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-    l = l * alpha + sum;
-#pragma unroll
-    for (int i = 0; i < D / AT_T; ++i) acc[i] *= alpha;
-    for (int j = 0; j < AT_T; ++j) {
-      const int64_t b = base[j];
-      if (b < 0) continue;
-      const float pv = p[j] * vscale[j];
-#pragma unroll
-      for (int i = 0; i < D / AT_T; ++i)
-        acc[i] = __builtin_fmaf(pv, decode<FMT>(a.vc[b + lane + i * AT_T]), acc[i]);
-    }
-    __syncthreads();
-  }
-  T* out = static_cast<T*>(a.out) + tok * a.out_stride + (int64_t)head * D;
-#pragma unroll
-  for (int i = 0; i < D / AT_T; ++i) out[lane + i * AT_T] = (T)(l == 0.0f ? 0.0f : acc[i] / l);
+constexpr int AT_T = 256, AT_W = AT_T / 64;
+constexpr int AT_TILE = 32;              // tokens of one step of a wave
+constexpr int AT_CHUNK = AT_W * AT_TILE; // tokens of one step of a block
+constexpr float kLog2e = 1.4426950408889634f;
+// Weights are held times 2^13: a unit of values (below) may make them twice as
+// large, still inside fp16, and fp16's subnormals begin 2^-27 below the largest.
+constexpr float kWeightExp = 13.0f;
+
+// ---------------------------------------------------------------- pieces of both products
+
+__device__ inline float max_of_row(float x) {  // over the four lanes that share a row
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-uint64_t attend_workspace(int32_t, int32_t, int32_t, int64_t, int32_t) { return 0; }
+__device__ inline float sum_of_row(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Two codes (bytes 0, 1 or 2, 3 of w) as fp16, exactly.
+template <int FMT, bool HI>
+__device__ inline h2 decode2(uint32_t w) {
+  if (FMT == EFFORT_KV_I8) {
+    // code + 128 in the low bits of the fp16 number 1024 + (code + 128)
+    const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w ^ 0x80808080u, HI ? 0x07030602u : 0x05010400u);
+    const h2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    return __builtin_bit_cast(h2, u) - bias;
+  }
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
+}
+
+__device__ inline h8 join8(h2 a, h2 b, h2 c, h2 d) {
+  return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <int FMT>
+__device__ inline h8 decode8(uint32_t lo, uint32_t hi) {
+  return join8(decode2<FMT, false>(lo), decode2<FMT, true>(lo), decode2<FMT, false>(hi), decode2<FMT, true>(hi));
+}
+
+// Eight weights as fp16, and what that leaves off as fp16 too.
+__device__ inline h8 weights8(const float* p) {
+  h8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = (_Float16)p[i];
+  return r;
+}
+
+__device__ inline h8 rest8(const float* p, h8 w) {
+  h8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = (_Float16)(p[i] - (float)w[i]);
+  return r;
+}
+
+// ---------------------------------------------------------------- who does what
+
+// A sequence's part of a call.
+struct Seq {
+  int32_t first, n;   // its rows of q
+  int64_t pos;        // position of its first new token
+  int32_t lo, hi;     // tokens that any row sees, lo a multiple of AT_TILE
+  int32_t tiles;      // row tiles of `rows` rows
+  int32_t chunks;     // of AT_CHUNK tokens
+};
+
+__device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
+  Seq q;
+  const int32_t s0 = start_of(a.b, s), s1 = start_of(a.b, s + 1);
+  q.first = s0;
+  q.n = s1 > s0 ? s1 - s0 : 0;
+  const int64_t len = a.b.lens[s], cap = (int64_t)a.b.max_pages * a.page_tokens;
+  q.pos = len - q.n;
+  const int64_t from = a.window && q.pos + 1 > a.window ? q.pos + 1 - a.window : 0;
+  const int64_t to = len < cap ? len : cap;
+  q.tiles = (int32_t)(((int64_t)q.n * group + rows - 1) / rows);
+  q.chunks = 0;
+  q.lo = q.hi = 0;
+  if (q.n > 0 && to > from) {
+    q.lo = (int32_t)(from & ~(int64_t)(AT_TILE - 1));
+    q.hi = (int32_t)to;
+    q.chunks = (int32_t)((to - q.lo + AT_CHUNK - 1) / AT_CHUNK);
+  }
+  return q;
+}
+
+// Chunks before each sequence, in before[0 .. seqs]; every block computes it
+// from the lengths, so that a captured call follows them.
+__device__ void plan(const AttendArgs& a, int group, int rows, uint64_t* before, uint64_t* part) {
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int PER = EFFORT_KV_MAX_SEQS / AT_T;
+  uint64_t mine[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = tid * PER + i;
+    mine[i] = sum;
+    if (s < a.b.seqs) {
+      const Seq q = seq_of(a, s, group, rows);
+      sum += (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+    }
+  }
+  uint64_t run = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up(run, d);
+    if (lane >= d) run += o;
+  }
+  if (lane == 63) part[wave] = run;
+  __syncthreads();
+  uint64_t base = run - sum;
+  for (int w = 0; w < wave; ++w) base += part[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = tid * PER + i;
+    if (s <= a.b.seqs) before[s] = base + mine[i];
+  }
+  if (tid == AT_T - 1 && a.b.seqs == EFFORT_KV_MAX_SEQS) before[EFFORT_KV_MAX_SEQS] = base + sum;
+  __syncthreads();
+}
+
+// The sequence that owns chunk c: the last one with before[s] <= c among those that have chunks.
+__device__ inline int owner(const uint64_t* before, int seqs, uint64_t c) {
+  int lo = 0, hi = seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= c) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- split over blocks
+
+// One 32-token step's codes and scales of a head, as loaded.
+template <int D>
+struct Codes {
+  uint4 k[2][D / 64];
+  uint32_t v[2][4][D / 64];
+  float ks[2], vs[2];
+  bool ok[2];
+};
+
+template <int D>
+__device__ inline void load_codes(const AttendArgs& a, const int32_t* table, int head, int32_t t, int32_t hi,
+                                  int shift, Codes<D>* c) {
+  const int lane = (int)threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int32_t tok = t + 16 * u;
+    int32_t page = -1;
+    if (tok < hi) page = table[tok >> shift];
+    page = __builtin_amdgcn_readfirstlane(page);
+    c->ok[u] = page >= 0 && page < a.b.pages;
+    const int64_t ph = (int64_t)(c->ok[u] ? page : 0) * a.kv_heads + head;  // page 0: read, never used
+    const int64_t at = ((ph << shift) + (tok & ((1 << shift) - 1))) * D;
+    const uint8_t* kp = a.kc + at + i * D + g * 16;
+    const uint8_t* vp = a.vc + at + g * 4 * D + i * (D / 16);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) c->k[u][x] = *reinterpret_cast<const uint4*>(kp + 64 * x);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(vp + r * D);
+        c->v[u][r][0] = w.x;
+        c->v[u][r][D / 64 - 1] = w.y;
+      } else {
+        c->v[u][r][0] = *reinterpret_cast<const uint32_t*>(vp + r * D);
+      }
+    }
+    c->ks[u] = a.ks[ph];
+    c->vs[u] = a.vs[ph];
+  }
+}
+
+// Blocks share the (sequence, head, row tile) items' chunks evenly, in order:
+// block b takes the chunks [b W / B, (b + 1) W / B) of all W (B: the grid, or W if that is less).  An item that one
+// block has whole is finished there; the others leave (maximum, sum, weighted
+// values) of their part for k_attend_join.  A decode batch of unequal lengths
+// keeps every CU busy to the end without the host knowing the lengths.
+// `RT`: 16-row tiles of an item.
+template <int DT, int FMT, int D, int RT>
+__global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* parts) {
+  typedef typename ElemOf<DT>::T T;
+  constexpr bool SPLIT = DT == EFFORT_F32;
+  constexpr int KS = D / 32, ND = D / 16, ROWS = 16 * RT, LD = D + 4;
+  __shared__ uint64_t before[EFFORT_KV_MAX_SEQS + 1];
+  __shared__ uint64_t part[AT_W];
+  __shared__ float s_o[AT_W][ROWS][LD];
+  __shared__ float s_m[AT_W][ROWS], s_l[AT_W][ROWS], s_u[AT_W];
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, j = lane & 15, g = lane >> 4;
+  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens);
+  plan(a, group, ROWS, before, part);
+  const uint64_t total = before[a.b.seqs], nb = total < gridDim.x ? total : gridDim.x;  // no block has nothing
+  if (blockIdx.x >= nb) return;
+  uint64_t c = total * blockIdx.x / nb;
+  const uint64_t c_end = total * (blockIdx.x + 1) / nb;
+  int s = owner(before, a.b.seqs, c);
+  while (c < c_end) {
+    while (before[s + 1] <= c) ++s;
+    const Seq q = seq_of(a, s, group, ROWS);
+    const uint64_t in = c - before[s];
+    const uint32_t item = (uint32_t)(in / q.chunks), ch0 = (uint32_t)(in % q.chunks);
+    const int head = (int)(item / (uint32_t)q.tiles), tile = (int)(item % (uint32_t)q.tiles);
+    const uint32_t left = q.chunks - ch0;
+    const uint32_t take = c_end - c < left ? (uint32_t)(c_end - c) : left;
+    const bool whole = ch0 == 0 && take == (uint32_t)q.chunks;
+    const int32_t* table = a.b.table + s * a.b.table_stride;
+    const int rows = q.n * group - tile * ROWS < ROWS ? q.n * group - tile * ROWS : ROWS;
+
+    // the rows' queries, scaled by a power of two to at most 2^14
+    h8 qh[RT][KS], ql[RT][KS];
+    float f[RT];
+    int64_t p[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      int r = rt * 16 + j;
+      r = tile * ROWS + (r < rows ? r : rows - 1);  // rows behind the last one repeat it
+      const int i = r / group;
+      p[rt] = q.pos + i;
+      const T* src = static_cast<const T*>(a.q) + (q.first + i) * a.q_stride +
+                     (int64_t)(head * group + r - i * group) * D + g * 16;
+      float x[KS][8], top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[k][e] = (float)src[(k >> 1) * 64 + (k & 1) * 8 + e];
+          top = fmaxf(top, fabsf(x[k][e]));
+        }
+      }
+      top = max_of_row(top);
+      int up = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
+      up = top > 0.0f && top < INFINITY ? (up > 100 ? 100 : up) : 0;
+      const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+      f[rt] = a.scale * kLog2e / by;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] *= by;
+        qh[rt][k] = weights8(x[k]);
+        if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
+      }
+    }
+    const int32_t row0 = tile * ROWS, row1 = row0 + rows - 1;
+    const int64_t p_min = q.pos + row0 / group, p_max = q.pos + row1 / group;
+
+    f4 o[RT][ND];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      m[rt] = -INFINITY;
+      l[rt] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // O counts in `unit`s: a value is code * scale, and scales that equal the
+    // unit (mostly all of them: powers of two) cost nothing.  The unit follows
+    // the scales up at once, down when they are 2^10 smaller.
+    float unit = 1.0f, unit_top = 0.0f;
+    const int32_t t_begin = q.lo + (int32_t)(ch0 * AT_CHUNK) + wave * AT_TILE;
+    const int64_t stop = (int64_t)q.lo + (int64_t)(ch0 + take) * AT_CHUNK;
+    const int32_t t_end = stop < q.hi ? (int32_t)stop : q.hi;
+
+    Codes<D> nxt;
+    if (t_begin < t_end) load_codes<D>(a, table, head, t_begin, q.hi, shift, &nxt);
+    for (int32_t t = t_begin; t < t_end; t += AT_CHUNK) {
+      Codes<D> cur = nxt;
+      if (t + AT_CHUNK < t_end) load_codes<D>(a, table, head, t + AT_CHUNK, q.hi, shift, &nxt);
+      const bool full = cur.ok[0] && cur.ok[1] && t + AT_TILE <= q.hi && t + AT_TILE - 1 <= p_min &&
+                        (a.window == 0 || t > p_max - a.window);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // a poisoned page: its scores are NaN, its values count as any
+        if (!(fabsf(cur.ks[u]) < INFINITY) || !(fabsf(cur.vs[u]) < INFINITY)) {
+          cur.ks[u] = __uint_as_float(0x7FC00000u);
+          cur.vs[u] = unit;
+        }
+      }
+      if (!full) {  // values of tokens that no row sees weigh 0, so they must not be NaN
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!cur.ok[u] || t + 16 * u + g * 4 + r >= q.hi ||
+                (a.window && t + 16 * u + g * 4 + r <= p_min - a.window)) {
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x) cur.v[u][r][x] = 0u;
+            }
+      }
+      // scores
+      f4 sc[RT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint4 w = cur.k[u][k >> 1];
+          const h8 kf = (k & 1) ? decode8<FMT>(w.z, w.w) : decode8<FMT>(w.x, w.y);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[rt][k], sc[rt][u], 0, 0, 0);
+            if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[rt][k], sc[rt][u], 0, 0, 0);
+          }
+        }
+      }
+      float w[RT][8];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float fu = f[rt] * cur.ks[u];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            w[rt][u * 4 + r] = sc[rt][u][r] * fu;
+            if (!full) {
+              const int64_t at = t + 16 * u + g * 4 + r;
+              const bool seen = cur.ok[u] && at < q.hi && at <= p[rt] && (a.window == 0 || at > p[rt] - a.window);
+              if (!seen) w[rt][u * 4 + r] = -INFINITY;
+            }
+          }
+        }
+        float top = w[rt][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, w[rt][i]);
+        top = max_of_row(top);
+        if (__any(top > m[rt])) {
+          const float mn = fmaxf(top, m[rt]);
+          const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
+          m[rt] = mn;
+          l[rt] *= alpha;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
+        }
+        // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+        const float ref = (m[rt] == -INFINITY ? 0.0f : m[rt]) - kWeightExp;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[rt][i] = __builtin_amdgcn_exp2f(w[rt][i] - ref);
+          l[rt] += w[rt][i];
+        }
+      }
+      // Halves whose scales are far apart are weighed one after the other: the
+      // smaller's weights would lose bits below the larger's.
+      const float v0 = cur.ok[0] ? cur.vs[0] : 0.0f, v1 = cur.ok[1] ? cur.vs[1] : 0.0f;
+      const bool apart = cur.ok[0] && cur.ok[1] && fmaxf(v0, v1) > 0x1p10f * fminf(v0, v1);
+#pragma unroll 1
+      for (int pass = 0; pass < (apart ? 2 : 1); ++pass) {
+        const float s0 = pass == 0 ? v0 : 0.0f, s1 = apart && pass == 0 ? 0.0f : v1, top = fmaxf(s0, s1);
+        unit_top = fmaxf(unit_top, top);
+        if (top > 2.0f * unit || top < 0x1p-10f * unit) {
+          // not so far down that what is there could overflow
+          const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f);
+          const float by = unit / now;
+          unit = now;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[rt][d] *= by;
+        }
+        const float rel[2] = {s0 / unit, s1 / unit};
+        h8 ph[RT], pl[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = w[rt][i] * rel[i >> 2];
+          ph[rt] = weights8(y);
+          if (SPLIT) pl[rt] = rest8(y, ph[rt]);
+        }
+        // weighted values: element n * ND + d of a head is row n of product d
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          uint32_t e[2][4];  // [token pairs 01 | 23 of a half..][bytes 0 1 of both tokens, 2 3 of both]
+          uint32_t e2[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            e[u][0] = __builtin_amdgcn_perm(cur.v[u][1][x], cur.v[u][0][x], 0x05010400u);
+            e[u][1] = __builtin_amdgcn_perm(cur.v[u][3][x], cur.v[u][2][x], 0x05010400u);
+            e2[u][0] = __builtin_amdgcn_perm(cur.v[u][1][x], cur.v[u][0][x], 0x07030602u);
+            e2[u][1] = __builtin_amdgcn_perm(cur.v[u][3][x], cur.v[u][2][x], 0x07030602u);
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            h8 vf;
+            if (d == 0)
+              vf = join8(decode2<FMT, false>(e[0][0]), decode2<FMT, false>(e[0][1]), decode2<FMT, false>(e[1][0]),
+                         decode2<FMT, false>(e[1][1]));
+            else if (d == 1)
+              vf = join8(decode2<FMT, true>(e[0][0]), decode2<FMT, true>(e[0][1]), decode2<FMT, true>(e[1][0]),
+                         decode2<FMT, true>(e[1][1]));
+            else if (d == 2)
+              vf = join8(decode2<FMT, false>(e2[0][0]), decode2<FMT, false>(e2[0][1]),
+                         decode2<FMT, false>(e2[1][0]), decode2<FMT, false>(e2[1][1]));
+            else
+              vf = join8(decode2<FMT, true>(e2[0][0]), decode2<FMT, true>(e2[0][1]), decode2<FMT, true>(e2[1][0]),
+                         decode2<FMT, true>(e2[1][1]));
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              f4& acc = o[rt][x * 4 + d];
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph[rt], acc, 0, 0, 0);
+              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[rt], acc, 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+
+    // the four waves' parts become one
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float lt = sum_of_row(l[rt]);
+      if (g == 0) {
+        s_m[wave][rt * 16 + j] = m[rt];
+        s_l[wave][rt * 16 + j] = lt;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int x = 0; x < ND / 4; ++x)
+          *reinterpret_cast<f4*>(&s_o[wave][rt * 16 + j][(g * 4 + r) * ND + x * 4]) =
+              f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]};
+    }
+    if (lane == 0) s_u[wave] = unit;
+    __syncthreads();
+    // slot 0: a part that does not start its item, slot 1: one that does
+    float* mine = parts + ((int64_t)blockIdx.x * 2 + (ch0 == 0 ? 1 : 0)) * ROWS * (D + 2);
+    for (int i = tid; i < rows * (D / 4); i += AT_T) {
+      const int r = i / (D / 4), x = (i % (D / 4)) * 4;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < AT_W; ++w) top = fmaxf(top, s_m[w][r]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < AT_W; ++w) {
+        const float e = __builtin_amdgcn_exp2f(s_m[w][r] - ref);
+        // a wave that saw only NaN has no maximum: its sum stays NaN
+        sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * e;
+        v += *reinterpret_cast<const f4*>(&s_o[w][r][x]) * (e * s_u[w]);
+      }
+      if (whole) {
+        const int row = tile * ROWS + r, tok = row / group;
+        T* out = static_cast<T*>(a.out) + (q.first + tok) * a.out_stride +
+                 (int64_t)(head * group + row - tok * group) * D + x;
+        const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * by);
+      } else {
+        *reinterpret_cast<f4*>(mine + r * D + x) = v;
+        if (x == 0) {
+          mine[ROWS * D + r] = top;
+          mine[ROWS * D + ROWS + r] = sum;
+        }
+      }
+    }
+    c += take;
+  }
+}
+
+// Joins the parts that blocks left of an item, and writes the rows that see
+// nothing.  One block per (row tile, head); tiles of a sequence are counted
+// from first * group / ROWS + s, enough for every sequence before it.
+template <int DT, int D, int RT>
+__global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32) {
+  typedef typename ElemOf<DT>::T T;
+  constexpr int ROWS = 16 * RT;
+  __shared__ uint64_t before[EFFORT_KV_MAX_SEQS + 1];
+  __shared__ uint64_t part[AT_W];
+  __shared__ int s_seq;
+  const int tid = (int)threadIdx.x, head = (int)blockIdx.y;
+  const int group = a.q_heads / a.kv_heads;
+  if (tid == 0) s_seq = a.b.seqs;
+  plan(a, group, ROWS, before, part);
+  auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / ROWS + i; };
+  for (int i = tid; i < a.b.seqs; i += AT_T)
+    if (base(i) <= blockIdx.x && blockIdx.x < base(i + 1)) atomicMin(&s_seq, i);
+  __syncthreads();
+  const int s = s_seq;
+  if (s >= a.b.seqs) return;
+  const Seq q = seq_of(a, s, group, ROWS);
+  const int tile = (int)(blockIdx.x - base(s));
+  if (tile >= q.tiles) return;
+  const int rows = q.n * group - tile * ROWS < ROWS ? q.n * group - tile * ROWS : ROWS;
+  auto out_of = [&](int r) {
+    const int row = tile * ROWS + r, tok = row / group;
+    return static_cast<T*>(a.out) + (q.first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
+  };
+  if (q.chunks == 0) {
+    for (int i = tid; i < rows * D; i += AT_T) out_of(i / D)[i % D] = (T)0.0f;
+    return;
+  }
+  const uint64_t total = before[a.b.seqs], nb = total < nb32 ? total : nb32;
+  const uint64_t c0 = before[s] + ((uint64_t)head * q.tiles + tile) * q.chunks, c1 = c0 + q.chunks - 1;
+  const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
+  if (b0 == b1) return;
+  auto slot = [&](uint64_t b) { return parts + (b * 2 + (b == b0 ? 1 : 0)) * (uint64_t)(ROWS * (D + 2)); };
+  for (int i = tid; i < rows * (D / 4); i += AT_T) {
+    const int r = i / (D / 4), x = (i % (D / 4)) * 4;
+    float top = -INFINITY;
+    for (uint64_t b = b0; b <= b1; ++b) top = fmaxf(top, slot(b)[ROWS * D + r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint64_t b = b0; b <= b1; ++b) {
+      const float* p = slot(b);
+      const float mb = p[ROWS * D + r], e = __builtin_amdgcn_exp2f(mb - ref);
+      sum += mb == -INFINITY ? p[ROWS * D + ROWS + r] : p[ROWS * D + ROWS + r] * e;
+      v += *reinterpret_cast<const f4*>(p + r * D + x) * e;
+    }
+    T* out = out_of(r) + x;
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * by);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// 16-row tiles of an item: two where a sequence has more than 16 rows.
+static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group > 16 * (int64_t)seqs ? 2 : 1; }
+
+static int64_t split_blocks(int32_t) { return 2 * (int64_t)cu_count(); }
+
+uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads) {
+  if (seqs == 0 || tokens == 0) return 0;
+  const int rt = row_tiles(seqs, tokens, q_heads / kv_heads);
+  return (uint64_t)split_blocks(seqs) * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
+}
+
+template <int DT, int FMT, int D, int RT>
+static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
+  const int64_t nb = split_blocks(a.b.seqs);
+  float* parts = static_cast<float*>(a.ws);
+  hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;
+  hipLaunchKernelGGL((k_attend_join<DT, D, RT>), dim3((unsigned)tiles, (unsigned)a.kv_heads), dim3(AT_T), 0, s, a,
+                     parts, (uint32_t)nb);
+  return hipGetLastError();
+}
+
+template <int DT, int FMT, int D>
+static hipError_t attend_rows(const AttendArgs& a, hipStream_t s) {
+  return row_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads) == 1 ? attend_rt<DT, FMT, D, 1>(a, s)
+                                                                      : attend_rt<DT, FMT, D, 2>(a, s);
+}
 
 template <int DT, int FMT>
 static hipError_t attend_dim(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.b.tokens, (unsigned)a.q_heads);
-  if (a.dim == 64)
-    hipLaunchKernelGGL((k_attend_rows<DT, FMT, 64>), grid, dim3(AT_T), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_attend_rows<DT, FMT, 128>), grid, dim3(AT_T), 0, s, a);
-  return hipGetLastError();
+  return a.dim == 64 ? attend_rows<DT, FMT, 64>(a, s) : attend_rows<DT, FMT, 128>(a, s);
 }
 
 template <int DT>

@@ -14,6 +14,7 @@ namespace {
 constexpr int64_t kMaxTokens = 1ll << 24;
 constexpr int64_t kMaxNorm = 1ll << 20;
 constexpr int64_t kMaxIndex = 0x7FFFFFFFll;
+constexpr int64_t kMaxLength = 1ll << 30;  // kernels step past a length in 32 bits
 constexpr int32_t kMaxKvHeads = 256, kMaxGroup = 64;
 
 uintptr_t bytes_of(int32_t dtype) { return dtype == EFFORT_F32 ? 4 : 2; }
@@ -37,7 +38,7 @@ bool batch_ok(const effort_kv_batch* b, int32_t page_tokens) {
   if (!b || b->seqs < 0 || b->seqs > EFFORT_KV_MAX_SEQS || b->tokens < 0 || b->tokens > kMaxTokens)
     return false;
   if (b->seqs == 0 || b->tokens == 0) return true;
-  return b->max_pages >= 1 && (int64_t)b->max_pages * page_tokens <= kMaxIndex &&
+  return b->max_pages >= 1 && (int64_t)b->max_pages * page_tokens <= kMaxLength &&
          b->table_stride >= b->max_pages && b->page_table && b->kv_lens && b->q_starts &&
          aligned(b->page_table, 4) && aligned(b->kv_lens, 4) && aligned(b->q_starts, 4);
 }

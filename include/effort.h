@@ -395,7 +395,7 @@ typedef struct effort_kv_cache {
    that receives new tokens must stand in the table once. */
 typedef struct effort_kv_batch {
   int32_t seqs;              /* 0..EFFORT_KV_MAX_SEQS */
-  int32_t max_pages;         /* columns of the page table; max_pages * page_tokens < 2^31 */
+  int32_t max_pages;         /* columns of the page table; max_pages * page_tokens <= 2^30 */
   int64_t tokens;            /* rows of q, k, v, out; 0..2^24 */
   int64_t table_stride;      /* elements between the rows of the page table, >= max_pages */
   const int32_t* page_table; /* device [seqs][max_pages] */
