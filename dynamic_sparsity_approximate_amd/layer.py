@@ -20,51 +20,36 @@ def _dtype(t, name):
     return d
 
 
-class _On:
-    """Runs a call on the tensors' own device: `with _On(device, stream) as s`
-    makes that device and `stream` (None: the device's current stream) current,
-    so that what the call allocates belongs to that stream, and gives the
-    stream's handle."""
-
-    __slots__ = ("device", "stream", "_dev", "_ctx")
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("the tensors must be on a GPU")
-        self.device, self.stream, self._dev, self._ctx = device, stream, None, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self._dev = torch.cuda.device(self.device)
-            self._dev.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        s = self.stream
-        if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, device=self.device)
-        self._ctx = torch.cuda.stream(s)
-        self._ctx.__enter__()
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+def _run(device, stream, call):
+    """call(handle) on the tensors' own device with `stream` (None: that
+    device's current stream), both made current, so that what the call
+    allocates belongs to that stream.  The usual case, the current device and
+    its current stream, costs a microsecond of host time; the contexts cost ten."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _heads(t, name, tokens, dim, like):
     """(token stride, heads) of [tokens][heads][dim] rows of `like`'s type and device."""
-    if t.dim() != 3 or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (tokens is not None and shape[0] != tokens):
         raise ValueError("%s: shape %s, wanted [%s, heads, %d]" % (
-            name, tuple(t.shape), "tokens" if tokens is None else tokens, dim))
-    if t.dtype != like.dtype or t.device != like.device:
+            name, tuple(shape), "tokens" if tokens is None else tokens, dim))
+    if t is not like and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError("%s: %s on %s, wanted %s on %s" % (name, t.dtype, t.device, like.dtype, like.device))
-    s0, s1, s2 = t.stride()
-    h = t.shape[1]
-    if s2 != 1 or (h > 1 and s1 != dim):
-        raise ValueError("%s: a token's heads must be contiguous (strides %s)" % (name, (s0, s1, s2)))
-    return (s0 if t.shape[0] > 1 else h * dim), h
+    strides, h = t.stride(), shape[1]
+    if strides[2] != 1 or (h > 1 and strides[1] != dim):
+        raise ValueError("%s: a token's heads must be contiguous (strides %s)" % (name, strides))
+    return (strides[0] if shape[0] > 1 else h * dim), h
 
 
 class KVBatch:
@@ -88,14 +73,19 @@ class KVBatch:
         self.page_table, self.kv_lens, self.q_starts = page_table, kv_lens, q_starts
         self.device = page_table.device
         stride = page_table.stride(0) if seqs > 1 else page_table.shape[1]
-        self.desc = B.effort_kv_batch(seqs, page_table.shape[1], 0, stride, page_table.data_ptr(),
-                                      kv_lens.data_ptr(), q_starts.data_ptr())
+        self.seqs = seqs
+        self._args = (seqs, page_table.shape[1])
+        self._ptrs = (stride, page_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr())
+        self._descs = {}
 
-    def with_tokens(self, n: int):
-        """The C descriptor for a call with n rows."""
-        if self.desc.tokens != n:
-            self.desc.tokens = n
-        return self.desc
+    def desc(self, tokens: int):
+        """The C descriptor for a call with that many rows."""
+        d = self._descs.get(tokens)
+        if d is None:
+            if len(self._descs) >= 64:
+                self._descs.clear()
+            d = self._descs[tokens] = B.effort_kv_batch(*self._args, tokens, *self._ptrs)
+        return d
 
 
 class KVCache:
@@ -132,6 +122,7 @@ class KVCache:
         self.device = k.device
         self.desc = B.effort_kv_cache(format, self.kv_heads, self.head_dim, self.page_tokens, self.pages,
                                       k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+        self._ws_bytes = {}
 
     def _place(self, batch):
         if batch.device != self.device:
@@ -156,20 +147,21 @@ class KVCache:
                     not rope.is_contiguous() or rope.device != self.device:
                 raise ValueError("rope must be a contiguous float32 table [rows][rot_dim / 2][2] on %s" % self.device)
             rows, rot = rope.shape[0], 2 * rope.shape[1]
-        with _On(self.device, stream) as s:
-            qs = qh = os = 0
+        qs, qh = _heads(q, "q", tokens, self.head_dim, k) if q is not None else (0, 0)
+
+        def call(handle):
+            out, os = None, 0
             if q is not None:
-                qs, qh = _heads(q, "q", tokens, self.head_dim, k)
-                if q_out is None:
-                    q_out = torch.empty((tokens, qh, self.head_dim), dtype=q.dtype, device=q.device)
-                os, oh = _heads(q_out, "q_out", tokens, self.head_dim, k)
+                out = q_out if q_out is not None else torch.empty((tokens, qh, self.head_dim), dtype=q.dtype,
+                                                                  device=q.device)
+                os, oh = _heads(out, "q_out", tokens, self.head_dim, k)
                 if oh != qh:
                     raise ValueError("q_out must have q's heads")
-            else:
-                q_out = None
-            B.effort_kv_append(self.desc, batch.with_tokens(tokens), dt, rope, rows, rot, int(interleaved), q, qs,
-                               qh, q_out, os, k, ks, v, vs, s)
-        return q_out
+            B.effort_kv_append(self.desc, batch.desc(tokens), dt, rope, rows, rot, int(interleaved), q, qs, qh, out,
+                               os, k, ks, v, vs, handle)
+            return out
+
+        return _run(self.device, stream, call)
 
     def attend(self, batch: KVBatch, q, window: int = 0, scale=None, out=None, stream=None):
         """Causal attention of the new tokens' (rotated) queries over the cache,
@@ -184,18 +176,25 @@ class KVCache:
             raise ValueError("q is on %s, the cache on %s" % (q.device, self.device))
         if scale is None:
             scale = self.head_dim ** -0.5
-        with _On(self.device, stream) as s:
-            if out is None:
-                out = torch.empty((tokens, qh, self.head_dim), dtype=q.dtype, device=q.device)
-            os, oh = _heads(out, "out", tokens, self.head_dim, q)
+
+        def call(handle):
+            o = out if out is not None else torch.empty((tokens, qh, self.head_dim), dtype=q.dtype, device=q.device)
+            os, oh = _heads(o, "out", tokens, self.head_dim, q)
             if oh != qh:
                 raise ValueError("out must have q's heads")
-            n = B.effort_kv_workspace_bytes(self.desc, batch.desc.seqs, tokens, qh)
+            key = (batch.seqs, tokens, qh)
+            n = self._ws_bytes.get(key)
+            if n is None:
+                n = B.effort_kv_workspace_bytes(self.desc, *key)
+                if len(self._ws_bytes) >= 256:
+                    self._ws_bytes.clear()
+                self._ws_bytes[key] = n
             # of this call alone: calls on other streams and other captured graphs have their own
             ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-            B.effort_kv_attention(self.desc, batch.with_tokens(tokens), dt, q, qs, qh, scale, window, out, os, ws,
-                                  n, s)
-        return out
+            B.effort_kv_attention(self.desc, batch.desc(tokens), dt, q, qs, qh, scale, window, o, os, ws, n, handle)
+            return o
+
+        return _run(self.device, stream, call)
 
 
 def rope_table(base: float, rows: int, rot_dim: int, device="cuda", stream=None):
@@ -203,20 +202,24 @@ def rope_table(base: float, rows: int, rot_dim: int, device="cuda", stream=None)
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    with _On(device, stream) as s:
+
+    def call(handle):
         table = torch.empty((rows, rot_dim // 2, 2), dtype=torch.float32, device=device)
-        B.effort_rope_table(base, rows, rot_dim, table, s)
-    return table
+        B.effort_rope_table(base, rows, rot_dim, table, handle)
+        return table
+
+    return _run(device, stream, call)
 
 
 def _rows(t, name, shape, dtype, device):
     """Row stride of a tensor [rows][n] (or [n])."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError("%s: %s %s on %s, wanted %s %s on %s" % (
-            name, t.dtype, tuple(t.shape), t.device, dtype, shape, device))
-    if shape[-1] > 1 and t.stride(-1) != 1:
+            name, t.dtype, tuple(t.shape), t.device, dtype, tuple(shape), device))
+    strides, n = t.stride(), shape[-1]
+    if strides[-1] != 1 and n > 1:
         raise ValueError("%s: its rows must be contiguous" % name)
-    return t.stride(0) if len(shape) == 2 and shape[0] > 1 else shape[-1]
+    return strides[0] if len(strides) == 2 and shape[0] > 1 else n
 
 
 def norm_residual(x, resid=None, post_w=None, gate=None, scale: float = 1.0, pre_w=None, eps: float = 1e-5,
@@ -226,36 +229,38 @@ def norm_residual(x, resid=None, post_w=None, gate=None, scale: float = 1.0, pre
     x [rows][n] or [n]; resid alike, of x's type or float32; gate [n] or
     [rows][n].  Returns (r, out); `with_sum` / `with_norm` False leave out one
     of them (None is returned for it).  resid_out may be resid, out may be x."""
-    if x.dim() not in (1, 2):
+    shape, dev, xdt = x.shape, x.device, x.dtype
+    if len(shape) not in (1, 2):
         raise ValueError("x must be [rows][n] or [n]")
-    dt, dev, shape = _dtype(x, "x"), x.device, tuple(x.shape)
+    dt = _dtype(x, "x")
     rows, n = (shape[0] if len(shape) == 2 else 1), shape[-1]
-    xs = _rows(x, "x", shape, x.dtype, dev)
-    rdt = resid.dtype if resid is not None else resid_out.dtype if resid_out is not None else x.dtype
-    if rdt not in (x.dtype, torch.float32):
+    xs = _rows(x, "x", shape, xdt, dev)
+    rdt = resid.dtype if resid is not None else resid_out.dtype if resid_out is not None else xdt
+    if rdt is not xdt and rdt is not torch.float32:
         raise TypeError("resid must be of x's type or float32")
     rs = _rows(resid, "resid", shape, rdt, dev) if resid is not None else 0
-    for w, name in ((post_w, "post_w"), (pre_w, "pre_w")):
-        if w is not None:
-            _rows(w, name, (n,), x.dtype, dev)
+    if post_w is not None:
+        _rows(post_w, "post_w", (n,), xdt, dev)
+    if pre_w is not None:
+        _rows(pre_w, "pre_w", (n,), xdt, dev)
     gs = 0
     if gate is not None:
-        gs = _rows(gate, "gate", (n,) if gate.dim() == 1 else (rows, n), x.dtype, dev)
-        gs = 0 if gate.dim() == 1 else gs
-    with _On(dev, stream) as s:
+        if gate.dim() == 1:
+            _rows(gate, "gate", (n,), xdt, dev)
+        else:
+            gs = _rows(gate, "gate", (rows, n), xdt, dev)
+
+    def call(handle):
+        r = o = None
         ros = os = 0
         if with_sum:
-            if resid_out is None:
-                resid_out = torch.empty(shape, dtype=rdt, device=dev)
-            ros = _rows(resid_out, "resid_out", shape, rdt, dev)
-        else:
-            resid_out = None
+            r = resid_out if resid_out is not None else torch.empty(shape, dtype=rdt, device=dev)
+            ros = _rows(r, "resid_out", shape, rdt, dev)
         if with_norm:
-            if out is None:
-                out = torch.empty(shape, dtype=x.dtype, device=dev)
-            os = _rows(out, "out", shape, x.dtype, dev)
-        else:
-            out = None
-        B.effort_norm_residual(dt, rows, n, x, xs, _DTYPES[rdt], resid, rs, post_w, gate, gs, scale, pre_w, eps,
-                               resid_out, ros, out, os, s)
-    return resid_out, out
+            o = out if out is not None else torch.empty(shape, dtype=xdt, device=dev)
+            os = _rows(o, "out", shape, xdt, dev)
+        B.effort_norm_residual(dt, rows, n, x, xs, _DTYPES[rdt], resid, rs, post_w, gate, gs, scale, pre_w, eps, r,
+                               ros, o, os, handle)
+        return r, o
+
+    return _run(dev, stream, call)
