@@ -2,31 +2,156 @@
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
+#include "host.hpp"
 #include "layer.hpp"
 
 namespace effort {
 
-constexpr int NM_T = 256;
+constexpr int NM_T = 1024;  // threads of a row at most
 
-__device__ inline float block_sum(float x, float* red) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-  __syncthreads();
-  float t = 0.0f;
-#pragma unroll
-  for (int w = 0; w < NM_T / 64; ++w) t += red[w];
-  return t;
+template <int CTRL>
+__device__ inline float dpp_add(float x) {
+  const int y = __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true);
+  return x + __int_as_float(y);
 }
 
-// One block per row; the row is read once for each of its sums and once more
-// for the outputs (after the first time from the caches).
-template <int DT, int RT>
-__global__ __launch_bounds__(NM_T) void k_norm(NormArgs a) {
+// The sum over a wave, in every lane: rotations within 16 lanes, then two exchanges.
+__device__ inline float wave_sum(float x) {
+  x = dpp_add<0x128>(x);  // row_ror 8, 4, 2, 1
+  x = dpp_add<0x124>(x);
+  x = dpp_add<0x122>(x);
+  x = dpp_add<0x121>(x);
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The sum over the block; `red` is used once per kernel.
+__device__ inline float block_sum(float x, float* red) {
+  x = wave_sum(x);
+  const int waves = (int)blockDim.x >> 6;
+  if (waves == 1) return x;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  const int lane = (int)threadIdx.x & 63;
+  return wave_sum(lane < waves ? red[lane] : 0.0f);
+}
+
+// Elements of one 16-byte load of the narrower type.
+template <int DT>
+constexpr int norm_width() {
+  return DT == EFFORT_F32 ? 4 : 8;
+}
+
+template <int E, typename T>
+__device__ inline void load_part(const T* p, int64_t i, int64_t n, bool vec, float* x) {
+  if (vec) {
+    load_n<E>(p + i, true, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = i + k < n ? (float)p[i + k] : 0.0f;
+  }
+}
+
+template <int E, typename T>
+__device__ inline void store_part(T* p, int64_t i, int64_t n, bool vec, const float* x) {
+  if (vec) {
+    store_n<E>(p + i, true, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (i + k < n) p[i + k] = (T)x[k];
+  }
+}
+
+// One block per row, the row in registers: NC pieces of E elements a thread.
+// Everything that the outputs need is loaded before the first sum, so that a
+// single row costs one trip to memory and two exchanges over the block; for
+// many rows the kernel moves each byte once and is bound by that.
+template <int DT, int RT, int NC>
+__global__ __launch_bounds__(NM_T) void k_norm(NormArgs a, int32_t vec) {
   typedef typename ElemOf<DT>::T T;
   typedef typename ElemOf<RT>::T R;
-  __shared__ float red[NM_T / 64];
+  constexpr int E = norm_width<DT>();
+  __shared__ float red[2][NM_T / 64];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const R* resid = a.resid ? static_cast<const R*>(a.resid) + row * a.resid_stride : nullptr;
+  const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_stride : nullptr;
+  const T* post = static_cast<const T*>(a.post_w);
+  const T* pre = static_cast<const T*>(a.pre_w);
+  const float inv_n = 1.0f / (float)a.n;
+  float r[NC][E], old[NC][E], w[NC][E];
+  float s = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
+#pragma unroll
+    for (int k = 0; k < E; ++k) r[c][k] = old[c][k] = 0.0f, w[c][k] = a.scale;
+    if (i >= a.n) continue;
+    load_part<E>(x, i, a.n, vec != 0, r[c]);
+    if (resid) load_part<E>(resid, i, a.n, vec != 0, old[c]);
+    if (post) {
+      float p[E];
+      load_part<E>(post, i, a.n, vec != 0, p);
+#pragma unroll
+      for (int k = 0; k < E; ++k) w[c][k] *= p[k];
+    }
+    if (gate) {
+      float p[E];
+      load_part<E>(gate, i, a.n, vec != 0, p);
+#pragma unroll
+      for (int k = 0; k < E; ++k) w[c][k] *= p[k];
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) s = __builtin_fmaf(r[c][k], r[c][k], s);
+  }
+  const float rx = post ? 1.0f / sqrtf(block_sum(s, red[0]) * inv_n + a.eps) : 1.0f;
+  s = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      r[c][k] = __builtin_fmaf(r[c][k] * rx, w[c][k], old[c][k]);
+      s = __builtin_fmaf(r[c][k], r[c][k], s);
+    }
+  if (a.resid_out) {
+    R* to = static_cast<R*>(a.resid_out) + row * a.resid_out_stride;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
+      if (i < a.n) store_part<E>(to, i, a.n, vec != 0, r[c]);
+    }
+  }
+  if (!a.out) return;
+  float p[NC][E];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
+#pragma unroll
+    for (int k = 0; k < E; ++k) p[c][k] = 1.0f;
+    if (pre && i < a.n) load_part<E>(pre, i, a.n, vec != 0, p[c]);
+  }
+  const float rr = 1.0f / sqrtf(block_sum(s, red[1]) * inv_n + a.eps);
+  T* out = static_cast<T*>(a.out) + row * a.out_stride;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
+    if (i >= a.n) continue;
+#pragma unroll
+    for (int k = 0; k < E; ++k) r[c][k] = r[c][k] * rr * p[c][k];
+    store_part<E>(out, i, a.n, vec != 0, r[c]);
+  }
+}
+
+// Rows too long for the registers of a block: read once for each sum and once
+// more for the outputs.
+template <int DT, int RT>
+__global__ __launch_bounds__(NM_T) void k_norm_long(NormArgs a) {
+  typedef typename ElemOf<DT>::T T;
+  typedef typename ElemOf<RT>::T R;
+  __shared__ float red[2][NM_T / 64];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const R* resid = a.resid ? static_cast<const R*>(a.resid) + row * a.resid_stride : nullptr;
@@ -38,14 +163,13 @@ __global__ __launch_bounds__(NM_T) void k_norm(NormArgs a) {
   if (post) {
     float s = 0.0f;
     for (int64_t i = threadIdx.x; i < a.n; i += NM_T) s = __builtin_fmaf((float)x[i], (float)x[i], s);
-    rx = 1.0f / sqrtf(block_sum(s, red) * inv_n + a.eps);
+    rx = 1.0f / sqrtf(block_sum(s, red[0]) * inv_n + a.eps);
   }
   auto value = [&](int64_t i) {
-    float t = (float)x[i];
-    if (post) t = t * rx * (float)post[i];
-    if (gate) t *= (float)gate[i];
-    t *= a.scale;
-    return resid ? (float)resid[i] + t : t;
+    float w = a.scale;
+    if (post) w *= (float)post[i];
+    if (gate) w *= (float)gate[i];
+    return __builtin_fmaf((float)x[i] * rx, w, resid ? (float)resid[i] : 0.0f);
   };
   float rr = 1.0f;
   if (a.out) {
@@ -54,7 +178,7 @@ __global__ __launch_bounds__(NM_T) void k_norm(NormArgs a) {
       const float r = value(i);
       s = __builtin_fmaf(r, r, s);
     }
-    rr = 1.0f / sqrtf(block_sum(s, red) * inv_n + a.eps);
+    rr = 1.0f / sqrtf(block_sum(s, red[1]) * inv_n + a.eps);
   }
   R* resid_out = a.resid_out ? static_cast<R*>(a.resid_out) + row * a.resid_out_stride : nullptr;
   T* out = a.out ? static_cast<T*>(a.out) + row * a.out_stride : nullptr;
@@ -67,7 +191,33 @@ __global__ __launch_bounds__(NM_T) void k_norm(NormArgs a) {
 
 template <int DT, int RT>
 static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm<DT, RT>), dim3((unsigned)a.rows), dim3(NM_T), 0, s, a);
+  typedef typename ElemOf<DT>::T T;
+  typedef typename ElemOf<RT>::T R;
+  constexpr int E = norm_width<DT>(), NC_MAX = 32 / E;
+  const int64_t pieces = (a.n + E - 1) / E;
+  const dim3 grid((unsigned)a.rows);
+  if (pieces > (int64_t)NM_T * NC_MAX) {
+    hipLaunchKernelGGL((k_norm_long<DT, RT>), grid, dim3(NM_T), 0, s, a);
+    return hipGetLastError();
+  }
+  const bool vec = a.n % E == 0 && rows_aligned<E, T>(a.x, a.x_stride) &&
+                   (!a.resid || rows_aligned<E, R>(a.resid, a.resid_stride)) &&
+                   (!a.resid_out || rows_aligned<E, R>(a.resid_out, a.resid_out_stride)) &&
+                   (!a.out || rows_aligned<E, T>(a.out, a.out_stride)) &&
+                   (!a.gate || rows_aligned<E, T>(a.gate, a.gate_stride)) && rows_aligned<E, T>(a.post_w, 0) &&
+                   rows_aligned<E, T>(a.pre_w, 0);
+  // Few rows: as many threads as there are pieces, a row's time is its latency.
+  // Rows for every CU: 16 elements a thread, so that a row's exchanges weigh less.
+  int nc = a.rows >= 2 * (int64_t)cu_count() ? 16 / E : 1;
+  while (pieces > (int64_t)nc * NM_T) nc *= 2;
+  const int64_t threads = ((pieces + nc - 1) / nc + 63) / 64 * 64;
+  const dim3 block((unsigned)threads);
+  switch (nc) {
+    case 1: hipLaunchKernelGGL((k_norm<DT, RT, 1>), grid, block, 0, s, a, (int32_t)vec); break;
+    case 2: hipLaunchKernelGGL((k_norm<DT, RT, 2>), grid, block, 0, s, a, (int32_t)vec); break;
+    case 4: hipLaunchKernelGGL((k_norm<DT, RT, 4>), grid, block, 0, s, a, (int32_t)vec); break;
+    default: hipLaunchKernelGGL((k_norm<DT, RT, NC_MAX>), grid, block, 0, s, a, (int32_t)vec); break;
+  }
   return hipGetLastError();
 }
 
