@@ -124,10 +124,29 @@ __device__ inline uint32_t encode4(float y0, float y1, float y2, float y3) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, w, true);
 }
 
-// One block per (page of a sequence, head, keys or values), then blocks of
-// 256 chunks of the queries.  A page's block reads its new rows twice (the
-// second time from the caches): for the largest magnitude, then for the codes.
-template <int DT, int FMT>
+// The rotation of one chunk's queries, rounded once in fp32.
+__device__ inline void rotate_near(const float* x, const float2* cs, bool rotated, float* y) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    y[j] = rotated ? __builtin_fmaf(x[j], cs[j].x, -(x[4 + j] * cs[j].y)) : x[j];
+    y[4 + j] = rotated ? __builtin_fmaf(x[4 + j], cs[j].x, x[j] * cs[j].y) : x[4 + j];
+  }
+}
+
+__device__ inline void load_rope(const float2* row, const Chunk& k, float2* cs) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) cs[j] = k.rotated ? row[k.pair + j] : make_float2(1.0f, 0.0f);
+}
+
+constexpr int AP_QH = 4;  // query heads of a thread: they share its cosines and sines
+
+// One block per (page of a sequence, head, keys or values), then blocks of 256
+// (token, 4 heads, chunk) items of the queries.  A page's block keeps its new
+// elements in registers between the search for the largest magnitude and the
+// codes: IT chunks a thread, up to a whole page.  A prompt is bound by its
+// bytes (and read once), a single token by the chain starts -> page -> scale;
+// the new rows are therefore asked for before the page is known.
+template <int DT, int FMT, int IT>
 __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, int32_t per_token,
                                                  int32_t kv_vec, int32_t q_vec) {
   typedef typename ElemOf<DT>::T T;
@@ -140,7 +159,7 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
 
   if ((int64_t)blockIdx.x >= kv_blocks) {
     const int64_t i = ((int64_t)blockIdx.x - kv_blocks) * AP_T + tid;
-    const int64_t per = (int64_t)a.q_heads * cpr;
+    const int32_t per = (a.q_heads + AP_QH - 1) / AP_QH * cpr;
     const int64_t tok = i / per;
     if (tok >= a.b.tokens) return;
     int lo = 0, hi = a.b.seqs;  // the last sequence that starts at or before tok
@@ -152,29 +171,30 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
     if (tok < s0 || tok >= s1) return;
     const int64_t pos = (int64_t)a.b.lens[lo] - (s1 - s0) + (tok - s0);
     if (pos < 0 || pos >= (int64_t)a.b.max_pages * a.page_tokens) return;
-    const int r = (int)(i - tok * per), head = r / cpr;
-    const Chunk k = chunk_of(r - head * cpr, dim, a.rot, inter);
+    const int r = (int)(i - tok * per), head = r / cpr * AP_QH;
+    const Chunk k = chunk_of(r % cpr, dim, a.rot, inter);
+    float2 cs[4];
+    load_rope(rope + pos * half, k, cs);
     const T* row = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * dim;
     T* out = static_cast<T*>(a.q_out) + tok * a.q_out_stride + (int64_t)head * dim;
-    float x[8], y[8];
-    load_chunk(row, k, inter, q_vec != 0, x);
+    float x[AP_QH][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[j];
-    if (k.rotated) {
+    for (int h = 0; h < AP_QH; ++h)
+      if (head + h < a.q_heads) load_chunk(row + h * dim, k, inter, q_vec != 0, x[h]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 cs = rope[pos * half + k.pair + j];
-        y[j] = __builtin_fmaf(x[j], cs.x, -(x[4 + j] * cs.y));
-        y[4 + j] = __builtin_fmaf(x[4 + j], cs.x, x[j] * cs.y);
-      }
-      if (inter) {
+    for (int h = 0; h < AP_QH; ++h) {
+      if (head + h >= a.q_heads) break;
+      float y[8];
+      rotate_near(x[h], cs, k.rotated, y);
+      if (k.rotated && inter) {
         const float z[8] = {y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = z[j];
+        store_n<4>(out + h * dim + k.a, q_vec != 0, z);
+        store_n<4>(out + h * dim + k.b, q_vec != 0, z + 4);
+      } else {
+        store_n<4>(out + h * dim + k.a, q_vec != 0, y);
+        store_n<4>(out + h * dim + k.b, q_vec != 0, y + 4);
       }
     }
-    store_n<4>(out + k.a, q_vec != 0, y);
-    store_n<4>(out + k.b, q_vec != 0, y + 4);
     return;
   }
 
@@ -191,13 +211,18 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
     const int32_t t = start_of(a.b, i);
     return per_token ? t : t / pt + 2 * i;
   };
-  if (tid == 0) s_seq = a.b.seqs;
-  __syncthreads();
-  for (int i = tid; i < a.b.seqs; i += AP_T)
-    if (before(i) <= u && u < before(i + 1)) atomicMin(&s_seq, i);
-  __syncthreads();
-  const int seq = s_seq;
-  if (seq >= a.b.seqs) return;
+  int seq = 0;
+  if (a.b.seqs > 1) {
+    if (tid == 0) s_seq = a.b.seqs;
+    __syncthreads();
+    for (int i = tid; i < a.b.seqs; i += AP_T)
+      if (before(i) <= u && u < before(i + 1)) atomicMin(&s_seq, i);
+    __syncthreads();
+    seq = s_seq;
+    if (seq >= a.b.seqs) return;
+  } else if (u < before(0) || u >= before(1)) {
+    return;
+  }
   const int32_t t0 = start_of(a.b, seq);
   const int64_t n = (int64_t)start_of(a.b, seq + 1) - t0, len = a.b.lens[seq];
   const int64_t pos0 = len - n, from = pos0 > 0 ? pos0 : 0;
@@ -206,41 +231,41 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   const int64_t lo = pg * pt > from ? pg * pt : from, hi = (pg + 1) * pt < len ? (pg + 1) * pt : len;
   if (lo >= hi) return;
   const int32_t page = a.b.table[seq * a.b.table_stride + pg];
-  if (page < 0 || page >= a.b.pages) return;
   const int slot0 = (int)(lo - pg * pt), m = (int)(hi - lo);
   const int64_t tok0 = t0 + (lo - pos0);
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const T* rows = static_cast<const T*>(is_k ? a.k : a.v) + tok0 * stride + (int64_t)head * dim;
+  const int rot = is_k ? a.rot : 0, items = m * cpr;
+  const bool side = is_k && inter;
+
+  float y[IT][8];  // the new elements, first rotated (round_to_odd), then coded
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int i = tid + it * AP_T, r = i / cpr;
+    if (i < items) load_chunk(rows + r * stride, chunk_of(i - r * cpr, dim, rot, side), side, kv_vec != 0, y[it]);
+  }
+  if (page < 0 || page >= a.b.pages) return;
   uint8_t* codes = (is_k ? a.kc : a.vc) + ((int64_t)page * a.kv_heads + head) * pt * dim;
   float* scale = (is_k ? a.ks : a.vs) + (int64_t)page * a.kv_heads + head;
   const float old = *scale;
-  const int rot = is_k ? a.rot : 0;
-  const bool side = is_k && inter;
-
-  auto rotated = [&](int i, Chunk* k, double* y) {
-    const int r = i / cpr;
-    *k = chunk_of(i - r * cpr, dim, rot, side);
-    float x[8];
-    load_chunk(rows + r * stride, *k, side, kv_vec != 0, x);
-    float2 cs[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] = make_float2(1.0f, 0.0f);
-    if (k->rotated) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = rope[(lo + r) * half + k->pair + j];
-    }
-    rotate_exact(x, cs, k->rotated, y);
-    return r;
-  };
 
   uint32_t top = 0;  // as bits: a NaN is above an infinity, that above every number
-  for (int i = tid; i < m * cpr; i += AP_T) {
-    Chunk k;
-    double y[8];
-    rotated(i, &k, y);
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int i = tid + it * AP_T, r = i / cpr;
+    if (i >= items) continue;
+    const Chunk k = chunk_of(i - r * cpr, dim, rot, side);
+    if (k.rotated) {
+      float2 cs[4];
+      double z[8];
+      load_rope(rope + (lo + r) * half, k, cs);
+      rotate_exact(y[it], cs, true, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[it][j] = round_to_odd(z[j]);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(round_to_odd(y[j])) & 0x7FFFFFFFu;
+      const uint32_t b = __float_as_uint(y[it][j]) & 0x7FFFFFFFu;
       top = b > top ? b : top;
     }
   }
@@ -268,23 +293,37 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
     uint32_t* w = reinterpret_cast<uint32_t*>(codes);
     for (int i = tid; i < slot0 * dim / 4; i += AP_T) {
       const uint32_t c = w[i];
-      float y[4];
+      float z[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = round_to_odd((double)decode<FMT>(c >> (8 * j) & 0xFFu) * ratio);
-      w[i] = encode4<FMT>(y[0], y[1], y[2], y[3]);
+      for (int j = 0; j < 4; ++j) z[j] = round_to_odd((double)decode<FMT>(c >> (8 * j) & 0xFFu) * ratio);
+      w[i] = encode4<FMT>(z[0], z[1], z[2], z[3]);
     }
   }
-  const double per = 1.0 / (double)now;  // exact for a power of two
+  // A power of two divides exactly.  By another scale (a cache that this
+  // kernel did not begin) the elements are rotated again and divided in double.
   const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
-  for (int i = tid; i < m * cpr; i += AP_T) {
-    Chunk k;
-    double y[8];
-    const int r = rotated(i, &k, y);
+  const float per = (float)(1.0 / (double)now);
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int i = tid + it * AP_T, r = i / cpr;
+    if (i >= items) continue;
+    const Chunk k = chunk_of(i - r * cpr, dim, rot, side);
+    float* z = y[it];
+    if (pow2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] *= per;
+    } else if (!bad) {
+      float x[8];
+      float2 cs[4];
+      double d[8];
+      load_chunk(rows + r * stride, k, side, kv_vec != 0, x);
+      load_rope(rope + (lo + r) * half, k, cs);
+      rotate_exact(x, cs, k.rotated, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = round_to_odd(d[j] / (double)now);
+    }
     uint32_t c[2] = {0, 0};
     if (!bad) {
-      float z[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = round_to_odd(pow2 ? y[j] * per : y[j] / (double)now);
       if (k.rotated && side) {
         c[0] = encode4<FMT>(z[0], z[4], z[1], z[5]);
         c[1] = encode4<FMT>(z[2], z[6], z[3], z[7]);
@@ -299,25 +338,37 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   }
 }
 
-template <int DT>
-static hipError_t append_launch(const AppendArgs& a, hipStream_t s) {
+template <int DT, int FMT, int IT>
+static hipError_t append_it(const AppendArgs& a, hipStream_t s) {
   typedef typename ElemOf<DT>::T T;
   // units: pages that may receive tokens (fewer of the two bounds)
   const int64_t by_page = a.b.tokens / a.page_tokens + 2 * (int64_t)a.b.seqs;
   const int per_token = a.b.tokens <= by_page ? 1 : 0;
   const int64_t units = per_token ? a.b.tokens : by_page;
-  const int64_t q_blocks = ((int64_t)a.b.tokens * a.q_heads * (a.dim / 8) + AP_T - 1) / AP_T;
-  const int64_t blocks = units * a.kv_heads * 2 + q_blocks;
+  const int64_t q_items = (int64_t)a.b.tokens * ((a.q_heads + AP_QH - 1) / AP_QH) * (a.dim / 8);
+  const int64_t blocks = units * a.kv_heads * 2 + (q_items + AP_T - 1) / AP_T;
   if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
   const int kv_vec = rows_aligned<4, T>(a.k, a.k_stride) && rows_aligned<4, T>(a.v, a.v_stride);
   const int q_vec = a.q_heads && rows_aligned<4, T>(a.q, a.q_stride) && rows_aligned<4, T>(a.q_out, a.q_out_stride);
-  if (a.format == EFFORT_KV_I8)
-    hipLaunchKernelGGL((k_append<DT, EFFORT_KV_I8>), dim3((unsigned)blocks), dim3(AP_T), 0, s, a,
-                       (int32_t)units, per_token, kv_vec, q_vec);
-  else
-    hipLaunchKernelGGL((k_append<DT, EFFORT_KV_E4M3>), dim3((unsigned)blocks), dim3(AP_T), 0, s, a,
-                       (int32_t)units, per_token, kv_vec, q_vec);
+  hipLaunchKernelGGL((k_append<DT, FMT, IT>), dim3((unsigned)blocks), dim3(AP_T), 0, s, a, (int32_t)units,
+                     per_token, kv_vec, q_vec);
   return hipGetLastError();
+}
+
+// Chunks of a page per thread: a page's rows, or the call's if those are fewer.
+template <int DT, int FMT>
+static hipError_t append_fmt(const AppendArgs& a, hipStream_t s) {
+  const int64_t rows = a.b.tokens < a.page_tokens ? a.b.tokens : a.page_tokens;
+  const int64_t it = (rows * (a.dim / 8) + AP_T - 1) / AP_T;
+  if (it <= 1) return append_it<DT, FMT, 1>(a, s);
+  if (it <= 2) return append_it<DT, FMT, 2>(a, s);
+  if (it <= 4) return append_it<DT, FMT, 4>(a, s);
+  return append_it<DT, FMT, 8>(a, s);
+}
+
+template <int DT>
+static hipError_t append_launch(const AppendArgs& a, hipStream_t s) {
+  return a.format == EFFORT_KV_I8 ? append_fmt<DT, EFFORT_KV_I8>(a, s) : append_fmt<DT, EFFORT_KV_E4M3>(a, s);
 }
 
 hipError_t launch_append(const AppendArgs& a, int32_t dtype, hipStream_t s) {

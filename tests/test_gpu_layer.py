@@ -185,6 +185,22 @@ def test_append_ties_zeros_extremes():
         c.check_cache()
 
 
+def test_append_to_scales_of_another_program():
+    """Pages whose scales are no powers of two keep them while they suffice."""
+    for fmt in ("e4m3", "i8"):
+        for inter in (False, True):
+            c = Case(61, [20, 40, 33], [3, 5, 1], fmt=fmt)
+            c.np["ks"] = (0.03 + 0.05 * c.rng.random(c.np["ks"].shape)).astype(np.float32)
+            c.np["vs"] = (0.03 + 0.05 * c.rng.random(c.np["vs"].shape)).astype(np.float32)
+            c.cache.k_scale.copy_(torch.from_numpy(c.np["ks"]))
+            c.cache.v_scale.copy_(torch.from_numpy(c.np["vs"]))
+            k, v = c.rand(2), c.rand(2, 40.0)
+            rope = L.rope_rows(10000.0, c.table.shape[1] * c.page, 128)
+            c.cache.append(c.batch, k, v, rope=torch.from_numpy(rope).cuda(), interleaved=inter)
+            L.append(c.np, c.table, c.lens, c.starts, f64(k), f64(v), rope, inter, fmt)
+            c.check_cache()
+
+
 def test_append_rows_of_nobody_and_bad_pages():
     """Padded rows, a negative position, a length behind the table, page ids out
     of range: nothing of them is stored and their q rows stay."""
