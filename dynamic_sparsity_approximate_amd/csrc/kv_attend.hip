@@ -85,6 +85,24 @@ __device__ inline h8 rest8(const float* p, h8 w) {
   return r;
 }
 
+// The power of two that brings a row whose largest magnitude is `top` to [2^13, 2^14).
+__device__ inline float power_of_row(float top) {
+  int up = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
+  up = top > 0.0f && top < INFINITY ? (up > 100 ? 100 : up) : 0;
+  return __uint_as_float((uint32_t)(up + 127) << 23);
+}
+
+// The tokens after `low`, up to `high`, that a row at `pos` sees of `to` tokens.
+struct Sight {
+  int32_t low, high;
+};
+__device__ inline Sight sight_of(int64_t pos, int32_t to, int32_t window) {
+  Sight v;
+  v.high = pos < to ? (int32_t)(pos < -1 ? -1 : pos) : to - 1;
+  v.low = window && pos - window > -1 ? (int32_t)(pos - window < to ? pos - window : to) : -1;
+  return v;
+}
+
 // ---------------------------------------------------------------- who does what
 
 // A sequence's part of a call.
@@ -241,13 +259,13 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
     // the rows' queries, scaled by a power of two to at most 2^14
     h8 qh[RT][KS], ql[RT][KS];
     float f[RT];
-    int64_t p[RT];
+    Sight see[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       int r = rt * 16 + j;
       r = tile * ROWS + (r < rows ? r : rows - 1);  // rows behind the last one repeat it
       const int i = r / group;
-      p[rt] = q.pos + i;
+      see[rt] = sight_of(q.pos + i, q.hi, a.window);
       const T* src = static_cast<const T*>(a.q) + (q.first + i) * a.q_stride +
                      (int64_t)(head * group + r - i * group) * D + g * 16;
       float x[KS][8], top = 0.0f;
@@ -259,10 +277,7 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
           top = fmaxf(top, fabsf(x[k][e]));
         }
       }
-      top = max_of_row(top);
-      int up = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
-      up = top > 0.0f && top < INFINITY ? (up > 100 ? 100 : up) : 0;
-      const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+      const float by = power_of_row(max_of_row(top));
       f[rt] = a.scale * kLog2e / by;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -273,7 +288,8 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
       }
     }
     const int32_t row0 = tile * ROWS, row1 = row0 + rows - 1;
-    const int64_t p_min = q.pos + row0 / group, p_max = q.pos + row1 / group;
+    const Sight see0 = sight_of(q.pos + row0 / group, q.hi, a.window);  // of the first row and the last
+    const Sight see1 = sight_of(q.pos + row1 / group, q.hi, a.window);
 
     f4 o[RT][ND];
     float m[RT], l[RT];
@@ -297,8 +313,7 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
     for (int32_t t = t_begin; t < t_end; t += AT_CHUNK) {
       Codes<D> cur = nxt;
       if (t + AT_CHUNK < t_end) load_codes<D>(a, table, head, t + AT_CHUNK, q.hi, shift, &nxt);
-      const bool full = cur.ok[0] && cur.ok[1] && t + AT_TILE <= q.hi && t + AT_TILE - 1 <= p_min &&
-                        (a.window == 0 || t > p_max - a.window);
+      const bool full = cur.ok[0] && cur.ok[1] && t + AT_TILE - 1 <= see0.high && t > see1.low;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         // a poisoned page: its scores are NaN, its values count as any
@@ -312,8 +327,7 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (!cur.ok[u] || t + 16 * u + g * 4 + r >= q.hi ||
-                (a.window && t + 16 * u + g * 4 + r <= p_min - a.window)) {
+            if (!cur.ok[u] || t + 16 * u + g * 4 + r >= q.hi || t + 16 * u + g * 4 + r <= see0.low) {
 #pragma unroll
               for (int x = 0; x < D / 64; ++x) cur.v[u][r][x] = 0u;
             }
@@ -342,14 +356,15 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
         for (int u = 0; u < 2; ++u) {
           const float fu = f[rt] * cur.ks[u];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            w[rt][u * 4 + r] = sc[rt][u][r] * fu;
-            if (!full) {
-              const int64_t at = t + 16 * u + g * 4 + r;
-              const bool seen = cur.ok[u] && at < q.hi && at <= p[rt] && (a.window == 0 || at > p[rt] - a.window);
-              if (!seen) w[rt][u * 4 + r] = -INFINITY;
-            }
-          }
+          for (int r = 0; r < 4; ++r) w[rt][u * 4 + r] = sc[rt][u][r] * fu;
+        }
+        if (!full) {
+          const int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (!(cur.ok[u] && 16 * u + r <= high && 16 * u + r > low)) w[rt][u * 4 + r] = -INFINITY;
         }
         float top = w[rt][0];
 #pragma unroll
@@ -547,22 +562,454 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
   }
 }
 
+// ---------------------------------------------------------------- prompts
+
+constexpr int PR_ROWS = 32 * AT_W;  // rows of a block: 32 a wave
+constexpr int PR_TILE = 64;         // tokens of one step
+
+// 16-byte pieces of a step in LDS, as fp16, placed so that eight neighbouring
+// lanes' 16-byte accesses touch all 32 banks: keys [token][piece of 8 elements],
+// values [element][piece of 8 tokens, in the order in which the product of
+// weights and values counts them].
+template <int D>
+__device__ inline int key_piece(int token, int piece) {
+  return token * (D / 8) + (piece ^ (token & 7));
+}
+template <int D>
+__device__ inline int value_piece(int element, int piece) {
+  const int f = D == 128 ? (element >> 3) ^ ((element >> 2 & 1) << 2) : element >> 2;
+  return element * (PR_TILE / 8) + (piece ^ (f & 7));
+}
+
+// What a thread carries of a step from memory to LDS: D / 64 times 16 codes of a
+// key, and 4 elements of 8 tokens' values.
+template <int D>
+struct Staged {
+  uint4 k[D / 64];
+  uint32_t v[2][4];
+};
+
+// One block per (128 rows of a sequence, head, part of their tokens): its four
+// waves have 32 rows each and share every 64-token step's keys and values, which
+// are decoded once on their way into LDS (two buffers: the next step's codes
+// are in flight while this one is multiplied).  Decoding per wave instead
+// would cost as many vector instructions as the softmax.  Heads run fastest
+// over the grid: with 8 heads all blocks of a head share one XCD's L2.
+template <int DT, int FMT, int D>
+__global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* parts, int32_t splits) {
+  typedef typename ElemOf<DT>::T T;
+  constexpr bool SPLIT = DT == EFFORT_F32;
+  constexpr int KS = D / 32, ND = D / 16, RT = 2, SUB = PR_TILE / 16;
+  __shared__ h8 s_k[2][PR_TILE * D / 8];
+  __shared__ h8 s_v[2][PR_TILE * D / 8];
+  __shared__ int s_seq;
+  const int tid = (int)threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens), head = (int)blockIdx.x;
+  const int64_t bt = (int64_t)gridDim.y - 1 - blockIdx.y;  // the last rows see most: they go first
+  auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
+  if (tid == 0) s_seq = a.b.seqs;
+  __syncthreads();
+  for (int i = tid; i < a.b.seqs; i += AT_T)
+    if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
+  __syncthreads();
+  const int seq = __builtin_amdgcn_readfirstlane(s_seq);
+  if (seq >= a.b.seqs) return;
+  const int32_t first = start_of(a.b, seq), n = start_of(a.b, seq + 1) - first;
+  const int32_t row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
+  if (n <= 0 || row0 >= n * group) return;
+  const int rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+  const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens, pos = len - n;
+  const int64_t b_min = pos + row0 / group, b_max = pos + (row0 + rows - 1) / group;
+  // tokens that the block's rows see
+  const int64_t from = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
+  int64_t to = b_max + 1 < len ? b_max + 1 : len;
+  to = to < cap ? to : cap;
+  const int32_t lo = (int32_t)(from & ~(int64_t)(PR_TILE - 1)), hi = to > from ? (int32_t)to : lo;
+  const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
+  const int32_t z = (int32_t)blockIdx.z;
+  const int32_t step0 = (int32_t)((int64_t)steps * z / splits), step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
+  const int32_t* table = a.b.table + seq * a.b.table_stride;
+
+  // this wave's rows
+  const int my_rows = rows - wave * 32 < 32 ? rows - wave * 32 : 32;  // <= 0: none
+  h8 qh[RT][KS], ql[RT][KS];
+  float f[RT];
+  Sight see[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    int r = wave * 32 + rt * 16 + j;
+    r = row0 + (r < rows ? r : rows - 1);  // rows behind the last one repeat it
+    const int i = r / group;
+    see[rt] = sight_of(pos + i, hi, a.window);
+    const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
+    float x[KS][8], top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[k][e] = (float)src[(k * 4 + g) * 8 + e];
+        top = fmaxf(top, fabsf(x[k][e]));
+      }
+    const float by = power_of_row(max_of_row(top));
+    f[rt] = a.scale * kLog2e / by;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] *= by;
+      qh[rt][k] = weights8(x[k]);
+      if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
+    }
+  }
+  const int last = my_rows > 0 ? wave * 32 + my_rows - 1 : 0;
+  const Sight see0 = sight_of(pos + (row0 + (my_rows > 0 ? wave * 32 : 0)) / group, hi, a.window);
+  const Sight see1 = sight_of(pos + (row0 + last) / group, hi, a.window);
+
+  f4 o[RT][ND];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY;
+    l[rt] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  float unit = 1.0f, unit_top = 0.0f;
+
+  // page of sub-tile lane & 3 of the step at t; -1: none
+  auto page_at = [&](int32_t t) {
+    const int32_t tok = t + 16 * (lane & 3);
+    return tok < hi ? table[tok >> shift] : -1;
+  };
+  const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
+  const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
+  const bool v_mine = tid < 2 * D;
+  auto head_of = [&](int32_t pages, int sub) {  // (page, head) of a sub-tile; page 0 where there is none
+    const int32_t pg = __builtin_amdgcn_readlane(pages, sub);
+    return (int64_t)(pg >= 0 && pg < a.b.pages ? pg : 0) * a.kv_heads + head;
+  };
+  const int in_page = (1 << shift) - 1;
+  auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, float* ks, float* vs) {
+    const int32_t own = pages >= 0 && pages < a.b.pages ? pages : 0;
+    *ks = a.ks[(int64_t)own * a.kv_heads + head];
+    *vs = a.vs[(int64_t)own * a.kv_heads + head];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int tok = k_tok + i * (4096 / D);
+      const int sub = __builtin_amdgcn_readfirstlane(tok >> 4);
+      const int64_t at = (head_of(pages, sub) << shift) + ((t + tok) & in_page);
+      st->k[i] = *reinterpret_cast<const uint4*>(a.kc + at * D + k_piece * 16);
+    }
+    if (v_mine) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int sub = v_q * 2 + u;
+        const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16 + v_g * 4) & in_page);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(a.vc + (at + r) * D + v_el);
+      }
+    }
+  };
+  // `any`: some token of the step at t is not there or unseen by the block
+  auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, int buf) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int tok = k_tok + i * (4096 / D);
+      s_k[buf][key_piece<D>(tok, k_piece * 2)] = decode8<FMT>(st.k[i].x, st.k[i].y);
+      s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
+    }
+    if (!v_mine) return;
+    if (ok != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
+      // values of tokens that no row sees weigh 0, so they must not be NaN
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int32_t tok = t + (v_q * 2 + u) * 16 + v_g * 4 + r;
+          if (!(ok >> (v_q * 2 + u) & 1) || tok >= hi || tok < from) st.v[u][r] = 0u;
+        }
+    }
+    uint32_t e[4], e2[4];  // both tokens of a pair: bytes 0 and 1, bytes 2 and 3
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        e[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x05010400u);
+        e2[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x07030602u);
+      }
+    const int piece = v_q * 4 + v_g;
+    s_v[buf][value_piece<D>(v_el, piece)] =
+        join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]), decode2<FMT, false>(e[3]));
+    s_v[buf][value_piece<D>(v_el + 1, piece)] =
+        join8(decode2<FMT, true>(e[0]), decode2<FMT, true>(e[1]), decode2<FMT, true>(e[2]), decode2<FMT, true>(e[3]));
+    s_v[buf][value_piece<D>(v_el + 2, piece)] = join8(decode2<FMT, false>(e2[0]), decode2<FMT, false>(e2[1]),
+                                                      decode2<FMT, false>(e2[2]), decode2<FMT, false>(e2[3]));
+    s_v[buf][value_piece<D>(v_el + 3, piece)] =
+        join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]), decode2<FMT, true>(e2[3]));
+  };
+  auto there = [&](int32_t pages) {  // bit per sub-tile
+    return (uint32_t)(__ballot(pages >= 0 && pages < a.b.pages) & ((1u << SUB) - 1));
+  };
+
+  Staged<D> st;
+  float ks_l = 0.0f, vs_l = 0.0f;
+  int32_t pages = -1, pages_next = -1;
+  uint32_t ok = 0;
+  if (step0 < step1) {
+    const int32_t t = lo + step0 * PR_TILE;
+    pages = page_at(t);
+    pages_next = page_at(t + PR_TILE);
+    fetch(t, pages, &st, &ks_l, &vs_l);
+    ok = there(pages);
+    store(t, ok, st, 0);
+  }
+  __syncthreads();
+  int buf = 0;
+#pragma unroll 1
+  for (int32_t step = step0; step < step1; ++step, buf ^= 1) {
+    const int32_t t = lo + step * PR_TILE;
+    const float ks_now = ks_l, vs_now = vs_l;
+    const uint32_t ok_now = ok;
+    const bool more = step + 1 < step1;
+    if (more) {
+      pages = pages_next;
+      pages_next = page_at(t + 2 * PR_TILE);
+      fetch(t + PR_TILE, pages, &st, &ks_l, &vs_l);
+      ok = there(pages);
+    }
+    if (my_rows > 0 && t <= see1.high && t + PR_TILE - 1 > see0.low) {
+      float ks[SUB], vs[SUB];
+      float v_hi = 0.0f, v_lo = INFINITY;
+      bool same = true;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        ks[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_now), u));
+        vs[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_now), u));
+        // a poisoned page: its scores are NaN, its values count as any
+        if (!(fabsf(ks[u]) < INFINITY) || !(fabsf(vs[u]) < INFINITY)) {
+          ks[u] = __uint_as_float(0x7FC00000u);
+          vs[u] = unit;
+        }
+        if (ok_now >> u & 1) {
+          v_hi = fmaxf(v_hi, vs[u]);
+          v_lo = fminf(v_lo, vs[u]);
+        } else {
+          vs[u] = 0.0f;
+        }
+        same = same && vs[u] == unit;
+      }
+      const bool full = ok_now == (1u << SUB) - 1 && t + PR_TILE - 1 <= see0.high && t > see1.low;
+      f4 sc[RT][SUB];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const h8 kf = s_k[buf][key_piece<D>(u * 16 + j, k * 4 + g)];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[rt][k], sc[rt][u], 0, 0, 0);
+            if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[rt][k], sc[rt][u], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) sc[rt][u] *= f[rt] * ks[u];
+        if (!full) {
+          const int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (!((ok_now >> u & 1) && 16 * u + r <= high && 16 * u + r > low)) sc[rt][u][r] = -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
+        top = max_of_row(top);
+        if (__any(top > m[rt])) {
+          const float mn = fmaxf(top, m[rt]);
+          const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
+          m[rt] = mn;
+          l[rt] *= alpha;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
+        }
+        const float ref = (m[rt] == -INFINITY ? 0.0f : m[rt]) - kWeightExp;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc[rt][u][r] = __builtin_amdgcn_exp2f(sc[rt][u][r] - ref);
+            l[rt] += sc[rt][u][r];
+          }
+      }
+      // as in k_attend_split: weights in units of the values' scale, sub-tiles
+      // far apart one after the other
+      const bool apart = !same && v_hi > 0x1p10f * v_lo;
+#pragma unroll 1
+      for (int pass = 0; pass < (apart ? SUB : 1); ++pass) {
+        float rel[SUB];
+        if (!same) {
+          float top = 0.0f;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            rel[u] = apart && u != pass ? 0.0f : vs[u];
+            top = fmaxf(top, rel[u]);
+          }
+          unit_top = fmaxf(unit_top, top);
+          if (top > 2.0f * unit || top < 0x1p-10f * unit) {
+            const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f);
+            const float by = unit / now;
+            unit = now;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int d = 0; d < ND; ++d) o[rt][d] *= by;
+          }
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) rel[u] /= unit;
+        }
+        h8 ph[RT][2], pl[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = sc[rt][h * 2 + (i >> 2)][i & 3];
+            if (!same) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] *= rel[h * 2 + (i >> 2)];
+            }
+            ph[rt][h] = weights8(y);
+            if (SPLIT) pl[rt][h] = rest8(y, ph[rt][h]);
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const h8 vf = s_v[buf][value_piece<D>(j * ND + d, h * 4 + g)];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph[rt][h], o[rt][d], 0, 0, 0);
+              if (SPLIT) o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[rt][h], o[rt][d], 0, 0, 0);
+            }
+          }
+      }
+    }
+    if (more) store(t + PR_TILE, ok, st, buf ^ 1);
+    __syncthreads();
+  }
+
+  // rows of the result: element (g * 4 + r) * ND + d of row j
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float sum = sum_of_row(l[rt]);
+    const int r0 = wave * 32 + rt * 16 + j;
+    if (r0 >= rows) continue;
+    if (splits == 1) {
+      const int row = row0 + r0, tok = row / group;
+      T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
+      const float by = sum == 0.0f ? 0.0f : unit / sum;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) out[(g * 4 + r) * ND + d] = (T)(o[rt][d][r] * by);
+    } else {
+      float* mine = parts + (((int64_t)bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
+      if (g == 0) {
+        mine[PR_ROWS * D + r0] = m[rt];
+        mine[PR_ROWS * D + PR_ROWS + r0] = sum;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int x = 0; x < ND / 4; ++x)
+          *reinterpret_cast<f4*>(mine + r0 * D + (g * 4 + r) * ND + x * 4) =
+              f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]} * unit;
+    }
+  }
+}
+
+// Joins the parts of k_attend_prompt's rows: one block per (128 rows, head).
+template <int DT, int D>
+__global__ __launch_bounds__(AT_T) void k_attend_prompt_join(AttendArgs a, const float* parts, int32_t splits) {
+  typedef typename ElemOf<DT>::T T;
+  __shared__ int s_seq;
+  const int tid = (int)threadIdx.x, group = a.q_heads / a.kv_heads, head = (int)blockIdx.x;
+  const int64_t bt = blockIdx.y;
+  auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
+  if (tid == 0) s_seq = a.b.seqs;
+  __syncthreads();
+  for (int i = tid; i < a.b.seqs; i += AT_T)
+    if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
+  __syncthreads();
+  const int seq = s_seq;
+  if (seq >= a.b.seqs) return;
+  const int32_t first = start_of(a.b, seq), n = start_of(a.b, seq + 1) - first;
+  const int32_t row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
+  if (n <= 0 || row0 >= n * group) return;
+  const int rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+  const float* mine = parts + ((int64_t)bt * a.kv_heads + head) * splits * PR_ROWS * (D + 2);
+  for (int i = tid + (int)blockIdx.z * AT_T; i < rows * (D / 4); i += AT_T * (int)gridDim.z) {
+    const int r = i / (D / 4), x = (i % (D / 4)) * 4;
+    float top = -INFINITY, sum = 0.0f;
+    for (int z = 0; z < splits; ++z) top = fmaxf(top, mine[(int64_t)z * PR_ROWS * (D + 2) + PR_ROWS * D + r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int z = 0; z < splits; ++z) {
+      const float* p = mine + (int64_t)z * PR_ROWS * (D + 2);
+      const float mz = p[PR_ROWS * D + r], e = __builtin_amdgcn_exp2f(mz - ref);
+      sum += mz == -INFINITY ? p[PR_ROWS * D + PR_ROWS + r] : p[PR_ROWS * D + PR_ROWS + r] * e;
+      v += *reinterpret_cast<const f4*>(p + r * D + x) * e;
+    }
+    const int row = row0 + r, tok = row / group;
+    T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D + x;
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * by);
+  }
+}
+
 // ---------------------------------------------------------------- launches
 
-// 16-row tiles of an item: two where a sequence has more than 16 rows.
-static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group > 16 * (int64_t)seqs ? 2 : 1; }
+// Which kernel, by the rows (new tokens times group) of a sequence on average:
+// up to 16 or 32 they fit a wave's one or two row tiles and the call is bound
+// by reading the cache; beyond that blocks of 128 rows share what they read.
+static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) {
+  const int64_t rows = tokens * group;
+  return rows <= 16 * (int64_t)seqs ? 1 : rows <= 32 * (int64_t)seqs ? 2 : 0;
+}
 
-static int64_t split_blocks(int32_t) { return 2 * (int64_t)cu_count(); }
+static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
+
+// 128-row blocks of a head (a bound), and in how many parts their tokens are
+// taken so that two blocks fall to every CU.
+static int64_t prompt_tiles(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group / PR_ROWS + seqs; }
+static int32_t prompt_splits(int64_t tiles, int32_t kv_heads) {
+  const int64_t z = 2 * (int64_t)cu_count() / (tiles * kv_heads);
+  return (int32_t)(z < 1 ? 1 : z > 32 ? 32 : z);
+}
 
 uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads) {
   if (seqs == 0 || tokens == 0) return 0;
-  const int rt = row_tiles(seqs, tokens, q_heads / kv_heads);
-  return (uint64_t)split_blocks(seqs) * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
+  const int32_t group = q_heads / kv_heads;
+  const int rt = row_tiles(seqs, tokens, group);
+  if (rt) return (uint64_t)split_blocks() * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
+  const int64_t tiles = prompt_tiles(seqs, tokens, group);
+  const int32_t splits = prompt_splits(tiles, kv_heads);
+  return splits == 1 ? 0 : (uint64_t)tiles * kv_heads * splits * PR_ROWS * (dim + 2) * sizeof(float);
 }
 
 template <int DT, int FMT, int D, int RT>
 static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
-  const int64_t nb = split_blocks(a.b.seqs);
+  const int64_t nb = split_blocks();
   float* parts = static_cast<float*>(a.ws);
   hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
   hipError_t e = hipGetLastError();
@@ -574,9 +1021,26 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
 }
 
 template <int DT, int FMT, int D>
+static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
+  const int64_t tiles = prompt_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads);
+  const int32_t splits = prompt_splits(tiles, a.kv_heads);
+  float* parts = static_cast<float*>(a.ws);
+  hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, (unsigned)splits),
+                     dim3(AT_T), 0, s, a, parts, splits);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, 4), dim3(AT_T), 0, s,
+                     a, parts, splits);
+  return hipGetLastError();
+}
+
+template <int DT, int FMT, int D>
 static hipError_t attend_rows(const AttendArgs& a, hipStream_t s) {
-  return row_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads) == 1 ? attend_rt<DT, FMT, D, 1>(a, s)
-                                                                      : attend_rt<DT, FMT, D, 2>(a, s);
+  switch (row_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads)) {
+    case 1: return attend_rt<DT, FMT, D, 1>(a, s);
+    case 2: return attend_rt<DT, FMT, D, 2>(a, s);
+    default: return attend_prompt<DT, FMT, D>(a, s);
+  }
 }
 
 template <int DT, int FMT>
