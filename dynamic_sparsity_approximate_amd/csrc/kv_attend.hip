@@ -29,9 +29,11 @@ constexpr int AT_T = 256, AT_W = AT_T / 64;
 constexpr int AT_TILE = 32;              // tokens of one step of a wave
 constexpr int AT_CHUNK = AT_W * AT_TILE; // tokens of one step of a block
 constexpr float kLog2e = 1.4426950408889634f;
-// Weights are held times 2^13: a unit of values (below) may make them twice as
-// large, still inside fp16, and fp16's subnormals begin 2^-27 below the largest.
-constexpr float kWeightExp = 13.0f;
+// Weights are held times 2^6 relative to a row's reference score, which follows
+// the row's maximum only when that is 2^8 times larger (most steps then rescale
+// nothing), and the unit of values (below) may double them: at most 2^15, inside
+// fp16, whose normal numbers begin 2^-20 below the reference.
+constexpr float kWeightExp = 6.0f, kSlack = 8.0f;
 
 // ---------------------------------------------------------------- pieces of both products
 
@@ -48,6 +50,18 @@ __device__ inline float sum_of_row(float x) {
   r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+
+template <int CTRL>
+__device__ inline float dpp_max(float x) {
+  return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true)));
+}
+// Over four neighbouring lanes.
+__device__ inline float quad_max(float x) { return dpp_max<0x4E>(dpp_max<0xB1>(x)); }  // quad_perm 1032, 2301
+
+__device__ inline float lane_of(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
+}
+__device__ inline float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
 
 // Two codes (bytes 0, 1 or 2, 3 of w) as fp16, exactly.
 template <int FMT, bool HI>
@@ -566,6 +580,7 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
 
 constexpr int PR_ROWS = 32 * AT_W;  // rows of a block: 32 a wave
 constexpr int PR_TILE = 64;         // tokens of one step
+constexpr int PR_SUB = PR_TILE / 16;
 
 // 16-byte pieces of a step in LDS, as fp16, placed so that eight neighbouring
 // lanes' 16-byte accesses touch all 32 banks: keys [token][piece of 8 elements],
@@ -589,6 +604,9 @@ struct Staged {
   uint32_t v[2][4];
 };
 
+// NaN-propagating: a row that sees a NaN score has no maximum, and ends as NaN.
+__device__ inline float max_of(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 // One block per (128 rows of a sequence, head, part of their tokens): its four
 // waves have 32 rows each and share every 64-token step's keys and values, which
 // are decoded once on their way into LDS (two buffers: the next step's codes
@@ -596,10 +614,10 @@ struct Staged {
 // would cost as many vector instructions as the softmax.  Heads run fastest
 // over the grid: with 8 heads all blocks of a head share one XCD's L2.
 template <int DT, int FMT, int D>
-__global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* parts, int32_t splits) {
+__global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
-  constexpr int KS = D / 32, ND = D / 16, RT = 2, SUB = PR_TILE / 16;
+  constexpr int KS = D / 32, ND = D / 16, RT = 2, SUB = PR_SUB;
   __shared__ h8 s_k[2][PR_TILE * D / 8];
   __shared__ h8 s_v[2][PR_TILE * D / 8];
   __shared__ int s_seq;
@@ -622,24 +640,24 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
   const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens, pos = len - n;
   const int64_t b_min = pos + row0 / group, b_max = pos + (row0 + rows - 1) / group;
   // tokens that the block's rows see
-  const int64_t from = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
+  const int64_t from64 = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
   int64_t to = b_max + 1 < len ? b_max + 1 : len;
   to = to < cap ? to : cap;
-  const int32_t lo = (int32_t)(from & ~(int64_t)(PR_TILE - 1)), hi = to > from ? (int32_t)to : lo;
+  const int32_t from = from64 < to ? (int32_t)from64 : 0, hi = from64 < to ? (int32_t)to : 0;
+  const int32_t lo = from & ~(PR_TILE - 1);
   const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
   const int32_t z = (int32_t)blockIdx.z;
   const int32_t step0 = (int32_t)((int64_t)steps * z / splits), step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
   const int32_t* table = a.b.table + seq * a.b.table_stride;
 
-  // this wave's rows
-  const int my_rows = rows - wave * 32 < 32 ? rows - wave * 32 : 32;  // <= 0: none
+  // this wave's rows (those behind the last one repeat it)
   h8 qh[RT][KS], ql[RT][KS];
   float f[RT];
   Sight see[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     int r = wave * 32 + rt * 16 + j;
-    r = row0 + (r < rows ? r : rows - 1);  // rows behind the last one repeat it
+    r = row0 + (r < rows ? r : rows - 1);
     const int i = r / group;
     see[rt] = sight_of(pos + i, hi, a.window);
     const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
@@ -651,19 +669,22 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
         x[k][e] = (float)src[(k * 4 + g) * 8 + e];
         top = fmaxf(top, fabsf(x[k][e]));
       }
+    // the scale's sign goes into q: what is left of it keeps the scores' order
     const float by = power_of_row(max_of_row(top));
-    f[rt] = a.scale * kLog2e / by;
+    f[rt] = fabsf(a.scale) * kLog2e / by;
+    const float mul = a.scale < 0.0f ? -by : by;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] *= by;
+      for (int e = 0; e < 8; ++e) x[k][e] *= mul;
       qh[rt][k] = weights8(x[k]);
       if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
     }
   }
-  const int last = my_rows > 0 ? wave * 32 + my_rows - 1 : 0;
-  const Sight see0 = sight_of(pos + (row0 + (my_rows > 0 ? wave * 32 : 0)) / group, hi, a.window);
-  const Sight see1 = sight_of(pos + (row0 + last) / group, hi, a.window);
+  const int last = wave * 32 + 31 < rows ? wave * 32 + 31 : rows - 1;
+  const int front = wave * 32 < rows ? wave * 32 : rows - 1;
+  const int32_t all_high = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + front) / group, hi, a.window).high);
+  const int32_t all_low = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + last) / group, hi, a.window).low);
 
   f4 o[RT][ND];
   float m[RT], l[RT];
@@ -674,7 +695,23 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  float unit = 1.0f, unit_top = 0.0f;
+  // O counts in `unit`s of the values' scale: a token of scale vs weighs w * vs /
+  // unit, with the ratio inside the exponent.  The unit follows the scales up at
+  // once, down when they are 2^10 smaller (but never to where what is there
+  // could overflow).
+  float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
+  auto set_unit = [&](float top) {
+    unit_top = fmaxf(unit_top, top);
+    if (top > 2.0f * unit || (top < 0x1p-10f * unit && top > 0.0f)) {
+      const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f), by = unit / now;
+      unit = now;
+      per_unit = 1.0f / now;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[rt][d] *= by;
+    }
+  };
 
   // page of sub-tile lane & 3 of the step at t; -1: none
   auto page_at = [&](int32_t t) {
@@ -683,35 +720,34 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
   };
   const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
   const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
-  const bool v_mine = tid < 2 * D;
+  const bool v_mine = D == 128 || wave < 2;
+  const int in_page = (1 << shift) - 1;
   auto head_of = [&](int32_t pages, int sub) {  // (page, head) of a sub-tile; page 0 where there is none
     const int32_t pg = __builtin_amdgcn_readlane(pages, sub);
     return (int64_t)(pg >= 0 && pg < a.b.pages ? pg : 0) * a.kv_heads + head;
   };
-  const int in_page = (1 << shift) - 1;
-  auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, float* ks, float* vs) {
+  auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, uint32_t* ks, uint32_t* vs) {
     const int32_t own = pages >= 0 && pages < a.b.pages ? pages : 0;
-    *ks = a.ks[(int64_t)own * a.kv_heads + head];
-    *vs = a.vs[(int64_t)own * a.kv_heads + head];
+    *ks = __float_as_uint(a.ks[(int64_t)own * a.kv_heads + head]);
+    *vs = __float_as_uint(a.vs[(int64_t)own * a.kv_heads + head]);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const int tok = k_tok + i * (4096 / D);
-      const int sub = __builtin_amdgcn_readfirstlane(tok >> 4);
-      const int64_t at = (head_of(pages, sub) << shift) + ((t + tok) & in_page);
-      st->k[i] = *reinterpret_cast<const uint4*>(a.kc + at * D + k_piece * 16);
+      const int sub = D == 128 ? i * 2 + (wave >> 1) : wave;  // of token k_tok + i * 4096 / D
+      const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16) & in_page);
+      st->k[i] = *reinterpret_cast<const uint4*>(a.kc + at * D + ((k_tok & 15) * D + k_piece * 16));
     }
     if (v_mine) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int sub = v_q * 2 + u;
-        const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16 + v_g * 4) & in_page);
+        const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16) & in_page);
+        const uint8_t* from_row = a.vc + at * D + (v_g * 4 * D + v_el);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(a.vc + (at + r) * D + v_el);
+        for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(from_row + r * D);
       }
     }
   };
-  // `any`: some token of the step at t is not there or unseen by the block
-  auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, int buf) {
+  auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, uint32_t vs, int buf) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const int tok = k_tok + i * (4096 / D);
@@ -719,8 +755,10 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
       s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
     }
     if (!v_mine) return;
-    if (ok != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
-      // values of tokens that no row sees weigh 0, so they must not be NaN
+    ok &= (uint32_t)__ballot(vs != 0u);
+    if ((ok & ((1u << SUB) - 1)) != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
+      // values of tokens that no row sees weigh 0, so they must not be NaN;
+      // those of scale 0 are 0
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -752,158 +790,164 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
   };
 
   Staged<D> st;
-  float ks_l = 0.0f, vs_l = 0.0f;
-  int32_t pages = -1, pages_next = -1;
-  uint32_t ok = 0;
+  uint32_t ks_l = 0, vs_l = 0, ok = 0;
+  int32_t pages_next = -1;
   if (step0 < step1) {
     const int32_t t = lo + step0 * PR_TILE;
-    pages = page_at(t);
+    const int32_t pages = page_at(t);
     pages_next = page_at(t + PR_TILE);
     fetch(t, pages, &st, &ks_l, &vs_l);
     ok = there(pages);
-    store(t, ok, st, 0);
+    store(t, ok, st, vs_l, 0);
   }
   __syncthreads();
+  // the lane's first piece of a key by the product's parity, and of a value's
+  // tokens by its half; the others lie at constant distances
+  const int k_at[2] = {key_piece<D>(j, g), key_piece<D>(j, 4 + g)};
+  const int v_at[2] = {value_piece<D>(j * ND, g), value_piece<D>(j * ND, 4 + g)};
   int buf = 0;
 #pragma unroll 1
   for (int32_t step = step0; step < step1; ++step, buf ^= 1) {
     const int32_t t = lo + step * PR_TILE;
-    const float ks_now = ks_l, vs_now = vs_l;
-    const uint32_t ok_now = ok;
-    const bool more = step + 1 < step1;
-    if (more) {
-      pages = pages_next;
+    // the step's scales, those of sub-tile lane & 3 in each lane
+    const uint32_t there_now = ok;
+    // a poisoned page: its scores are NaN, its values count as any
+    const bool bad = ks_l >= 0x7F800000u || vs_l >= 0x7F800000u;
+    const float ks_lane = __uint_as_float(bad ? 0x7FC00000u : ks_l);
+    // 0 where a sub-tile has no say in the unit (values of scale 0 are 0 in LDS)
+    const float vs_lane = (there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
+    const float v_hi = uniform(quad_max(vs_lane)), v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
+    if (step + 1 < step1) {
+      const int32_t pages = pages_next;
       pages_next = page_at(t + 2 * PR_TILE);
       fetch(t + PR_TILE, pages, &st, &ks_l, &vs_l);
       ok = there(pages);
     }
-    if (my_rows > 0 && t <= see1.high && t + PR_TILE - 1 > see0.low) {
-      float ks[SUB], vs[SUB];
-      float v_hi = 0.0f, v_lo = INFINITY;
-      bool same = true;
+    // Sub-tiles whose values' scales are far apart are taken one after the
+    // other: the weights of the smaller would lose bits below the larger.
+    const int passes = v_hi > 0x1p10f * v_lo ? SUB : 1;
+#pragma unroll 1
+    for (int pass = 0; pass < passes; ++pass) {
+    const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
+    // The fences keep the compiler from loading all pieces at once, for which
+    // there are no registers: those of one sub-tile are loaded while the one
+    // before is multiplied.
+    f4 sc[RT][SUB];
+    h8 kf[2][KS];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        ks[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_now), u));
-        vs[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_now), u));
-        // a poisoned page: its scores are NaN, its values count as any
-        if (!(fabsf(ks[u]) < INFINITY) || !(fabsf(vs[u]) < INFINITY)) {
-          ks[u] = __uint_as_float(0x7FC00000u);
-          vs[u] = unit;
-        }
-        if (ok_now >> u & 1) {
-          v_hi = fmaxf(v_hi, vs[u]);
-          v_lo = fminf(v_lo, vs[u]);
-        } else {
-          vs[u] = 0.0f;
-        }
-        same = same && vs[u] == unit;
+    for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k & 1] + (k >> 1) * 8];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      if (u + 1 < SUB) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          kf[(u + 1) & 1][k] = s_k[buf][k_at[k & 1] + (u + 1) * 16 * (D / 8) + (k >> 1) * 8];
       }
-      const bool full = ok_now == (1u << SUB) - 1 && t + PR_TILE - 1 <= see0.high && t > see1.low;
-      f4 sc[RT][SUB];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
+      for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < KS; ++k) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const h8 kf = s_k[buf][key_piece<D>(u * 16 + j, k * 4 + g)];
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[rt][k], sc[rt][u], 0, 0, 0);
-            if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[rt][k], sc[rt][u], 0, 0, 0);
-          }
+        for (int rt = 0; rt < RT; ++rt) {
+          sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], qh[rt][k], sc[rt][u], 0, 0, 0);
+          if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], ql[rt][k], sc[rt][u], 0, 0, 0);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // scores are sc * c
+    float c[RT][SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        c[rt][u] = f[rt] * lane_of(ks_lane, u);
+    if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
+        int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+        // not to be compared outside this branch: most steps hide nothing
+        asm volatile("" : "+v"(high), "+v"(low));
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) sc[rt][u] *= f[rt] * ks[u];
-        if (!full) {
-          const int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+        for (int u = 0; u < SUB; ++u) {
+          sc[rt][u] *= c[rt][u];
+          c[rt][u] = 1.0f;
+          const int32_t high_u = here >> u & 1 ? high : -PR_TILE;
 #pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (!((ok_now >> u & 1) && 16 * u + r <= high && 16 * u + r > low)) sc[rt][u][r] = -INFINITY;
+          for (int r = 0; r < 4; ++r)
+            if (16 * u + r > high_u || 16 * u + r <= low) sc[rt][u][r] = -INFINITY;
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][u][r]);
-        top = max_of_row(top);
-        if (__any(top > m[rt])) {
-          const float mn = fmaxf(top, m[rt]);
-          const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-          m[rt] = mn;
-          l[rt] *= alpha;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
-        }
-        const float ref = (m[rt] == -INFINITY ? 0.0f : m[rt]) - kWeightExp;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sc[rt][u][r] = __builtin_amdgcn_exp2f(sc[rt][u][r] - ref);
-            l[rt] += sc[rt][u][r];
-          }
-      }
-      // as in k_attend_split: weights in units of the values' scale, sub-tiles
-      // far apart one after the other
-      const bool apart = !same && v_hi > 0x1p10f * v_lo;
-#pragma unroll 1
-      for (int pass = 0; pass < (apart ? SUB : 1); ++pass) {
-        float rel[SUB];
-        if (!same) {
-          float top = 0.0f;
-#pragma unroll
-          for (int u = 0; u < SUB; ++u) {
-            rel[u] = apart && u != pass ? 0.0f : vs[u];
-            top = fmaxf(top, rel[u]);
-          }
-          unit_top = fmaxf(unit_top, top);
-          if (top > 2.0f * unit || top < 0x1p-10f * unit) {
-            const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f);
-            const float by = unit / now;
-            unit = now;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int d = 0; d < ND; ++d) o[rt][d] *= by;
-          }
-#pragma unroll
-          for (int u = 0; u < SUB; ++u) rel[u] /= unit;
-        }
-        h8 ph[RT][2], pl[RT][2];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = sc[rt][h * 2 + (i >> 2)][i & 3];
-            if (!same) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] *= rel[h * 2 + (i >> 2)];
-            }
-            ph[rt][h] = weights8(y);
-            if (SPLIT) pl[rt][h] = rest8(y, ph[rt][h]);
-          }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const h8 vf = s_v[buf][value_piece<D>(j * ND + d, h * 4 + g)];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph[rt][h], o[rt][d], 0, 0, 0);
-              if (SPLIT) o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[rt][h], o[rt][d], 0, 0, 0);
-            }
-          }
       }
     }
-    if (more) store(t + PR_TILE, ok, st, buf ^ 1);
+    float ref[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+        top = max_of(top, max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]) * c[rt][u]);
+      top = max_of_row(top);
+      if (__any(top > m[rt] + kSlack)) {
+        const float mn = fmaxf(top, m[rt]);
+        const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
+        m[rt] = mn;
+        l[rt] *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
+      }
+      // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+      ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
+    }
+    if (pass == 0) store(t + PR_TILE, ok, st, vs_l, buf ^ 1);  // behind the last step: never read
+    const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
+    set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
+    const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
+    const float up_lane = __builtin_amdgcn_logf(rel), back_lane = __builtin_amdgcn_rcpf(rel);
+    h8 ph[RT][2], pl[RT][2];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const float up = lane_of(up_lane, u), back = lane_of(back_lane, u);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float w[4];
+        const float base = ref[rt] + up;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
+        l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int e = (u & 1) * 4 + r;
+          ph[rt][u >> 1][e] = (_Float16)w[r];
+          if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+      h8 vf[2][4];
+      auto load_values = [&](int i, h8* to) {  // products 4 i .. 4 i + 3 of both halves' 2 ND
+        const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          to[d] = s_v[buf][v_at[D == 128 ? h ^ (d0 >> 2) : h] + (d0 + d) * (PR_TILE / 8)];
+      };
+      load_values(0, vf[0]);
+#pragma unroll
+      for (int i = 0; i < ND / 2; ++i) {
+        if (i + 1 < ND / 2) load_values(i + 1, vf[(i + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            f4& acc = o[rt][d0 + d];
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], ph[rt][h], acc, 0, 0, 0);
+            if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], pl[rt][h], acc, 0, 0, 0);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     __syncthreads();
   }
 
@@ -920,7 +964,10 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_prompt(AttendArgs a, float* 
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) out[(g * 4 + r) * ND + d] = (T)(o[rt][d][r] * by);
+        for (int x = 0; x < ND; x += 4) {
+          const float y[4] = {o[rt][x][r] * by, o[rt][x + 1][r] * by, o[rt][x + 2][r] * by, o[rt][x + 3][r] * by};
+          store_n<4>(out + (g * 4 + r) * ND + x, out_vec != 0, y);
+        }
     } else {
       float* mine = parts + (((int64_t)bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
       if (g == 0) {
@@ -1025,8 +1072,9 @@ static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
   const int64_t tiles = prompt_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads);
   const int32_t splits = prompt_splits(tiles, a.kv_heads);
   float* parts = static_cast<float*>(a.ws);
+  const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
   hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, (unsigned)splits),
-                     dim3(AT_T), 0, s, a, parts, splits);
+                     dim3(AT_T), 0, s, a, parts, splits, out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, 4), dim3(AT_T), 0, s,
