@@ -37,11 +37,14 @@ constexpr float kWeightExp = 6.0f, kSlack = 8.0f;
 
 // ---------------------------------------------------------------- pieces of both products
 
+// NaN-propagating (and one instruction, for three operands too).
+__device__ inline float max_of(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 __device__ inline float max_of_row(float x) {  // over the four lanes that share a row
   auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  x = max_of(__uint_as_float(r[0]), __uint_as_float(r[1]));
   r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return max_of(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 __device__ inline float sum_of_row(float x) {
@@ -53,7 +56,7 @@ __device__ inline float sum_of_row(float x) {
 
 template <int CTRL>
 __device__ inline float dpp_max(float x) {
-  return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true)));
+  return max_of(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true)));
 }
 // Over four neighbouring lanes.
 __device__ inline float quad_max(float x) { return dpp_max<0x4E>(dpp_max<0xB1>(x)); }  // quad_perm 1032, 2301
@@ -604,9 +607,6 @@ struct Staged {
   uint32_t v[2][4];
 };
 
-// NaN-propagating: a row that sees a NaN score has no maximum, and ends as NaN.
-__device__ inline float max_of(float x, float y) { return __builtin_elementwise_maximum(x, y); }
-
 // One block per (128 rows of a sequence, head, part of their tokens): its four
 // waves have 32 rows each and share every 64-token step's keys and values, which
 // are decoded once on their way into LDS (two buffers: the next step's codes
@@ -748,8 +748,11 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     }
   };
   auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, uint32_t vs, int buf) {
+    // nothing of this may move up to where the codes are still on their way
+    asm volatile("" : "+v"(vs));
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
+      asm volatile("" : "+v"(st.k[i].x), "+v"(st.k[i].y), "+v"(st.k[i].z), "+v"(st.k[i].w));
       const int tok = k_tok + i * (4096 / D);
       s_k[buf][key_piece<D>(tok, k_piece * 2)] = decode8<FMT>(st.k[i].x, st.k[i].y);
       s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
@@ -759,11 +762,13 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     if ((ok & ((1u << SUB) - 1)) != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
       // values of tokens that no row sees weigh 0, so they must not be NaN;
       // those of scale 0 are 0
+      int32_t tok0 = t + v_q * 32 + v_g * 4;
+      asm volatile("" : "+v"(tok0));
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int32_t tok = t + (v_q * 2 + u) * 16 + v_g * 4 + r;
+          const int32_t tok = tok0 + u * 16 + r;
           if (!(ok >> (v_q * 2 + u) & 1) || tok >= hi || tok < from) st.v[u][r] = 0u;
         }
     }
