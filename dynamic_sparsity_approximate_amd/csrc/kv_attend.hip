@@ -522,61 +522,121 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
   }
 }
 
+// Joins `count` parts of a row by 256 / R threads: a group of 32 has D / 32
+// elements each of every (8 / R)-th part, four parts in flight, with the
+// maximum and sum of what it has seen; then the groups are joined the same way.
+// `at(i)` is part i: the values of `rows` rows, their maxima, their sums.
+template <int D, int R, typename T, typename At>
+__device__ void join_row(int count, int rows, int r, At at, T* out) {
+  constexpr int E = D / 32, GROUPS = 8 / R, FLY = 4;
+  __shared__ float s_m[8], s_l[8];
+  __shared__ float s_v[8][D];
+  const int tid = (int)threadIdx.x, lane = tid & 31, slot = tid >> 5, k = slot % GROUPS;
+  float m = -INFINITY, l = 0.0f, v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  for (int i0 = k; i0 < count; i0 += GROUPS * FLY) {
+    float mi[FLY], li[FLY];
+    Vec<E, float> y[FLY];
+#pragma unroll
+    for (int j = 0; j < FLY; ++j) {
+      const int i = i0 + j * GROUPS;
+      const float* p = at(i < count ? i : i0);
+      mi[j] = i < count ? p[rows * D + r] : -INFINITY;
+      li[j] = i < count ? p[rows * D + rows + r] : 0.0f;
+      y[j] = *reinterpret_cast<const Vec<E, float>*>(p + r * D + lane * E);
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < FLY; ++j) top = fmaxf(top, mi[j]);
+    const float ref = top == -INFINITY ? 0.0f : top, was = __builtin_amdgcn_exp2f(m - ref);
+    // a part that saw only NaN has no maximum: its sum stays NaN
+    l = m == -INFINITY ? l : l * was;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= was;
+    m = top;
+#pragma unroll
+    for (int j = 0; j < FLY; ++j) {
+      const float by = __builtin_amdgcn_exp2f(mi[j] - ref);
+      l += mi[j] == -INFINITY ? li[j] : li[j] * by;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = by > 0.0f ? __builtin_fmaf(y[j].e[e], by, v[e]) : v[e];
+    }
+  }
+  if (GROUPS > 1) {
+    if (lane == 0) {
+      s_m[slot] = m;
+      s_l[slot] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_v[slot][lane * E + e] = v[e];
+    __syncthreads();
+    if (k != 0) return;
+    float top = m;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) top = fmaxf(top, s_m[slot + g]);
+    const float ref = top == -INFINITY ? 0.0f : top, was = __builtin_amdgcn_exp2f(m - ref);
+    l = m == -INFINITY ? l : l * was;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= was;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) {
+      const float mg = s_m[slot + g], by = __builtin_amdgcn_exp2f(mg - ref);
+      l += mg == -INFINITY ? s_l[slot + g] : s_l[slot + g] * by;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = __builtin_fmaf(s_v[slot + g][lane * E + e], by, v[e]);
+    }
+  }
+  const float by = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[lane * E + e] = (T)(v[e] * by);
+}
+
 // Joins the parts that blocks left of an item, and writes the rows that see
-// nothing.  One block per (row tile, head); tiles of a sequence are counted
+// nothing.  One block per (R rows, head); row tiles of a sequence are counted
 // from first * group / ROWS + s, enough for every sequence before it.
-template <int DT, int D, int RT>
+template <int DT, int D, int RT, int R>
 __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32) {
   typedef typename ElemOf<DT>::T T;
   constexpr int ROWS = 16 * RT;
   __shared__ uint64_t before[EFFORT_KV_MAX_SEQS + 1];
   __shared__ uint64_t part[AT_W];
   __shared__ int s_seq;
-  const int tid = (int)threadIdx.x, head = (int)blockIdx.y;
-  const int group = a.q_heads / a.kv_heads;
-  if (tid == 0) s_seq = a.b.seqs;
-  plan(a, group, ROWS, before, part);
+  const int tid = (int)threadIdx.x, head = (int)blockIdx.y, group = a.q_heads / a.kv_heads;
+  const uint32_t bt = blockIdx.x / (ROWS / R);
+  const int r0 = (int)(blockIdx.x % (ROWS / R)) * R;
   auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / ROWS + i; };
-  for (int i = tid; i < a.b.seqs; i += AT_T)
-    if (base(i) <= blockIdx.x && blockIdx.x < base(i + 1)) atomicMin(&s_seq, i);
-  __syncthreads();
-  const int s = s_seq;
-  if (s >= a.b.seqs) return;
+  int s = 0;
+  if (a.b.seqs > 1) {
+    if (tid == 0) s_seq = a.b.seqs;
+    __syncthreads();
+    for (int i = tid; i < a.b.seqs; i += AT_T)
+      if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
+    __syncthreads();
+    s = s_seq;
+    if (s >= a.b.seqs) return;
+  }
   const Seq q = seq_of(a, s, group, ROWS);
-  const int tile = (int)(blockIdx.x - base(s));
-  if (tile >= q.tiles) return;
-  const int rows = q.n * group - tile * ROWS < ROWS ? q.n * group - tile * ROWS : ROWS;
-  auto out_of = [&](int r) {
-    const int row = tile * ROWS + r, tok = row / group;
-    return static_cast<T*>(a.out) + (q.first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
-  };
+  const int tile = (int)(bt - base(s));
+  if (tile * ROWS + r0 >= q.n * group) return;
+  const int r = r0 + (tid >> 5) / (8 / R);
+  const bool mine = tile * ROWS + r < q.n * group;
+  const int row = mine ? tile * ROWS + r : tile * ROWS + r0, tok = row / group;
+  T* out = static_cast<T*>(a.out) + (q.first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
   if (q.chunks == 0) {
-    for (int i = tid; i < rows * D; i += AT_T) out_of(i / D)[i % D] = (T)0.0f;
+    for (int i = tid & 31; i < D; i += 32) out[i] = (T)0.0f;
     return;
   }
+  plan(a, group, ROWS, before, part);
   const uint64_t total = before[a.b.seqs], nb = total < nb32 ? total : nb32;
   const uint64_t c0 = before[s] + ((uint64_t)head * q.tiles + tile) * q.chunks, c1 = c0 + q.chunks - 1;
   const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
   if (b0 == b1) return;
-  auto slot = [&](uint64_t b) { return parts + (b * 2 + (b == b0 ? 1 : 0)) * (uint64_t)(ROWS * (D + 2)); };
-  for (int i = tid; i < rows * (D / 4); i += AT_T) {
-    const int r = i / (D / 4), x = (i % (D / 4)) * 4;
-    float top = -INFINITY;
-    for (uint64_t b = b0; b <= b1; ++b) top = fmaxf(top, slot(b)[ROWS * D + r]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint64_t b = b0; b <= b1; ++b) {
-      const float* p = slot(b);
-      const float mb = p[ROWS * D + r], e = __builtin_amdgcn_exp2f(mb - ref);
-      sum += mb == -INFINITY ? p[ROWS * D + ROWS + r] : p[ROWS * D + ROWS + r] * e;
-      v += *reinterpret_cast<const f4*>(p + r * D + x) * e;
-    }
-    T* out = out_of(r) + x;
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * by);
-  }
+  const float* first = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
+  const float* rest = parts + (b0 + 1) * 2 * (uint64_t)(ROWS * (D + 2));
+  auto at = [&](int i) { return i == 0 ? first : rest + (uint64_t)(i - 1) * 2 * (ROWS * (D + 2)); };
+  // a row behind the last one repeats the block's first
+  join_row<D, R>((int)(b1 - b0) + 1, ROWS, mine ? r : r0, at, out);
 }
 
 // ---------------------------------------------------------------- prompts
@@ -989,13 +1049,14 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
   }
 }
 
-// Joins the parts of k_attend_prompt's rows: one block per (128 rows, head).
+// Joins the parts of k_attend_prompt's rows: one block per (8 rows, head).
 template <int DT, int D>
 __global__ __launch_bounds__(AT_T) void k_attend_prompt_join(AttendArgs a, const float* parts, int32_t splits) {
   typedef typename ElemOf<DT>::T T;
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, group = a.q_heads / a.kv_heads, head = (int)blockIdx.x;
-  const int64_t bt = blockIdx.y;
+  const int64_t bt = blockIdx.y / (PR_ROWS / 8);
+  const int r = (int)(blockIdx.y % (PR_ROWS / 8)) * 8 + (tid >> 5);
   auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
   if (tid == 0) s_seq = a.b.seqs;
   __syncthreads();
@@ -1005,28 +1066,13 @@ __global__ __launch_bounds__(AT_T) void k_attend_prompt_join(AttendArgs a, const
   const int seq = s_seq;
   if (seq >= a.b.seqs) return;
   const int32_t first = start_of(a.b, seq), n = start_of(a.b, seq + 1) - first;
-  const int32_t row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
-  if (n <= 0 || row0 >= n * group) return;
-  const int rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
-  const float* mine = parts + ((int64_t)bt * a.kv_heads + head) * splits * PR_ROWS * (D + 2);
-  for (int i = tid + (int)blockIdx.z * AT_T; i < rows * (D / 4); i += AT_T * (int)gridDim.z) {
-    const int r = i / (D / 4), x = (i % (D / 4)) * 4;
-    float top = -INFINITY, sum = 0.0f;
-    for (int z = 0; z < splits; ++z) top = fmaxf(top, mine[(int64_t)z * PR_ROWS * (D + 2) + PR_ROWS * D + r]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < splits; ++z) {
-      const float* p = mine + (int64_t)z * PR_ROWS * (D + 2);
-      const float mz = p[PR_ROWS * D + r], e = __builtin_amdgcn_exp2f(mz - ref);
-      sum += mz == -INFINITY ? p[PR_ROWS * D + PR_ROWS + r] : p[PR_ROWS * D + PR_ROWS + r] * e;
-      v += *reinterpret_cast<const f4*>(p + r * D + x) * e;
-    }
-    const int row = row0 + r, tok = row / group;
-    T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D + x;
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) out[k] = (T)(v[k] * by);
-  }
+  const int32_t row = (int32_t)(bt - base(seq)) * PR_ROWS + r;
+  if (row >= n * group) return;
+  const int tok = row / group;
+  T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
+  const float* mine = parts + (bt * a.kv_heads + head) * splits * PR_ROWS * (D + 2);
+  auto at = [&](int i) { return mine + (int64_t)i * PR_ROWS * (D + 2); };
+  join_row<D, 8>(splits, PR_ROWS, r, at, out);
 }
 
 // ---------------------------------------------------------------- launches
@@ -1067,8 +1113,15 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;
-  hipLaunchKernelGGL((k_attend_join<DT, D, RT>), dim3((unsigned)tiles, (unsigned)a.kv_heads), dim3(AT_T), 0, s, a,
-                     parts, (uint32_t)nb);
+  // rows of a joining block: one where an item has many parts on average, so
+  // that eight groups share them (one sequence of 200003 tokens, 64 parts: 6 us
+  // against 9 with four rows; 16 sequences, 4 parts: 11 against 7 us)
+  const bool many = nb >= 16 * (int64_t)a.b.seqs * a.kv_heads;
+  const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
+  if (many)
+    hipLaunchKernelGGL((k_attend_join<DT, D, RT, 1>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
+  else
+    hipLaunchKernelGGL((k_attend_join<DT, D, RT, 4>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
   return hipGetLastError();
 }
 
@@ -1082,8 +1135,8 @@ static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
                      dim3(AT_T), 0, s, a, parts, splits, out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, 4), dim3(AT_T), 0, s,
-                     a, parts, splits);
+  hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)(tiles * PR_ROWS / 8)), dim3(AT_T),
+                     0, s, a, parts, splits);
   return hipGetLastError();
 }
 
