@@ -151,129 +151,204 @@ __device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
   return q;
 }
 
-// Chunks before each sequence, in before[0 .. seqs]; every block computes it
-// from the lengths, so that a captured call follows them.
-__device__ void plan(const AttendArgs& a, int group, int rows, uint64_t* before, uint64_t* part) {
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int PER = EFFORT_KV_MAX_SEQS / AT_T;
-  uint64_t mine[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int s = tid * PER + i;
-    mine[i] = sum;
-    if (s < a.b.seqs) {
-      const Seq q = seq_of(a, s, group, rows);
-      sum += (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
-    }
-  }
+__device__ inline uint64_t chunks_of(const AttendArgs& a, int s, int group, int rows) {
+  const Seq q = seq_of(a, s, group, rows);
+  return (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+}
+
+// Chunks before the sequences, one entry for `per` of them (one each up to 256
+// sequences); every block computes it from the lengths, so that a captured call
+// follows them.
+struct Plan {
+  uint64_t before[AT_T + 1];
+  uint64_t part[AT_W];
+};
+__device__ inline int per_entry(const AttendArgs& a) { return (a.b.seqs + AT_T - 1) / AT_T; }
+
+// Returns all sequences' chunks; for one sequence that is all there is to know.
+__device__ uint64_t make_plan(const AttendArgs& a, int group, int rows, Plan* p) {
+  if (a.b.seqs == 1) return chunks_of(a, 0, group, rows);
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, per = per_entry(a);
+  uint64_t sum = 0;
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < a.b.seqs) sum += chunks_of(a, tid * per + i, group, rows);
   uint64_t run = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint64_t o = __shfl_up(run, d);
     if (lane >= d) run += o;
   }
-  if (lane == 63) part[wave] = run;
+  if (lane == 63) p->part[wave] = run;
   __syncthreads();
   uint64_t base = run - sum;
-  for (int w = 0; w < wave; ++w) base += part[w];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int s = tid * PER + i;
-    if (s <= a.b.seqs) before[s] = base + mine[i];
-  }
-  if (tid == AT_T - 1 && a.b.seqs == EFFORT_KV_MAX_SEQS) before[EFFORT_KV_MAX_SEQS] = base + sum;
+  for (int w = 0; w < wave; ++w) base += p->part[w];
+  p->before[tid] = base;
+  if (tid == AT_T - 1) p->before[AT_T] = base + sum;
   __syncthreads();
+  return p->before[AT_T];
 }
 
-// The sequence that owns chunk c: the last one with before[s] <= c among those that have chunks.
-__device__ inline int owner(const uint64_t* before, int seqs, uint64_t c) {
-  int lo = 0, hi = seqs;
+// Chunks before sequence s.
+__device__ inline uint64_t start_of_seq(const AttendArgs& a, const Plan& p, int s, int group, int rows) {
+  if (a.b.seqs == 1) return 0;
+  const int per = per_entry(a);
+  uint64_t c = p.before[s / per];
+  for (int i = s / per * per; i < s; ++i) c += chunks_of(a, i, group, rows);
+  return c;
+}
+
+// The sequence that owns chunk c (of those that have chunks), at or after `from`.
+__device__ inline int owner(const AttendArgs& a, const Plan& p, uint64_t c, int group, int rows) {
+  if (a.b.seqs == 1) return 0;
+  const int per = per_entry(a);
+  int lo = 0, hi = AT_T;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (before[mid] <= c) lo = mid; else hi = mid;
+    if (p.before[mid] <= c) lo = mid; else hi = mid;
   }
-  return lo;
+  int s = lo * per;
+  uint64_t at = p.before[lo];
+  for (;;) {
+    const uint64_t n = chunks_of(a, s, group, rows);
+    if (c < at + n || s + 1 >= a.b.seqs) return s;
+    at += n;
+    ++s;
+  }
 }
 
 // ---------------------------------------------------------------- split over blocks
 
-// One 32-token step's codes and scales of a head, as loaded.
-template <int D>
-struct Codes {
-  uint4 k[2][D / 64];
-  uint32_t v[2][4][D / 64];
-  float ks[2], vs[2];
-  bool ok[2];
-};
-
-template <int D>
-__device__ inline void load_codes(const AttendArgs& a, const int32_t* table, int head, int32_t t, int32_t hi,
-                                  int shift, Codes<D>* c) {
-  const int lane = (int)threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int32_t tok = t + 16 * u;
-    int32_t page = -1;
-    if (tok < hi) page = table[tok >> shift];
-    page = __builtin_amdgcn_readfirstlane(page);
-    c->ok[u] = page >= 0 && page < a.b.pages;
-    const int64_t ph = (int64_t)(c->ok[u] ? page : 0) * a.kv_heads + head;  // page 0: read, never used
-    const int64_t at = ((ph << shift) + (tok & ((1 << shift) - 1))) * D;
-    const uint8_t* kp = a.kc + at + i * D + g * 16;
-    const uint8_t* vp = a.vc + at + g * 4 * D + i * (D / 16);
-#pragma unroll
-    for (int x = 0; x < D / 64; ++x) c->k[u][x] = *reinterpret_cast<const uint4*>(kp + 64 * x);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(vp + r * D);
-        c->v[u][r][0] = w.x;
-        c->v[u][r][D / 64 - 1] = w.y;
-      } else {
-        c->v[u][r][0] = *reinterpret_cast<const uint32_t*>(vp + r * D);
-      }
-    }
-    c->ks[u] = a.ks[ph];
-    c->vs[u] = a.vs[ph];
-  }
-}
-
+// A wave takes 32 tokens at a time; its keys' codes are asked for again as soon
+// as the scores are done with them, its values' as soon as the weighted sum is:
+// each is on its way during the other's work, with one set of registers.
+//
 // Blocks share the (sequence, head, row tile) items' chunks evenly, in order:
-// block b takes the chunks [b W / B, (b + 1) W / B) of all W (B: the grid, or W if that is less).  An item that one
-// block has whole is finished there; the others leave (maximum, sum, weighted
-// values) of their part for k_attend_join.  A decode batch of unequal lengths
-// keeps every CU busy to the end without the host knowing the lengths.
-// `RT`: 16-row tiles of an item.
-template <int DT, int FMT, int D, int RT>
-__global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* parts) {
+// block b takes the chunks [b W / B, (b + 1) W / B) of all W (B: the grid, or W
+// if that is less).  An item that one block has whole is finished there; the
+// others leave (maximum, sum, weighted values) of their part for k_attend_join.
+// A decode batch of unequal lengths keeps every CU busy to the end without the
+// host knowing the lengths.  With WHOLE a block takes one item to its end, for
+// tables of so few tokens that joining would cost more than it saves.
+// `RT`: 16-row tiles of an item, `NW`: waves of a block.
+template <int DT, int FMT, int D, int RT, int NW, bool WHOLE>
+__global__ __launch_bounds__(64 * NW, DT == EFFORT_F32 || RT == 2 ? 2 : 3) void k_attend_split(AttendArgs a,
+                                                                                         float* parts) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
-  constexpr int KS = D / 32, ND = D / 16, ROWS = 16 * RT, LD = D + 4;
-  __shared__ uint64_t before[EFFORT_KV_MAX_SEQS + 1];
-  __shared__ uint64_t part[AT_W];
-  __shared__ float s_o[AT_W][ROWS][LD];
-  __shared__ float s_m[AT_W][ROWS], s_l[AT_W][ROWS], s_u[AT_W];
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, j = lane & 15, g = lane >> 4;
-  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens);
-  plan(a, group, ROWS, before, part);
-  const uint64_t total = before[a.b.seqs], nb = total < gridDim.x ? total : gridDim.x;  // no block has nothing
-  if (blockIdx.x >= nb) return;
-  uint64_t c = total * blockIdx.x / nb;
-  const uint64_t c_end = total * (blockIdx.x + 1) / nb;
-  int s = owner(before, a.b.seqs, c);
+  constexpr int KS = D / 32, ND = D / 16, ROWS = 16 * RT, LD = D + 4, THREADS = 64 * NW, STEP = NW * AT_TILE;
+  static_assert(WHOLE || NW == AT_W, "a chunk is a step of a block");
+  __shared__ Plan s_plan;
+  __shared__ float s_o[NW][ROWS][LD];
+  __shared__ float s_m[NW][ROWS], s_l[NW][ROWS], s_u[NW];
+  __shared__ int s_seq;
+  const int tid = (int)threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens), in_page = (1 << shift) - 1;
+  uint64_t c = 0, c_end = 1;
+  int s = 0;
+  if (WHOLE) {
+    auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / ROWS + i; };
+    if (a.b.seqs > 1) {
+      if (tid == 0) s_seq = a.b.seqs;
+      __syncthreads();
+      for (int i = tid; i < a.b.seqs; i += THREADS)
+        if (base(i) <= blockIdx.y && blockIdx.y < base(i + 1)) atomicMin(&s_seq, i);
+      __syncthreads();
+      s = __builtin_amdgcn_readfirstlane(s_seq);
+      if (s >= a.b.seqs) return;
+    }
+  } else {
+    const uint64_t total = make_plan(a, group, ROWS, &s_plan);
+    const uint64_t nb = total < gridDim.x ? total : gridDim.x;  // no block has nothing
+    if (blockIdx.x >= nb) return;
+    c = total * blockIdx.x / nb;
+    c_end = total * (blockIdx.x + 1) / nb;
+    s = __builtin_amdgcn_readfirstlane(owner(a, s_plan, c, group, ROWS));
+  }
+  uint64_t s_start = WHOLE ? 0 : start_of_seq(a, s_plan, s, group, ROWS);
   while (c < c_end) {
-    while (before[s + 1] <= c) ++s;
     const Seq q = seq_of(a, s, group, ROWS);
-    const uint64_t in = c - before[s];
-    const uint32_t item = (uint32_t)(in / q.chunks), ch0 = (uint32_t)(in % q.chunks);
-    const int head = (int)(item / (uint32_t)q.tiles), tile = (int)(item % (uint32_t)q.tiles);
-    const uint32_t left = q.chunks - ch0;
-    const uint32_t take = c_end - c < left ? (uint32_t)(c_end - c) : left;
-    const bool whole = ch0 == 0 && take == (uint32_t)q.chunks;
+    int head, tile;
+    uint32_t ch0 = 0, take = 1;
+    if (WHOLE) {
+      head = (int)blockIdx.x;
+      tile = (int)(blockIdx.y - ((int64_t)q.first * group / ROWS + s));
+      if (tile < 0 || tile >= q.tiles) return;
+      take = (uint32_t)q.chunks;
+    } else {
+      const uint64_t mine = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+      if (c >= s_start + mine) {
+        s_start += mine;
+        if (++s >= a.b.seqs) return;
+        continue;
+      }
+      const uint64_t in = c - s_start;
+      const uint32_t item = (uint32_t)(in / (uint32_t)q.chunks);
+      ch0 = (uint32_t)(in % (uint32_t)q.chunks);
+      head = (int)(item / (uint32_t)q.tiles);
+      tile = (int)(item % (uint32_t)q.tiles);
+      const uint32_t left = q.chunks - ch0;
+      take = c_end - c < left ? (uint32_t)(c_end - c) : left;
+    }
+    const bool whole = WHOLE || (ch0 == 0 && take == (uint32_t)q.chunks);
     const int32_t* table = a.b.table + s * a.b.table_stride;
     const int rows = q.n * group - tile * ROWS < ROWS ? q.n * group - tile * ROWS : ROWS;
+    const int32_t t_begin = q.lo + (int32_t)(ch0 * AT_CHUNK) + wave * AT_TILE;
+    const int64_t stop = (int64_t)q.lo + (int64_t)(ch0 + take) * AT_CHUNK;
+    const int32_t t_end = stop < q.hi ? (int32_t)stop : q.hi;
 
-    // the rows' queries, scaled by a power of two to at most 2^14
+    // pages of the two 16-token halves of the step at t; -1: none, or not this block's
+    struct Two {
+      int32_t p[2];
+    };
+    auto pages_at = [&](int32_t t) {
+      Two r;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        r.p[u] = t < t_end && t + 16 * u < q.hi ? table[(t + 16 * u) >> shift] : -1;
+        r.p[u] = __builtin_amdgcn_readfirstlane(r.p[u]);
+      }
+      return r;
+    };
+    auto there = [&](int32_t p) { return p >= 0 && p < a.b.pages; };
+    auto head_at = [&](int32_t p) { return (int64_t)(there(p) ? p : 0) * a.kv_heads + head; };  // page 0: never used
+    uint4 kc[2][D / 64];
+    uint32_t vc[2][4][D / 64];
+    float ks[2], vs[2];
+    auto load_keys = [&](int32_t t, const Two& pg) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t ph = head_at(pg.p[u]);
+        const uint8_t* from = a.kc + ((ph << shift) + ((t + 16 * u) & in_page)) * D + (j * D + g * 16);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) kc[u][x] = *reinterpret_cast<const uint4*>(from + 64 * x);
+        ks[u] = a.ks[ph];
+      }
+    };
+    auto load_values = [&](int32_t t, const Two& pg) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t ph = head_at(pg.p[u]);
+        const uint8_t* from = a.vc + ((ph << shift) + ((t + 16 * u) & in_page)) * D + (g * 4 * D + j * (D / 16));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (D == 128) {
+            const uint2 w = *reinterpret_cast<const uint2*>(from + r * D);
+            vc[u][r][0] = w.x;
+            vc[u][r][D / 64 - 1] = w.y;
+          } else {
+            vc[u][r][0] = *reinterpret_cast<const uint32_t*>(from + r * D);
+          }
+        }
+        vs[u] = a.vs[ph];
+      }
+    };
+    Two now = pages_at(t_begin), next = pages_at(t_begin + STEP);
+    load_keys(t_begin, now);
+    load_values(t_begin, now);
+
+    // the rows' queries, scaled by a power of two to at most 2^14; the sign of
+    // the call's scale goes into them
     h8 qh[RT][KS], ql[RT][KS];
     float f[RT];
     Sight see[RT];
@@ -287,19 +362,19 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
                      (int64_t)(head * group + r - i * group) * D + g * 16;
       float x[KS][8], top = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           x[k][e] = (float)src[(k >> 1) * 64 + (k & 1) * 8 + e];
           top = fmaxf(top, fabsf(x[k][e]));
         }
-      }
       const float by = power_of_row(max_of_row(top));
-      f[rt] = a.scale * kLog2e / by;
+      f[rt] = fabsf(a.scale) * kLog2e / by;
+      const float mul = a.scale < 0.0f ? -by : by;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] *= by;
+        for (int e = 0; e < 8; ++e) x[k][e] *= mul;
         qh[rt][k] = weights8(x[k]);
         if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
       }
@@ -317,39 +392,13 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    // O counts in `unit`s: a value is code * scale, and scales that equal the
-    // unit (mostly all of them: powers of two) cost nothing.  The unit follows
-    // the scales up at once, down when they are 2^10 smaller.
-    float unit = 1.0f, unit_top = 0.0f;
-    const int32_t t_begin = q.lo + (int32_t)(ch0 * AT_CHUNK) + wave * AT_TILE;
-    const int64_t stop = (int64_t)q.lo + (int64_t)(ch0 + take) * AT_CHUNK;
-    const int32_t t_end = stop < q.hi ? (int32_t)stop : q.hi;
+    // O counts in `unit`s of the values' scale: a token of scale vs weighs w * vs /
+    // unit.  The unit follows the scales up at once, down when they are 2^10
+    // smaller (but never to where what is there could overflow).
+    float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
 
-    Codes<D> nxt;
-    if (t_begin < t_end) load_codes<D>(a, table, head, t_begin, q.hi, shift, &nxt);
-    for (int32_t t = t_begin; t < t_end; t += AT_CHUNK) {
-      Codes<D> cur = nxt;
-      if (t + AT_CHUNK < t_end) load_codes<D>(a, table, head, t + AT_CHUNK, q.hi, shift, &nxt);
-      const bool full = cur.ok[0] && cur.ok[1] && t + AT_TILE - 1 <= see0.high && t > see1.low;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        // a poisoned page: its scores are NaN, its values count as any
-        if (!(fabsf(cur.ks[u]) < INFINITY) || !(fabsf(cur.vs[u]) < INFINITY)) {
-          cur.ks[u] = __uint_as_float(0x7FC00000u);
-          cur.vs[u] = unit;
-        }
-      }
-      if (!full) {  // values of tokens that no row sees weigh 0, so they must not be NaN
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (!cur.ok[u] || t + 16 * u + g * 4 + r >= q.hi || t + 16 * u + g * 4 + r <= see0.low) {
-#pragma unroll
-              for (int x = 0; x < D / 64; ++x) cur.v[u][r][x] = 0u;
-            }
-      }
-      // scores
+    for (int32_t t = t_begin; t < t_end; t += STEP) {
+      const bool ok0 = there(now.p[0]), ok1 = there(now.p[1]);
       f4 sc[RT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -357,7 +406,7 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
         for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const uint4 w = cur.k[u][k >> 1];
+          const uint4 w = kc[u][k >> 1];
           const h8 kf = (k & 1) ? decode8<FMT>(w.z, w.w) : decode8<FMT>(w.x, w.y);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
@@ -366,28 +415,32 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
           }
         }
       }
+      // a poisoned page: its scores are NaN, its values count as any
+      const bool bad0 = __float_as_uint(ks[0]) >= 0x7F800000u || __float_as_uint(vs[0]) >= 0x7F800000u;
+      const bool bad1 = __float_as_uint(ks[1]) >= 0x7F800000u || __float_as_uint(vs[1]) >= 0x7F800000u;
+      const float k0 = bad0 ? __uint_as_float(0x7FC00000u) : ks[0], k1 = bad1 ? __uint_as_float(0x7FC00000u) : ks[1];
+      load_keys(t + STEP, next);
       float w[RT][8];
+      const bool full = ok0 && ok1 && t + AT_TILE - 1 <= see0.high && t > see1.low;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
+        const float c0 = f[rt] * k0, c1 = f[rt] * k1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float fu = f[rt] * cur.ks[u];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[rt][u * 4 + r] = sc[rt][u][r] * fu;
-        }
+        for (int i = 0; i < 8; ++i) w[rt][i] = sc[rt][i >> 2][i & 3] * (i < 4 ? c0 : c1);
         if (!full) {
-          const int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+          const int32_t low = see[rt].low - t - g * 4, high = see[rt].high - t - g * 4;
+          const int32_t high0 = ok0 ? high : -AT_TILE, high1 = ok1 ? high : -AT_TILE;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (!(cur.ok[u] && 16 * u + r <= high && 16 * u + r > low)) w[rt][u * 4 + r] = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const int at = (i >> 2) * 16 + (i & 3);
+            if (at > (i < 4 ? high0 : high1) || at <= low) w[rt][i] = -INFINITY;
+          }
         }
         float top = w[rt][0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, w[rt][i]);
+        for (int i = 1; i < 8; ++i) top = max_of(top, w[rt][i]);
         top = max_of_row(top);
-        if (__any(top > m[rt])) {
+        if (__any(top > m[rt] + kSlack)) {
           const float mn = fmaxf(top, m[rt]);
           const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
           m[rt] = mn;
@@ -398,78 +451,80 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
         // nothing seen so far (or only NaN): the weights are 0 (or NaN)
         const float ref = (m[rt] == -INFINITY ? 0.0f : m[rt]) - kWeightExp;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[rt][i] = __builtin_amdgcn_exp2f(w[rt][i] - ref);
-          l[rt] += w[rt][i];
-        }
+        for (int i = 0; i < 8; ++i) w[rt][i] = __builtin_amdgcn_exp2f(w[rt][i] - ref);
+        l[rt] += ((w[rt][0] + w[rt][1]) + (w[rt][2] + w[rt][3])) + ((w[rt][4] + w[rt][5]) + (w[rt][6] + w[rt][7]));
+      }
+      if (!full) {  // values of tokens that no row sees weigh 0, so they must not be NaN
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!(u ? ok1 : ok0) || t + 16 * u + g * 4 + r >= q.hi || t + 16 * u + g * 4 + r <= see0.low) {
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x) vc[u][r][x] = 0u;
+            }
       }
       // Halves whose scales are far apart are weighed one after the other: the
       // smaller's weights would lose bits below the larger's.
-      const float v0 = cur.ok[0] ? cur.vs[0] : 0.0f, v1 = cur.ok[1] ? cur.vs[1] : 0.0f;
-      const bool apart = cur.ok[0] && cur.ok[1] && fmaxf(v0, v1) > 0x1p10f * fminf(v0, v1);
+      const float v0 = ok0 && !bad0 ? vs[0] : 0.0f, v1 = ok1 && !bad1 ? vs[1] : 0.0f;
+      const bool apart = fminf(v0, v1) > 0.0f && fmaxf(v0, v1) > 0x1p10f * fminf(v0, v1);
 #pragma unroll 1
       for (int pass = 0; pass < (apart ? 2 : 1); ++pass) {
         const float s0 = pass == 0 ? v0 : 0.0f, s1 = apart && pass == 0 ? 0.0f : v1, top = fmaxf(s0, s1);
         unit_top = fmaxf(unit_top, top);
-        if (top > 2.0f * unit || top < 0x1p-10f * unit) {
-          // not so far down that what is there could overflow
-          const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f);
-          const float by = unit / now;
-          unit = now;
+        if (top > 2.0f * unit || (top < 0x1p-10f * unit && top > 0.0f)) {
+          const float to = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f), by = unit / to;
+          unit = to;
+          per_unit = 1.0f / to;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[rt][d] *= by;
         }
-        const float rel[2] = {s0 / unit, s1 / unit};
+        const float rel0 = bad0 && pass == 0 ? 1.0f : s0 * per_unit, rel1 = bad1 && pass == 0 ? 1.0f : s1 * per_unit;
         h8 ph[RT], pl[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = w[rt][i] * rel[i >> 2];
+          for (int i = 0; i < 8; ++i) y[i] = w[rt][i] * (i < 4 ? rel0 : rel1);
           ph[rt] = weights8(y);
           if (SPLIT) pl[rt] = rest8(y, ph[rt]);
         }
         // weighted values: element n * ND + d of a head is row n of product d
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
-          uint32_t e[2][4];  // [token pairs 01 | 23 of a half..][bytes 0 1 of both tokens, 2 3 of both]
-          uint32_t e2[2][4];
+          uint32_t e[4], e2[4];  // both tokens of a pair: bytes 0 and 1, bytes 2 and 3
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            e[u][0] = __builtin_amdgcn_perm(cur.v[u][1][x], cur.v[u][0][x], 0x05010400u);
-            e[u][1] = __builtin_amdgcn_perm(cur.v[u][3][x], cur.v[u][2][x], 0x05010400u);
-            e2[u][0] = __builtin_amdgcn_perm(cur.v[u][1][x], cur.v[u][0][x], 0x07030602u);
-            e2[u][1] = __builtin_amdgcn_perm(cur.v[u][3][x], cur.v[u][2][x], 0x07030602u);
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t lo = vc[h >> 1][(h & 1) * 2][x], hi = vc[h >> 1][(h & 1) * 2 + 1][x];
+            e[h] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+            e2[h] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
           }
+          const h8 vf[4] = {join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]),
+                                  decode2<FMT, false>(e[3])),
+                            join8(decode2<FMT, true>(e[0]), decode2<FMT, true>(e[1]), decode2<FMT, true>(e[2]),
+                                  decode2<FMT, true>(e[3])),
+                            join8(decode2<FMT, false>(e2[0]), decode2<FMT, false>(e2[1]), decode2<FMT, false>(e2[2]),
+                                  decode2<FMT, false>(e2[3])),
+                            join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]),
+                                  decode2<FMT, true>(e2[3]))};
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            h8 vf;
-            if (d == 0)
-              vf = join8(decode2<FMT, false>(e[0][0]), decode2<FMT, false>(e[0][1]), decode2<FMT, false>(e[1][0]),
-                         decode2<FMT, false>(e[1][1]));
-            else if (d == 1)
-              vf = join8(decode2<FMT, true>(e[0][0]), decode2<FMT, true>(e[0][1]), decode2<FMT, true>(e[1][0]),
-                         decode2<FMT, true>(e[1][1]));
-            else if (d == 2)
-              vf = join8(decode2<FMT, false>(e2[0][0]), decode2<FMT, false>(e2[0][1]),
-                         decode2<FMT, false>(e2[1][0]), decode2<FMT, false>(e2[1][1]));
-            else
-              vf = join8(decode2<FMT, true>(e2[0][0]), decode2<FMT, true>(e2[0][1]), decode2<FMT, true>(e2[1][0]),
-                         decode2<FMT, true>(e2[1][1]));
+          for (int d = 0; d < 4; ++d)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
               f4& acc = o[rt][x * 4 + d];
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph[rt], acc, 0, 0, 0);
-              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl[rt], acc, 0, 0, 0);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], ph[rt], acc, 0, 0, 0);
+              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pl[rt], acc, 0, 0, 0);
             }
-          }
         }
       }
+      load_values(t + STEP, next);
+      now = next;
+      next = pages_at(t + 2 * STEP);
     }
 
-    // the four waves' parts become one
+    // the waves' parts become one
     __syncthreads();
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -489,15 +544,15 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
     __syncthreads();
     // slot 0: a part that does not start its item, slot 1: one that does
     float* mine = parts + ((int64_t)blockIdx.x * 2 + (ch0 == 0 ? 1 : 0)) * ROWS * (D + 2);
-    for (int i = tid; i < rows * (D / 4); i += AT_T) {
+    for (int i = tid; i < rows * (D / 4); i += THREADS) {
       const int r = i / (D / 4), x = (i % (D / 4)) * 4;
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < AT_W; ++w) top = fmaxf(top, s_m[w][r]);
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
       const float ref = top == -INFINITY ? 0.0f : top;
       f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < AT_W; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float e = __builtin_amdgcn_exp2f(s_m[w][r] - ref);
         // a wave that saw only NaN has no maximum: its sum stays NaN
         sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * e;
@@ -518,6 +573,7 @@ __global__ __launch_bounds__(AT_T, 2) void k_attend_split(AttendArgs a, float* p
         }
       }
     }
+    if (WHOLE) return;
     c += take;
   }
 }
@@ -599,8 +655,7 @@ template <int DT, int D, int RT, int R>
 __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32) {
   typedef typename ElemOf<DT>::T T;
   constexpr int ROWS = 16 * RT;
-  __shared__ uint64_t before[EFFORT_KV_MAX_SEQS + 1];
-  __shared__ uint64_t part[AT_W];
+  __shared__ Plan s_plan;
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, head = (int)blockIdx.y, group = a.q_heads / a.kv_heads;
   const uint32_t bt = blockIdx.x / (ROWS / R);
@@ -617,8 +672,9 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     if (s >= a.b.seqs) return;
   }
   const Seq q = seq_of(a, s, group, ROWS);
-  const int tile = (int)(bt - base(s));
-  if (tile * ROWS + r0 >= q.n * group) return;
+  const int64_t at_tile = (int64_t)bt - base(s);
+  if (at_tile < 0 || at_tile * ROWS + r0 >= (int64_t)q.n * group) return;
+  const int tile = (int)at_tile;
   const int r = r0 + (tid >> 5) / (8 / R);
   const bool mine = tile * ROWS + r < q.n * group;
   const int row = mine ? tile * ROWS + r : tile * ROWS + r0, tok = row / group;
@@ -627,9 +683,8 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     for (int i = tid & 31; i < D; i += 32) out[i] = (T)0.0f;
     return;
   }
-  plan(a, group, ROWS, before, part);
-  const uint64_t total = before[a.b.seqs], nb = total < nb32 ? total : nb32;
-  const uint64_t c0 = before[s] + ((uint64_t)head * q.tiles + tile) * q.chunks, c1 = c0 + q.chunks - 1;
+  const uint64_t total = make_plan(a, group, ROWS, &s_plan), nb = total < nb32 ? total : nb32;
+  const uint64_t c0 = start_of_seq(a, s_plan, s, group, ROWS) + ((uint64_t)head * q.tiles + tile) * q.chunks, c1 = c0 + q.chunks - 1;
   const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
   if (b0 == b1) return;
   const float* first = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
@@ -1085,7 +1140,12 @@ static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) {
   return rows <= 16 * (int64_t)seqs ? 1 : rows <= 32 * (int64_t)seqs ? 2 : 0;
 }
 
-static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
+// Blocks that share a call's chunks: as many as the CUs hold at once.
+static int64_t split_blocks(bool f32, int rt) { return (f32 || rt == 2 ? 2 : 3) * (int64_t)cu_count(); }
+
+// Tables of up to 1024 tokens: one block of eight waves for each item, in at
+// most four steps, and nothing to join.
+constexpr int64_t kWholeTokens = 1024;
 
 // 128-row blocks of a head (a bound), and in how many parts their tokens are
 // taken so that two blocks fall to every CU.
@@ -1095,11 +1155,12 @@ static int32_t prompt_splits(int64_t tiles, int32_t kv_heads) {
   return (int32_t)(z < 1 ? 1 : z > 32 ? 32 : z);
 }
 
+// Enough for any type and any table.
 uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads) {
   if (seqs == 0 || tokens == 0) return 0;
   const int32_t group = q_heads / kv_heads;
   const int rt = row_tiles(seqs, tokens, group);
-  if (rt) return (uint64_t)split_blocks() * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
+  if (rt) return (uint64_t)split_blocks(false, rt) * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
   const int64_t tiles = prompt_tiles(seqs, tokens, group);
   const int32_t splits = prompt_splits(tiles, kv_heads);
   return splits == 1 ? 0 : (uint64_t)tiles * kv_heads * splits * PR_ROWS * (dim + 2) * sizeof(float);
@@ -1107,12 +1168,17 @@ uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t t
 
 template <int DT, int FMT, int D, int RT>
 static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
-  const int64_t nb = split_blocks();
+  const int64_t nb = split_blocks(DT == EFFORT_F32, RT);
+  const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;  // of a head, a bound
   float* parts = static_cast<float*>(a.ws);
-  hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
+  if ((int64_t)a.b.max_pages * a.page_tokens <= kWholeTokens && tiles <= 65535) {
+    hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true>), dim3((unsigned)a.kv_heads, (unsigned)tiles), dim3(512), 0,
+                       s, a, parts);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, AT_W, false>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;
   // rows of a joining block: one where an item has many parts on average, so
   // that eight groups share them (one sequence of 200003 tokens, 64 parts: 6 us
   // against 9 with four rows; 16 sequences, 4 parts: 11 against 7 us)

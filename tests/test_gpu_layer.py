@@ -279,16 +279,20 @@ ATTEND = [
 
 
 @pytest.mark.parametrize("fmt,dtype,dim,page,group,window", ATTEND)
-@pytest.mark.parametrize("kind", ["one", "few", "prompt"])
+@pytest.mark.parametrize("kind", ["one", "few", "prompt", "one in a long table", "few in a long table"])
 def test_attend(fmt, dtype, dim, page, group, window, kind):
-    if kind == "one":
+    room = 3000 if "long" in kind else 0
+    if kind == "one in a long table":
+        lens = [1, 15, 31, 32, 33, 127, 128, 129, 0, 300]
+        new = [1] * len(lens)
+    elif kind == "one":
         lens = [1, 15, 16, 17, 0, 31, 32, 33, 127, 128, 129, 700, 1403]
         new = [1] * len(lens)
-    elif kind == "few":
+    elif kind.startswith("few"):
         lens, new = [7, 1, 40, 0, 333, 5, 64, 200], [7, 1, 3, 2, 5, 0, 4, 8]
     else:
         lens, new = [130, 65, 64, 300, 33, 1, 257], [130, 65, 17, 41, 33, 1, 128]
-    c = Case(11, lens, new, group=group, dim=dim, page=page, fmt=fmt, dtype=dtype)
+    c = Case(11, lens, new, group=group, dim=dim, page=page, fmt=fmt, dtype=dtype, room=room)
     _, worst = c.check_attend(c.rand(2 * group, 1.5), window=window)
     say("attend %s %s %s D %d page %d group %d window %d: %.3f of the bound" % (
         kind, fmt, dtype, dim, page, group, window, worst))
@@ -331,6 +335,26 @@ def test_attend_rows_of_nobody_and_bad_pages():
         out = torch.full_like(q, 77.0)
         c.check_attend(q, out=out)
         assert bool((out[-3:] == 77.0).all()) and bool((out[c.starts[6]:c.starts[7]] == 0.0).all())
+
+
+@pytest.mark.parametrize("new", [[1], [5], [40], [1, 1], [3, 60]])
+@pytest.mark.parametrize("room", [0, 3000])
+def test_rows_before_the_first_sequence(new, room):
+    """q_starts[0] > 0: the rows before it are nobody's."""
+    lens = [n + 50 for n in new]
+    c = Case(62, lens, new, page=16, room=room)
+    c.starts = [x + 37 for x in c.starts]
+    c.batch = E.KVBatch(c.batch.page_table, ints(lens), ints(c.starts))
+    n = c.starts[-1] + 2
+    q, k, v = c.rand(4, rows=n), c.rand(2, rows=n), c.rand(2, rows=n)
+    q_out, out = torch.full_like(q, 77.0), torch.full_like(q, 77.0)
+    c.cache.append(c.batch, k, v, q=q, q_out=q_out)
+    L.append(c.np, c.table, lens, c.starts, f64(k), f64(v), None, False, "e4m3")
+    c.check_cache()
+    c.check_attend(q, out=out)
+    for t in (q_out, out):
+        assert bool((t[:37] == 77.0).all()) and bool((t[-2:] == 77.0).all())
+    assert torch.equal(q_out[37:-2], q[37:-2])
 
 
 def test_attend_poisoned_page_reaches_only_who_sees_it():
