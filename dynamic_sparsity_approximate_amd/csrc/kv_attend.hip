@@ -700,18 +700,20 @@ constexpr int PR_ROWS = 32 * AT_W;  // rows of a block: 32 a wave
 constexpr int PR_TILE = 64;         // tokens of one step
 constexpr int PR_SUB = PR_TILE / 16;
 
-// 16-byte pieces of a step in LDS, as fp16, placed so that eight neighbouring
-// lanes' 16-byte accesses touch all 32 banks: keys [token][piece of 8 elements],
-// values [element][piece of 8 tokens, in the order in which the product of
-// weights and values counts them].
+// 16-byte pieces of a step in LDS, as fp16: keys [token][piece of 8 elements],
+// values [element, in the products' order][piece of 8 tokens, in the order in
+// which the product of weights and values counts them].  The pieces of a row
+// are exchanged so that 16 neighbouring lanes' accesses, reading and writing,
+// fall on 16 different pieces of 256 bytes.
 template <int D>
 __device__ inline int key_piece(int token, int piece) {
-  return token * (D / 8) + (piece ^ (token & 7));
+  return D == 128 ? token * 16 + (piece ^ (token & 15)) : token * 8 + (piece ^ (token >> 1 & 7));
 }
 template <int D>
 __device__ inline int value_piece(int element, int piece) {
-  const int f = D == 128 ? (element >> 3) ^ ((element >> 2 & 1) << 2) : element >> 2;
-  return element * (PR_TILE / 8) + (piece ^ (f & 7));
+  constexpr int ND = D / 16;
+  const int d = element % ND, j = element / ND;
+  return (d * 16 + j) * (PR_TILE / 8) + (piece ^ (j >> 1 & 7) ^ (d >> 2 << 2));
 }
 
 // What a thread carries of a step from memory to LDS: D / 64 times 16 codes of a
@@ -909,26 +911,44 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     return (uint32_t)(__ballot(pages >= 0 && pages < a.b.pages) & ((1u << SUB) - 1));
   };
 
-  Staged<D> st;
-  uint32_t ks_l = 0, vs_l = 0, ok = 0;
-  int32_t pages_next = -1;
+  // Codes of two steps are in flight: those of the next one, which go to LDS
+  // during this one, and those of the one after (short prompts have few steps
+  // and cold caches: with one step in flight they waited for memory in each).
+  // Steps alternate between two sets, in a loop unrolled by two: moving a set
+  // would wait for it.
+  struct Flight {
+    Staged<D> st;
+    uint32_t ks, vs, ok;
+  };
+  Flight even, odd;  // of the steps step0, step0 + 2, ... and the others
+  int32_t pages2 = -1;
+  auto fetch_at = [&](int32_t step, int32_t pages, Flight& to) {
+    if (step < step1) {
+      fetch(lo + step * PR_TILE, pages, &to.st, &to.ks, &to.vs);
+      to.ok = there(pages);
+    }
+  };
+  even.ks = even.vs = even.ok = odd.ks = odd.vs = odd.ok = 0;
   if (step0 < step1) {
     const int32_t t = lo + step0 * PR_TILE;
-    const int32_t pages = page_at(t);
-    pages_next = page_at(t + PR_TILE);
-    fetch(t, pages, &st, &ks_l, &vs_l);
-    ok = there(pages);
-    store(t, ok, st, vs_l, 0);
+    const int32_t p0 = page_at(t), p1 = page_at(t + PR_TILE), p2 = page_at(t + 2 * PR_TILE);
+    fetch_at(step0, p0, even);
+    fetch_at(step0 + 1, p1, odd);
+    store(t, even.ok, even.st, even.vs, 0);
+    pages2 = p2;
   }
   __syncthreads();
-  // the lane's first piece of a key by the product's parity, and of a value's
-  // tokens by its half; the others lie at constant distances
-  const int k_at[2] = {key_piece<D>(j, g), key_piece<D>(j, 4 + g)};
+  // the lane's pieces of a key by the product, and of a value's tokens by its
+  // half; the others lie at constant distances
+  int k_at[KS];
+#pragma unroll
+  for (int k = 0; k < KS; ++k) k_at[k] = key_piece<D>(j, k * 4 + g);
   const int v_at[2] = {value_piece<D>(j * ND, g), value_piece<D>(j * ND, 4 + g)};
-  int buf = 0;
-#pragma unroll 1
-  for (int32_t step = step0; step < step1; ++step, buf ^= 1) {
+  // one step: its codes are in LDS buffer `buf` and its scales in `mine`, whose
+  // registers then take the step after the next
+  auto one_step = [&](int32_t step, int buf, Flight& mine, Flight& next) {
     const int32_t t = lo + step * PR_TILE;
+    const uint32_t ks_l = mine.ks, vs_l = mine.vs, ok = mine.ok;
     // the step's scales, those of sub-tile lane & 3 in each lane
     const uint32_t there_now = ok;
     // a poisoned page: its scores are NaN, its values count as any
@@ -937,12 +957,8 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     // 0 where a sub-tile has no say in the unit (values of scale 0 are 0 in LDS)
     const float vs_lane = (there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
     const float v_hi = uniform(quad_max(vs_lane)), v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
-    if (step + 1 < step1) {
-      const int32_t pages = pages_next;
-      pages_next = page_at(t + 2 * PR_TILE);
-      fetch(t + PR_TILE, pages, &st, &ks_l, &vs_l);
-      ok = there(pages);
-    }
+    fetch_at(step + 2, pages2, mine);
+    pages2 = page_at(t + 3 * PR_TILE);
     // Sub-tiles whose values' scales are far apart are taken one after the
     // other: the weights of the smaller would lose bits below the larger.
     const int passes = v_hi > 0x1p10f * v_lo ? SUB : 1;
@@ -955,13 +971,13 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     f4 sc[RT][SUB];
     h8 kf[2][KS];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k & 1] + (k >> 1) * 8];
+    for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k]];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       if (u + 1 < SUB) {
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          kf[(u + 1) & 1][k] = s_k[buf][k_at[k & 1] + (u + 1) * 16 * (D / 8) + (k >> 1) * 8];
+          kf[(u + 1) & 1][k] = s_k[buf][k_at[k] + (u + 1) * 16 * (D / 8)];
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1019,7 +1035,7 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
       // nothing seen so far (or only NaN): the weights are 0 (or NaN)
       ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
     }
-    if (pass == 0) store(t + PR_TILE, ok, st, vs_l, buf ^ 1);  // behind the last step: never read
+    if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
     const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
     set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
     const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
@@ -1049,7 +1065,7 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
         const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          to[d] = s_v[buf][v_at[D == 128 ? h ^ (d0 >> 2) : h] + (d0 + d) * (PR_TILE / 8)];
+          to[d] = s_v[buf][v_at[h ^ (d0 >> 2)] + (d0 + d) * 16 * (PR_TILE / 8)];
       };
       load_values(0, vf[0]);
 #pragma unroll
@@ -1069,6 +1085,11 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
       }
     }
     __syncthreads();
+  };
+#pragma unroll 1
+  for (int32_t step = step0; step < step1; step += 2) {
+    one_step(step, 0, even, odd);
+    if (step + 1 < step1) one_step(step + 1, 1, odd, even);
   }
 
   // rows of the result: element (g * 4 + r) * ND + d of row j
