@@ -730,7 +730,12 @@ struct Staged {
 // are in flight while this one is multiplied).  Decoding per wave instead
 // would cost as many vector instructions as the softmax.  Heads run fastest
 // over the grid: with 8 heads all blocks of a head share one XCD's L2.
-template <int DT, int FMT, int D>
+//
+// ONE: a step lies in one page (pages of 64 tokens and more), so that its scales
+// are two scalars.  Two waves a SIMD cannot hide their own instructions: the
+// general form, with four sub-tiles' scales, takes 309 vector and 250 scalar
+// instructions a step beside 64 products, and they are its time.
+template <int DT, int FMT, int D, bool ONE>
 __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
@@ -817,6 +822,8 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
   // once, down when they are 2^10 smaller (but never to where what is there
   // could overflow).
   float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
+  uint32_t now_vs = 0;  // ONE: the last step's scale, log2 of its ratio to the unit, and 1 / ratio
+  float now_up = 0.0f, now_back = 1.0f;
   auto set_unit = [&](float top) {
     unit_top = fmaxf(unit_top, top);
     if (top > 2.0f * unit || (top < 0x1p-10f * unit && top > 0.0f)) {
@@ -830,9 +837,9 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     }
   };
 
-  // page of sub-tile lane & 3 of the step at t; -1: none
+  // page of the step at t, or of its sub-tile lane & 3; -1: none
   auto page_at = [&](int32_t t) {
-    const int32_t tok = t + 16 * (lane & 3);
+    const int32_t tok = ONE ? t : t + 16 * (lane & 3);
     return tok < hi ? table[tok >> shift] : -1;
   };
   const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
@@ -840,13 +847,27 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
   const bool v_mine = D == 128 || wave < 2;
   const int in_page = (1 << shift) - 1;
   auto head_of = [&](int32_t pages, int sub) {  // (page, head) of a sub-tile; page 0 where there is none
-    const int32_t pg = __builtin_amdgcn_readlane(pages, sub);
+    const int32_t pg = ONE ? pages : __builtin_amdgcn_readlane(pages, sub);
     return (int64_t)(pg >= 0 && pg < a.b.pages ? pg : 0) * a.kv_heads + head;
   };
   auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, uint32_t* ks, uint32_t* vs) {
     const int32_t own = pages >= 0 && pages < a.b.pages ? pages : 0;
     *ks = __float_as_uint(a.ks[(int64_t)own * a.kv_heads + head]);
     *vs = __float_as_uint(a.vs[(int64_t)own * a.kv_heads + head]);
+    if (ONE) {  // one address, and constant distances
+      const int64_t at = (head_of(pages, 0) << shift) + (t & in_page);
+      const uint8_t *kp = a.kc + at * D, *vp = a.vc + at * D;
+      const uint32_t k_off = (uint32_t)(k_tok * D + k_piece * 16), v_off = (uint32_t)((v_q * 32 + v_g * 4) * D + v_el);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) st->k[i] = *reinterpret_cast<const uint4*>(kp + (k_off + i * 4096));
+      if (v_mine) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(vp + (v_off + (u * 16 + r) * D));
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const int sub = D == 128 ? i * 2 + (wave >> 1) : wave;  // of token k_tok + i * 4096 / D
@@ -875,7 +896,10 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
       s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
     }
     if (!v_mine) return;
-    ok &= (uint32_t)__ballot(vs != 0u);
+    if (ONE)
+      ok = __builtin_amdgcn_readfirstlane(vs) != 0u ? ok : 0u;
+    else
+      ok &= (uint32_t)__ballot(vs != 0u);
     if ((ok & ((1u << SUB) - 1)) != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
       // values of tokens that no row sees weigh 0, so they must not be NaN;
       // those of scale 0 are 0
@@ -908,7 +932,8 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
         join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]), decode2<FMT, true>(e2[3]));
   };
   auto there = [&](int32_t pages) {  // bit per sub-tile
-    return (uint32_t)(__ballot(pages >= 0 && pages < a.b.pages) & ((1u << SUB) - 1));
+    const bool in = pages >= 0 && pages < a.b.pages;
+    return ONE ? (in ? (1u << SUB) - 1 : 0u) : (uint32_t)__ballot(in) & ((1u << SUB) - 1);
   };
 
   // Codes of two steps are in flight: those of the next one, which go to LDS
@@ -953,15 +978,19 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     const uint32_t there_now = ok;
     // a poisoned page: its scores are NaN, its values count as any
     const bool bad = ks_l >= 0x7F800000u || vs_l >= 0x7F800000u;
-    const float ks_lane = __uint_as_float(bad ? 0x7FC00000u : ks_l);
+    const float ks_lane = __uint_as_float(bad ? 0x7FC00000u : ks_l);  // (ONE: of the step)
     // 0 where a sub-tile has no say in the unit (values of scale 0 are 0 in LDS)
-    const float vs_lane = (there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
-    const float v_hi = uniform(quad_max(vs_lane)), v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
+    const float vs_lane = (ONE ? there_now != 0 : there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
+    float v_hi = vs_lane, v_lo = vs_lane;
+    if (!ONE) {
+      v_hi = uniform(quad_max(vs_lane));
+      v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
+    }
     fetch_at(step + 2, pages2, mine);
     pages2 = page_at(t + 3 * PR_TILE);
     // Sub-tiles whose values' scales are far apart are taken one after the
     // other: the weights of the smaller would lose bits below the larger.
-    const int passes = v_hi > 0x1p10f * v_lo ? SUB : 1;
+    const int passes = !ONE && v_hi > 0x1p10f * v_lo ? SUB : 1;
 #pragma unroll 1
     for (int pass = 0; pass < passes; ++pass) {
     const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
@@ -998,7 +1027,7 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
-        c[rt][u] = f[rt] * lane_of(ks_lane, u);
+        c[rt][u] = ONE ? f[rt] * ks_lane : f[rt] * lane_of(ks_lane, u);
     if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -1016,41 +1045,70 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
         }
       }
     }
-    float ref[RT];
+    float ref[RT], top[RT];
+    bool over = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      float top = -INFINITY;
+      top[rt] = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
-        top = max_of(top, max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]) * c[rt][u]);
-      top = max_of_row(top);
-      if (__any(top > m[rt] + kSlack)) {
-        const float mn = fmaxf(top, m[rt]);
+      for (int u = 0; u < SUB; ++u) {
+        float x = max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]);
+        if (!ONE) x *= c[rt][u];
+        top[rt] = max_of(top[rt], x);
+      }
+      top[rt] = max_of_row(ONE ? top[rt] * c[rt][0] : top[rt]);
+      over = over || top[rt] > m[rt] + kSlack;
+    }
+    if (__any(over)) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float mn = fmaxf(top[rt], m[rt]);
         const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
         m[rt] = mn;
         l[rt] *= alpha;
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
       }
-      // nothing seen so far (or only NaN): the weights are 0 (or NaN)
-      ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
     }
+    // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
     if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
-    const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
-    set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
-    const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
-    const float up_lane = __builtin_amdgcn_logf(rel), back_lane = __builtin_amdgcn_rcpf(rel);
+    float up_lane = 0.0f, back_lane = 1.0f;
+    if (ONE) {
+      if (__float_as_uint(vs_lane) != now_vs) {  // another scale than the last step's
+        now_vs = __float_as_uint(vs_lane);
+        set_unit(vs_lane);
+        const float rel = vs_lane > 0.0f ? vs_lane * per_unit : 1.0f;
+        now_up = uniform(__builtin_amdgcn_logf(rel));
+        now_back = uniform(__builtin_amdgcn_rcpf(rel));
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) ref[rt] += now_up;
+    } else {
+      const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
+      set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
+      const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
+      up_lane = __builtin_amdgcn_logf(rel);
+      back_lane = __builtin_amdgcn_rcpf(rel);
+    }
+    float sum[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
     h8 ph[RT][2], pl[RT][2];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      const float up = lane_of(up_lane, u), back = lane_of(back_lane, u);
+      const float up = ONE ? 0.0f : lane_of(up_lane, u), back = ONE ? 1.0f : lane_of(back_lane, u);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float w[4];
-        const float base = ref[rt] + up;
+        const float base = ONE ? ref[rt] : ref[rt] + up;
 #pragma unroll
         for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
-        l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
+        if (ONE)
+          sum[rt] += (w[0] + w[1]) + (w[2] + w[3]);
+        else
+          l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int e = (u & 1) * 4 + r;
@@ -1058,6 +1116,10 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
           if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
         }
       }
+    }
+    if (ONE) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
     }
     __builtin_amdgcn_sched_barrier(0);
       h8 vf[2][4];
@@ -1218,8 +1280,11 @@ static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
   const int32_t splits = prompt_splits(tiles, a.kv_heads);
   float* parts = static_cast<float*>(a.ws);
   const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
-  hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D>), dim3((unsigned)a.kv_heads, (unsigned)tiles, (unsigned)splits),
-                     dim3(AT_T), 0, s, a, parts, splits, out_vec);
+  const dim3 grid((unsigned)a.kv_heads, (unsigned)tiles, (unsigned)splits);
+  if (a.page_tokens >= PR_TILE)
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true>), grid, dim3(AT_T), 0, s, a, parts, splits, out_vec);
+  else
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false>), grid, dim3(AT_T), 0, s, a, parts, splits, out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)(tiles * PR_ROWS / 8)), dim3(AT_T),
