@@ -696,7 +696,13 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
 
 // ---------------------------------------------------------------- prompts
 
-constexpr int PR_ROWS = 32 * AT_W;  // rows of a block: 32 a wave
+// Rows of a block: RT 16-row tiles a wave.  Two for prompts that fill the chip;
+// one where there are not two such blocks a CU, for twice the blocks and (heads
+// of 64 elements) three of them on a CU.
+template <int RT>
+constexpr int prompt_rows() {
+  return 16 * RT * AT_W;
+}
 constexpr int PR_TILE = 64;         // tokens of one step
 constexpr int PR_SUB = PR_TILE / 16;
 
@@ -724,8 +730,8 @@ struct Staged {
   uint32_t v[2][4];
 };
 
-// One block per (128 rows of a sequence, head, part of their tokens): its four
-// waves have 32 rows each and share every 64-token step's keys and values, which
+// One block per (128 or 64 rows of a sequence, head, part of their tokens): its
+// four waves have a quarter each and share every 64-token step's keys and values, which
 // are decoded once on their way into LDS (two buffers: the next step's codes
 // are in flight while this one is multiplied).  Decoding per wave instead
 // would cost as many vector instructions as the softmax.  Heads run fastest
@@ -735,11 +741,12 @@ struct Staged {
 // are two scalars.  Two waves a SIMD cannot hide their own instructions: the
 // general form, with four sub-tiles' scales, takes 309 vector and 250 scalar
 // instructions a step beside 64 products, and they are its time.
-template <int DT, int FMT, int D, bool ONE>
-__global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec) {
+template <int DT, int FMT, int D, bool ONE, int RT>
+__global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 ? 2 : 3) : DT == EFFORT_F32 && D == 128 ? 1 : 2)
+void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
-  constexpr int KS = D / 32, ND = D / 16, RT = 2, SUB = PR_SUB;
+  constexpr int KS = D / 32, ND = D / 16, SUB = PR_SUB, PR_ROWS = prompt_rows<RT>(), WROWS = 16 * RT;
   __shared__ h8 s_k[2][PR_TILE * D / 8];
   __shared__ h8 s_v[2][PR_TILE * D / 8];
   __shared__ int s_seq;
@@ -772,39 +779,8 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
   const int32_t step0 = (int32_t)((int64_t)steps * z / splits), step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
   const int32_t* table = a.b.table + seq * a.b.table_stride;
 
-  // this wave's rows (those behind the last one repeat it)
-  h8 qh[RT][KS], ql[RT][KS];
-  float f[RT];
-  Sight see[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    int r = wave * 32 + rt * 16 + j;
-    r = row0 + (r < rows ? r : rows - 1);
-    const int i = r / group;
-    see[rt] = sight_of(pos + i, hi, a.window);
-    const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
-    float x[KS][8], top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[k][e] = (float)src[(k * 4 + g) * 8 + e];
-        top = fmaxf(top, fabsf(x[k][e]));
-      }
-    // the scale's sign goes into q: what is left of it keeps the scores' order
-    const float by = power_of_row(max_of_row(top));
-    f[rt] = fabsf(a.scale) * kLog2e / by;
-    const float mul = a.scale < 0.0f ? -by : by;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] *= mul;
-      qh[rt][k] = weights8(x[k]);
-      if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
-    }
-  }
-  const int last = wave * 32 + 31 < rows ? wave * 32 + 31 : rows - 1;
-  const int front = wave * 32 < rows ? wave * 32 : rows - 1;
+  const int last = wave * WROWS + WROWS - 1 < rows ? wave * WROWS + WROWS - 1 : rows - 1;
+  const int front = wave * WROWS < rows ? wave * WROWS : rows - 1;
   const int32_t all_high = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + front) / group, hi, a.window).high);
   const int32_t all_low = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + last) / group, hi, a.window).low);
 
@@ -846,17 +822,30 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
   const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
   const bool v_mine = D == 128 || wave < 2;
   const int in_page = (1 << shift) - 1;
-  auto head_of = [&](int32_t pages, int sub) {  // (page, head) of a sub-tile; page 0 where there is none
-    const int32_t pg = ONE ? pages : __builtin_amdgcn_readlane(pages, sub);
-    return (int64_t)(pg >= 0 && pg < a.b.pages ? pg : 0) * a.kv_heads + head;
+  // Addresses are a lane's place in page 0 plus the page times a page's bytes
+  // (pages of 16 and 32 tokens divide a step, so that a lane's slot is the same
+  // in every step); with ONE a scalar address plus a lane's constant offset.
+  // Page 0 is read where there is none, and never used.
+  const uint32_t page_bytes = (uint32_t)a.kv_heads << shift << (D == 128 ? 7 : 6);
+  const int64_t at_head = (int64_t)head << shift;
+  auto lane_base = [&](const uint8_t* c, int tok, int byte) {  // of token `tok` of a step
+    return c + (at_head + (tok & in_page)) * D + byte;
   };
+  const uint8_t* k_base[D / 64];
+  const uint8_t* v_base[2];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) k_base[i] = lane_base(a.kc, k_tok + i * (4096 / D), k_piece * 16);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) v_base[u] = lane_base(a.vc, (v_q * 2 + u) * 16 + v_g * 4, v_el);
+  const float *ks_base = a.ks + head, *vs_base = a.vs + head;
+  auto valid = [&](int32_t page) { return (uint32_t)page < (uint32_t)a.b.pages ? (uint32_t)page : 0u; };
   auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, uint32_t* ks, uint32_t* vs) {
-    const int32_t own = pages >= 0 && pages < a.b.pages ? pages : 0;
-    *ks = __float_as_uint(a.ks[(int64_t)own * a.kv_heads + head]);
-    *vs = __float_as_uint(a.vs[(int64_t)own * a.kv_heads + head]);
-    if (ONE) {  // one address, and constant distances
-      const int64_t at = (head_of(pages, 0) << shift) + (t & in_page);
-      const uint8_t *kp = a.kc + at * D, *vp = a.vc + at * D;
+    const uint64_t own = (uint64_t)valid(pages) * (uint32_t)a.kv_heads;
+    *ks = __float_as_uint(ks_base[own]);
+    *vs = __float_as_uint(vs_base[own]);
+    if (ONE) {
+      const uint64_t at = (uint64_t)valid(pages) * page_bytes + (uint64_t)(at_head + (t & in_page)) * D;
+      const uint8_t *kp = a.kc + at, *vp = a.vc + at;
       const uint32_t k_off = (uint32_t)(k_tok * D + k_piece * 16), v_off = (uint32_t)((v_q * 32 + v_g * 4) * D + v_el);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) st->k[i] = *reinterpret_cast<const uint4*>(kp + (k_off + i * 4096));
@@ -868,18 +857,18 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
       }
       return;
     }
+    auto place = [&](int sub) {  // of the page of a sub-tile
+      return (uint64_t)valid(__builtin_amdgcn_readlane(pages, sub)) * page_bytes;
+    };
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const int sub = D == 128 ? i * 2 + (wave >> 1) : wave;  // of token k_tok + i * 4096 / D
-      const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16) & in_page);
-      st->k[i] = *reinterpret_cast<const uint4*>(a.kc + at * D + ((k_tok & 15) * D + k_piece * 16));
+      st->k[i] = *reinterpret_cast<const uint4*>(k_base[i] + place(sub));
     }
     if (v_mine) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int sub = v_q * 2 + u;
-        const int64_t at = (head_of(pages, sub) << shift) + ((t + sub * 16) & in_page);
-        const uint8_t* from_row = a.vc + at * D + (v_g * 4 * D + v_el);
+        const uint8_t* from_row = v_base[u] + place(v_q * 2 + u);
 #pragma unroll
         for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(from_row + r * D);
       }
@@ -932,7 +921,7 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
         join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]), decode2<FMT, true>(e2[3]));
   };
   auto there = [&](int32_t pages) {  // bit per sub-tile
-    const bool in = pages >= 0 && pages < a.b.pages;
+    const bool in = (uint32_t)pages < (uint32_t)a.b.pages;
     return ONE ? (in ? (1u << SUB) - 1 : 0u) : (uint32_t)__ballot(in) & ((1u << SUB) - 1);
   };
 
@@ -959,9 +948,40 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
     const int32_t p0 = page_at(t), p1 = page_at(t + PR_TILE), p2 = page_at(t + 2 * PR_TILE);
     fetch_at(step0, p0, even);
     fetch_at(step0 + 1, p1, odd);
-    store(t, even.ok, even.st, even.vs, 0);
     pages2 = p2;
   }
+  // this wave's rows (those behind the last one repeat it)
+  h8 qh[RT][KS], ql[RT][KS];
+  float f[RT];
+  Sight see[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    int r = wave * WROWS + rt * 16 + j;
+    r = row0 + (r < rows ? r : rows - 1);
+    const int i = r / group;
+    see[rt] = sight_of(pos + i, hi, a.window);
+    const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
+    float x[KS][8], top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[k][e] = (float)src[(k * 4 + g) * 8 + e];
+        top = fmaxf(top, fabsf(x[k][e]));
+      }
+    // the scale's sign goes into q: what is left of it keeps the scores' order
+    const float by = power_of_row(max_of_row(top));
+    f[rt] = fabsf(a.scale) * kLog2e / by;
+    const float mul = a.scale < 0.0f ? -by : by;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] *= mul;
+      qh[rt][k] = weights8(x[k]);
+      if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
+    }
+  }
+  if (step0 < step1) store(lo + step0 * PR_TILE, even.ok, even.st, even.vs, 0);
   __syncthreads();
   // the lane's pieces of a key by the product, and of a value's tokens by its
   // half; the others lie at constant distances
@@ -1158,7 +1178,7 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float sum = sum_of_row(l[rt]);
-    const int r0 = wave * 32 + rt * 16 + j;
+    const int r0 = wave * WROWS + rt * 16 + j;
     if (r0 >= rows) continue;
     if (splits == 1) {
       const int row = row0 + r0, tok = row / group;
@@ -1188,9 +1208,10 @@ __global__ __launch_bounds__(AT_T, DT == EFFORT_F32 && D == 128 ? 1 : 2) void k_
 }
 
 // Joins the parts of k_attend_prompt's rows: one block per (8 rows, head).
-template <int DT, int D>
+template <int DT, int D, int RT>
 __global__ __launch_bounds__(AT_T) void k_attend_prompt_join(AttendArgs a, const float* parts, int32_t splits) {
   typedef typename ElemOf<DT>::T T;
+  constexpr int PR_ROWS = prompt_rows<RT>();
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, group = a.q_heads / a.kv_heads, head = (int)blockIdx.x;
   const int64_t bt = blockIdx.y / (PR_ROWS / 8);
@@ -1230,12 +1251,27 @@ static int64_t split_blocks(bool f32, int rt) { return (f32 || rt == 2 ? 2 : 3) 
 // most four steps, and nothing to join.
 constexpr int64_t kWholeTokens = 1024;
 
-// 128-row blocks of a head (a bound), and in how many parts their tokens are
-// taken so that two blocks fall to every CU.
-static int64_t prompt_tiles(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group / PR_ROWS + seqs; }
-static int32_t prompt_splits(int64_t tiles, int32_t kv_heads) {
-  const int64_t z = 2 * (int64_t)cu_count() / (tiles * kv_heads);
-  return (int32_t)(z < 1 ? 1 : z > 32 ? 32 : z);
+// How a prompt is shared out: 16-row tiles of a wave, blocks of rows of a head
+// (a bound), and in how many parts their tokens are taken so that as many blocks
+// as a CU holds fall to every CU.
+struct PromptShape {
+  int rt;
+  int64_t tiles;
+  int32_t splits;
+};
+static PromptShape prompt_shape(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t group) {
+  PromptShape p;
+  p.rt = 2;
+  p.tiles = tokens * group / prompt_rows<2>() + seqs;
+  int64_t room = 2 * (int64_t)cu_count();
+  if (p.tiles * kv_heads < room) {
+    p.rt = 1;
+    p.tiles = tokens * group / prompt_rows<1>() + seqs;
+    room = (dim == 64 ? 3 : 2) * (int64_t)cu_count();
+  }
+  const int64_t z = (room + p.tiles * kv_heads / 2) / (p.tiles * kv_heads);  // the nearest (the tiles are a bound)
+  p.splits = (int32_t)(z < 1 ? 1 : z > 32 ? 32 : z);
+  return p;
 }
 
 // Enough for any type and any table.
@@ -1244,9 +1280,8 @@ uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t t
   const int32_t group = q_heads / kv_heads;
   const int rt = row_tiles(seqs, tokens, group);
   if (rt) return (uint64_t)split_blocks(false, rt) * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
-  const int64_t tiles = prompt_tiles(seqs, tokens, group);
-  const int32_t splits = prompt_splits(tiles, kv_heads);
-  return splits == 1 ? 0 : (uint64_t)tiles * kv_heads * splits * PR_ROWS * (dim + 2) * sizeof(float);
+  const PromptShape p = prompt_shape(kv_heads, dim, seqs, tokens, group);
+  return p.splits == 1 ? 0 : (uint64_t)p.tiles * kv_heads * p.splits * (64 * p.rt) * (dim + 2) * sizeof(float);
 }
 
 template <int DT, int FMT, int D, int RT>
@@ -1274,22 +1309,26 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, int FMT, int D>
-static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
-  const int64_t tiles = prompt_tiles(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads);
-  const int32_t splits = prompt_splits(tiles, a.kv_heads);
+template <int DT, int FMT, int D, int RT>
+static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream_t s) {
   float* parts = static_cast<float*>(a.ws);
   const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
-  const dim3 grid((unsigned)a.kv_heads, (unsigned)tiles, (unsigned)splits);
+  const dim3 grid((unsigned)a.kv_heads, (unsigned)p.tiles, (unsigned)p.splits);
   if (a.page_tokens >= PR_TILE)
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true>), grid, dim3(AT_T), 0, s, a, parts, splits, out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT>), grid, dim3(AT_T), 0, s, a, parts, p.splits, out_vec);
   else
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false>), grid, dim3(AT_T), 0, s, a, parts, splits, out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT>), grid, dim3(AT_T), 0, s, a, parts, p.splits, out_vec);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL((k_attend_prompt_join<DT, D>), dim3((unsigned)a.kv_heads, (unsigned)(tiles * PR_ROWS / 8)), dim3(AT_T),
-                     0, s, a, parts, splits);
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL((k_attend_prompt_join<DT, D, RT>), dim3((unsigned)a.kv_heads, (unsigned)(p.tiles * prompt_rows<RT>() / 8)),
+                     dim3(AT_T), 0, s, a, parts, p.splits);
   return hipGetLastError();
+}
+
+template <int DT, int FMT, int D>
+static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
+  const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads);
+  return p.rt == 1 ? prompt_rt<DT, FMT, D, 1>(a, p, s) : prompt_rt<DT, FMT, D, 2>(a, p, s);
 }
 
 template <int DT, int FMT, int D>
