@@ -362,12 +362,11 @@ __global__ __launch_bounds__(64 * NW, DT == EFFORT_F32 || RT == 2 ? 2 : 3) void 
                      (int64_t)(head * group + r - i * group) * D + g * 16;
       float x[KS][8], top = 0.0f;
 #pragma unroll
+      for (int k = 0; k < KS; ++k) load_n<8>(src + (k >> 1) * 64 + (k & 1) * 8, a.q_vec != 0, x[k]);
+#pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[k][e] = (float)src[(k >> 1) * 64 + (k & 1) * 8 + e];
-          top = fmaxf(top, fabsf(x[k][e]));
-        }
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
       const float by = power_of_row(max_of_row(top));
       f[rt] = fabsf(a.scale) * kLog2e / by;
       const float mul = a.scale < 0.0f ? -by : by;
@@ -963,12 +962,11 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
     const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
     float x[KS][8], top = 0.0f;
 #pragma unroll
+    for (int k = 0; k < KS; ++k) load_n<8>(src + (k * 4 + g) * 8, a.q_vec != 0, x[k]);
+#pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[k][e] = (float)src[(k * 4 + g) * 8 + e];
-        top = fmaxf(top, fabsf(x[k][e]));
-      }
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
     // the scale's sign goes into q: what is left of it keeps the scores' order
     const float by = power_of_row(max_of_row(top));
     f[rt] = fabsf(a.scale) * kLog2e / by;
@@ -1174,35 +1172,46 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
     if (step + 1 < step1) one_step(step + 1, 1, odd, even);
   }
 
-  // rows of the result: element (g * 4 + r) * ND + d of row j
+  // Rows of the result: a lane has the elements (g * 4 + r) * ND + d of row j.
+  // They go through LDS, 16 rows of a wave at a time, so that memory sees whole
+  // rows: stored from here, 8 bytes of 64 places at a time, they cost as much as
+  // a prompt's first hundreds of tokens.
+  float* rowbuf = reinterpret_cast<float*>(wave < 2 ? s_k[wave] : s_v[wave - 2]);  // 16 rows of D floats a wave
+  static_assert(sizeof(s_k[0]) >= 16 * D * sizeof(float), "a buffer holds a tile of rows");
+  float* mine = parts + (((int64_t)bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float sum = sum_of_row(l[rt]);
-    const int r0 = wave * WROWS + rt * 16 + j;
-    if (r0 >= rows) continue;
-    if (splits == 1) {
-      const int row = row0 + r0, tok = row / group;
-      T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
-      const float by = sum == 0.0f ? 0.0f : unit / sum;
+    const int r0 = wave * WROWS + rt * 16;
+    const float by = splits > 1 ? unit : sum == 0.0f ? 0.0f : unit / sum;
+    if (splits > 1 && g == 0 && r0 + j < rows) {
+      mine[PR_ROWS * D + r0 + j] = m[rt];
+      mine[PR_ROWS * D + PR_ROWS + r0 + j] = sum;
+    }
+    // 16-byte pieces, exchanged by the row so that neighbouring rows fall on different banks
+    auto piece = [&](int row, int x) { return row * D + ((x ^ (row & 7)) << 2); };
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int x = 0; x < ND; x += 4) {
-          const float y[4] = {o[rt][x][r] * by, o[rt][x + 1][r] * by, o[rt][x + 2][r] * by, o[rt][x + 3][r] * by};
-          store_n<4>(out + (g * 4 + r) * ND + x, out_vec != 0, y);
-        }
-    } else {
-      float* mine = parts + (((int64_t)bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
-      if (g == 0) {
-        mine[PR_ROWS * D + r0] = m[rt];
-        mine[PR_ROWS * D + PR_ROWS + r0] = sum;
+      for (int x = 0; x < ND / 4; ++x)
+        *reinterpret_cast<f4*>(rowbuf + piece(j, (g * 4 + r) * (ND / 4) + x)) =
+            f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]} * by;
+    __builtin_amdgcn_wave_barrier();
+    constexpr int LANES = D / 4, STEP_ROWS = 64 / LANES;  // lanes of a row
+#pragma unroll
+    for (int i = 0; i < 16; i += STEP_ROWS) {
+      const int r = i + lane / LANES, x = lane % LANES;
+      const f4 y = *reinterpret_cast<const f4*>(rowbuf + piece(r, x));
+      if (r0 + r >= rows) continue;
+      if (splits > 1) {
+        *reinterpret_cast<f4*>(mine + (r0 + r) * D + x * 4) = y;
+      } else {
+        const int row = row0 + r0 + r, tok = row / group;
+        T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
+        const float v[4] = {y[0], y[1], y[2], y[3]};
+        store_n<4>(out + x * 4, out_vec != 0, v);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int x = 0; x < ND / 4; ++x)
-          *reinterpret_cast<f4*>(mine + r0 * D + (g * 4 + r) * ND + x * 4) =
-              f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]} * unit;
     }
   }
 }

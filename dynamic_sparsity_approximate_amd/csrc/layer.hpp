@@ -38,6 +38,7 @@ struct AttendArgs {
   const float *ks, *vs;
   float scale;
   int32_t window, q_heads, kv_heads, dim, page_tokens, format;
+  int32_t q_vec;  // q's rows are aligned to 8 elements
   void* ws;
 };
 

@@ -161,6 +161,7 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
   a.dim = cache->head_dim;
   a.page_tokens = cache->page_tokens;
   a.format = cache->format;
+  a.q_vec = aligned(q_dev, 8 * es) && q_stride % 8 == 0;
   a.ws = ws_dev;
   return status_of(launch_attend(a, dtype, static_cast<hipStream_t>(stream)));
 }
