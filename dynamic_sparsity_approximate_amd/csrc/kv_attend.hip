@@ -812,10 +812,12 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
     }
   };
 
-  // page of the step at t, or of its sub-tile lane & 3; -1: none
+  // page of the step at t, or of its sub-tile lane & 3; -1: none, or behind the
+  // block's last step
+  const int32_t stop = lo + step1 * PR_TILE < hi ? lo + step1 * PR_TILE : hi;
   auto page_at = [&](int32_t t) {
     const int32_t tok = ONE ? t : t + 16 * (lane & 3);
-    return tok < hi ? table[tok >> shift] : -1;
+    return tok < stop ? table[tok >> shift] : -1;
   };
   const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
   const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
@@ -935,11 +937,11 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
   };
   Flight even, odd;  // of the steps step0, step0 + 2, ... and the others
   int32_t pages2 = -1;
+  // (Behind the last step it reads page 0: with a branch around the loads, the
+  // next wait for older ones would wait for these.)
   auto fetch_at = [&](int32_t step, int32_t pages, Flight& to) {
-    if (step < step1) {
-      fetch(lo + step * PR_TILE, pages, &to.st, &to.ks, &to.vs);
-      to.ok = there(pages);
-    }
+    fetch(lo + step * PR_TILE, pages, &to.st, &to.ks, &to.vs);
+    to.ok = there(pages);
   };
   even.ks = even.vs = even.ok = odd.ks = odd.vs = odd.ok = 0;
   if (step0 < step1) {
