@@ -33,74 +33,85 @@ hipError_t launch_rope_table(double base, int64_t rows, int32_t rot, float* tabl
 
 // ---------------------------------------------------------------- append
 
-// Four pairs of a head: where their elements are.  With `pairs` side by side
-// (interleaved, or nothing to rotate) the chunk is 8 elements from `a`; else 4
-// from `a` and 4 from `b`.
+// Pairs of a chunk (seven bf16 prompts of about 1500 tokens, 32 and 8 heads: 50 us; 8 pairs take 61 to 73).
+constexpr int CP = 4;
+
+// CP pairs of a head: where their elements are.  With the pairs side by side
+// (interleaved, or nothing to rotate) the chunk is 2 CP elements from `a`; else
+// CP from `a` and CP from `b`.
 struct Chunk {
   int a, b, pair;  // pair: of the table, when rotated
   bool rotated, side;
 };
 
-__device__ inline Chunk chunk_of(int c, int dim, int rot, bool interleaved) {
+__device__ inline Chunk chunk_of(int c, int rot, bool interleaved) {
   Chunk k;
-  const int p = 4 * c;
+  const int p = CP * c;
   k.rotated = p < rot / 2;
   k.pair = p;
   k.side = interleaved || !k.rotated;
-  if (interleaved) {
-    k.a = 2 * p;
-  } else if (k.rotated) {
-    k.a = p;
-  } else {
-    k.a = rot + 2 * (p - rot / 2);
-  }
-  k.b = k.side ? k.a + 4 : p + rot / 2;
+  k.a = k.side ? 2 * p : p;
+  k.b = k.side ? k.a + CP : p + rot / 2;
   return k;
 }
 
-// The chunk's elements in the order (first of a pair, second) x 4.
+// The chunk's elements in memory's order: two halves, or (`together`, a choice
+// of the whole block) one piece.  `vec`: elements that rows are aligned to.
 template <typename T>
-__device__ inline void load_chunk(const T* row, const Chunk& k, bool interleaved, bool vec, float* x) {
-  float a[4], b[4];
-  load_n<4>(row + k.a, vec, a);
-  load_n<4>(row + k.b, vec, b);
-  if (k.rotated && interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = i < 2 ? a[2 * i] : b[2 * i - 4];
-      x[4 + i] = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-    }
+__device__ inline void load_chunk(const T* row, const Chunk& k, bool together, int vec, float* y) {
+  if (together) {
+    load_n<2 * CP>(row + k.a, true, y);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = a[i];
-      x[4 + i] = b[i];
-    }
+    load_n<CP>(row + k.a, vec >= CP, y);
+    load_n<CP>(row + k.b, vec >= CP, y + CP);
   }
 }
 
-// x (double) to the float that rounds to the same code: towards zero, with the
-// last bit set if anything was cut off.  A later rounding to fewer bits, ties
-// to even, then gives what rounding x at once would.
+// ... the first of each pair and then the second ...
+__device__ inline void from_order(bool pairs, float* y) {
+  if (!pairs) return;
+  const float a[2 * CP] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+#pragma unroll
+  for (int i = 0; i < CP; ++i) {
+    y[i] = a[2 * i];
+    y[CP + i] = a[2 * i + 1];
+  }
+}
+
+// ... and back into their order in memory.
+__device__ inline void to_order(const float* x, bool pairs, float* y) {
+  if (pairs) {
+#pragma unroll
+    for (int i = 0; i < CP; ++i) {
+      y[2 * i] = x[i];
+      y[2 * i + 1] = x[CP + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * CP; ++i) y[i] = x[i];
+  }
+}
+
+// x (double) to the float that rounds to the same code: the nearest one, and if
+// that is inexact and its last bit 0, the neighbour on x's side (its last bit is
+// 1).  A later rounding to fewer bits, ties to even, then gives what rounding x
+// at once would: only an exact value can still look like a tie.
 __device__ inline float round_to_odd(double x) {
-  const float f = __double2float_rz(x);
-  return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+  const float f = (float)x;
+  const double rest = x - (double)f;  // exact; NaN for an infinite x, -+inf where f overflowed
+  const int32_t bits = __float_as_int(f);
+  const int32_t step = f == 0.0f || (rest > 0.0) == (f > 0.0f) ? 1 : -1;
+  return (rest > 0.0 || rest < 0.0) && (bits & 1) == 0 ? __int_as_float(bits + step) : f;
 }
 
 // The chunk rotated; a key's products and sum are exact to 2^-53, so that its
 // code is the nearest one even where the sum nearly cancels.
-__device__ inline void rotate_exact(const float* x, const float2* cs, bool rotated, double* y) {
+__device__ inline void rotate_exact(const float* x, const float2* cs, double* y) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const double a = x[i], b = x[4 + i];
-    if (rotated) {
-      const double c = cs[i].x, s = cs[i].y;
-      y[i] = __builtin_fma(a, c, -(b * s));
-      y[4 + i] = __builtin_fma(b, c, a * s);
-    } else {
-      y[i] = a;
-      y[4 + i] = b;
-    }
+  for (int i = 0; i < CP; ++i) {
+    const double a = x[i], b = x[CP + i], c = cs[i].x, s = cs[i].y;
+    y[i] = __builtin_fma(a, c, -(b * s));
+    y[CP + i] = __builtin_fma(b, c, a * s);
   }
 }
 
@@ -125,23 +136,25 @@ __device__ inline uint32_t encode4(float y0, float y1, float y2, float y3) {
 }
 
 // The rotation of one chunk's queries, rounded once in fp32.
-__device__ inline void rotate_near(const float* x, const float2* cs, bool rotated, float* y) {
+__device__ inline void rotate_near(const float* x, const float2* cs, float* y) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    y[j] = rotated ? __builtin_fmaf(x[j], cs[j].x, -(x[4 + j] * cs[j].y)) : x[j];
-    y[4 + j] = rotated ? __builtin_fmaf(x[4 + j], cs[j].x, x[j] * cs[j].y) : x[4 + j];
+  for (int j = 0; j < CP; ++j) {
+    y[j] = __builtin_fmaf(x[j], cs[j].x, -(x[CP + j] * cs[j].y));
+    y[CP + j] = __builtin_fmaf(x[CP + j], cs[j].x, x[j] * cs[j].y);
   }
 }
 
-__device__ inline void load_rope(const float2* row, const Chunk& k, float2* cs) {
+// A chunk's cosines and sines.
+__device__ inline void load_rope(const float2* at, float2* cs) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) cs[j] = k.rotated ? row[k.pair + j] : make_float2(1.0f, 0.0f);
+  for (int j = 0; j < CP; ++j) cs[j] = at[j];
 }
 
 constexpr int AP_QH = 4;  // query heads of a thread: they share its cosines and sines
 
-// One block per (page of a sequence, head, keys or values), then blocks of 256
-// (token, 4 heads, chunk) items of the queries.  A page's block keeps its new
+// One block per (page of a sequence, head, keys or values), then blocks of four
+// waves of the queries: a page's block waits most of its time, so those start
+// first (spread evenly among the queries' blocks: 54.3 us instead of 50.1).  A page's block keeps its new
 // elements in registers between the search for the largest magnitude and the
 // codes: IT chunks a thread, up to a whole page.  A prompt is bound by its
 // bytes (and read once), a single token by the chain starts -> page -> scale;
@@ -151,16 +164,20 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
                                                  int32_t kv_vec, int32_t q_vec) {
   typedef typename ElemOf<DT>::T T;
   const int tid = (int)threadIdx.x;
-  const int dim = a.dim, cpr = dim / 8;
+  const int dim = a.dim, cpr_log = __builtin_ctz(dim / (2 * CP));  // chunks of a row: a power of two
   const bool inter = a.interleaved != 0;
   const float2* rope = reinterpret_cast<const float2*>(a.rope);
   const int half = a.rot / 2;
-  const int64_t kv_blocks = (int64_t)units * a.kv_heads * 2;
+  const uint32_t kv_blocks = (uint32_t)units * (uint32_t)a.kv_heads * 2;
 
-  if ((int64_t)blockIdx.x >= kv_blocks) {
-    const int64_t i = ((int64_t)blockIdx.x - kv_blocks) * AP_T + tid;
-    const int32_t per = (a.q_heads + AP_QH - 1) / AP_QH * cpr;
-    const int64_t tok = i / per;
+  if (blockIdx.x >= kv_blocks) {
+    // a wave has 64 / chunks of a row * AP_QH heads of one token: all that leads
+    // to its place is scalar (looked up by every lane, it took as long as the rest)
+    const uint32_t slots = 64u >> cpr_log, per_wave = slots * AP_QH;
+    const uint32_t parts = ((uint32_t)a.q_heads + per_wave - 1) / per_wave;  // waves of a token
+    const uint32_t w = (blockIdx.x - kv_blocks) * (AP_T / 64) +
+                       (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
+    const int32_t tok = (int32_t)(w / parts);
     if (tok >= a.b.tokens) return;
     int lo = 0, hi = a.b.seqs;  // the last sequence that starts at or before tok
     while (hi - lo > 1) {
@@ -171,35 +188,50 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
     if (tok < s0 || tok >= s1) return;
     const int64_t pos = (int64_t)a.b.lens[lo] - (s1 - s0) + (tok - s0);
     if (pos < 0 || pos >= (int64_t)a.b.max_pages * a.page_tokens) return;
-    const int r = (int)(i - tok * per), head = r / cpr * AP_QH;
-    const Chunk k = chunk_of(r % cpr, dim, a.rot, inter);
-    float2 cs[4];
-    load_rope(rope + pos * half, k, cs);
-    const T* row = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * dim;
-    T* out = static_cast<T*>(a.q_out) + tok * a.q_out_stride + (int64_t)head * dim;
-    float x[AP_QH][8];
+    const uint32_t lane = (uint32_t)tid & 63;
+    const uint32_t head0 = (w - (uint32_t)tok * parts) * per_wave + (lane >> cpr_log);
+    const Chunk k = chunk_of((int)(lane & ((1u << cpr_log) - 1)), a.rot, inter);
+    const T* row = static_cast<const T*>(a.q) + (int64_t)tok * a.q_stride;
+    T* out = static_cast<T*>(a.q_out) + (int64_t)tok * a.q_out_stride;
+    auto at = [&](int h) { return (head0 + (uint32_t)h * slots) * (uint32_t)dim; };  // the h-th of the lane's heads
+    auto has = [&](int h) { return head0 + (uint32_t)h * slots < (uint32_t)a.q_heads; };
+    const bool together = (inter || a.rot == 0) && q_vec >= 2 * CP;
+    float x[AP_QH][2 * CP];
+    if (together) {
 #pragma unroll
-    for (int h = 0; h < AP_QH; ++h)
-      if (head + h < a.q_heads) load_chunk(row + h * dim, k, inter, q_vec != 0, x[h]);
+      for (int h = 0; h < AP_QH; ++h)
+        if (has(h)) load_chunk(row + at(h), k, true, q_vec, x[h]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < AP_QH; ++h)
+        if (has(h)) load_chunk(row + at(h), k, false, q_vec, x[h]);
+    }
+    float2 cs[CP];
+    if (k.rotated) load_rope(rope + pos * half + k.pair, cs);
 #pragma unroll
     for (int h = 0; h < AP_QH; ++h) {
-      if (head + h >= a.q_heads) break;
-      float y[8];
-      rotate_near(x[h], cs, k.rotated, y);
-      if (k.rotated && inter) {
-        const float z[8] = {y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]};
-        store_n<4>(out + h * dim + k.a, q_vec != 0, z);
-        store_n<4>(out + h * dim + k.b, q_vec != 0, z + 4);
+      if (!has(h)) break;
+      float y[2 * CP], z[2 * CP];
+      from_order(k.rotated && inter, x[h]);
+      if (k.rotated) {
+        rotate_near(x[h], cs, y);
       } else {
-        store_n<4>(out + h * dim + k.a, q_vec != 0, y);
-        store_n<4>(out + h * dim + k.b, q_vec != 0, y + 4);
+#pragma unroll
+        for (int j = 0; j < 2 * CP; ++j) y[j] = x[h][j];
+      }
+      to_order(y, k.rotated && inter, z);
+      if (together) {
+        store_n<2 * CP>(out + at(h) + k.a, true, z);
+      } else {
+        store_n<CP>(out + at(h) + k.a, q_vec >= CP, z);
+        store_n<CP>(out + at(h) + k.b, q_vec >= CP, z + CP);
       }
     }
     return;
   }
 
-  const int32_t ph = (int32_t)((int64_t)blockIdx.x / units);
-  const int32_t u = (int32_t)((int64_t)blockIdx.x - (int64_t)ph * units);
+  const int32_t ph = (int32_t)(blockIdx.x / (uint32_t)units);
+  const int32_t u = (int32_t)(blockIdx.x - (uint32_t)ph * (uint32_t)units);
   const int head = ph >> 1;
   const bool is_k = (ph & 1) == 0;
   __shared__ int s_seq;
@@ -235,14 +267,22 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   const int64_t tok0 = t0 + (lo - pos0);
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const T* rows = static_cast<const T*>(is_k ? a.k : a.v) + tok0 * stride + (int64_t)head * dim;
-  const int rot = is_k ? a.rot : 0, items = m * cpr;
-  const bool side = is_k && inter;
+  const int rot = is_k ? a.rot : 0, items = m << cpr_log, in_row = (1 << cpr_log) - 1;
+  const bool side = is_k && inter, together = (side || rot == 0) && kv_vec >= 2 * CP;
 
-  float y[IT][8];  // the new elements, first rotated (round_to_odd), then coded
+  float y[IT][2 * CP];  // the new elements, first rotated (round_to_odd), then coded
+  if (together) {
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int i = tid + it * AP_T, r = i / cpr;
-    if (i < items) load_chunk(rows + r * stride, chunk_of(i - r * cpr, dim, rot, side), side, kv_vec != 0, y[it]);
+    for (int it = 0; it < IT; ++it) {
+      const int i = tid + it * AP_T, r = i >> cpr_log;
+      if (i < items) load_chunk(rows + r * stride, chunk_of(i & in_row, rot, side), true, kv_vec, y[it]);
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int i = tid + it * AP_T, r = i >> cpr_log;
+      if (i < items) load_chunk(rows + r * stride, chunk_of(i & in_row, rot, side), false, kv_vec, y[it]);
+    }
   }
   if (page < 0 || page >= a.b.pages) return;
   uint8_t* codes = (is_k ? a.kc : a.vc) + ((int64_t)page * a.kv_heads + head) * pt * dim;
@@ -252,19 +292,20 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   uint32_t top = 0;  // as bits: a NaN is above an infinity, that above every number
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int i = tid + it * AP_T, r = i / cpr;
+    const int i = tid + it * AP_T, r = i >> cpr_log;
     if (i >= items) continue;
-    const Chunk k = chunk_of(i - r * cpr, dim, rot, side);
+    const Chunk k = chunk_of(i & in_row, rot, side);
     if (k.rotated) {
-      float2 cs[4];
-      double z[8];
-      load_rope(rope + (lo + r) * half, k, cs);
-      rotate_exact(y[it], cs, true, z);
+      float2 cs[CP];
+      double z[2 * CP];
+      from_order(side, y[it]);
+      load_rope(rope + (lo + r) * half + k.pair, cs);
+      rotate_exact(y[it], cs, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[it][j] = round_to_odd(z[j]);
+      for (int j = 0; j < 2 * CP; ++j) y[it][j] = round_to_odd(z[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 2 * CP; ++j) {
       const uint32_t b = __float_as_uint(y[it][j]) & 0x7FFFFFFFu;
       top = b > top ? b : top;
     }
@@ -305,36 +346,43 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   const float per = (float)(1.0 / (double)now);
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int i = tid + it * AP_T, r = i / cpr;
+    const int i = tid + it * AP_T, r = i >> cpr_log;
     if (i >= items) continue;
-    const Chunk k = chunk_of(i - r * cpr, dim, rot, side);
-    float* z = y[it];
+    const Chunk k = chunk_of(i & in_row, rot, side);
     if (pow2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] *= per;
+      for (int j = 0; j < 2 * CP; ++j) y[it][j] *= per;
     } else if (!bad) {
-      float x[8];
-      float2 cs[4];
-      double d[8];
-      load_chunk(rows + r * stride, k, side, kv_vec != 0, x);
-      load_rope(rope + (lo + r) * half, k, cs);
-      rotate_exact(x, cs, k.rotated, d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = round_to_odd(d[j] / (double)now);
-    }
-    uint32_t c[2] = {0, 0};
-    if (!bad) {
-      if (k.rotated && side) {
-        c[0] = encode4<FMT>(z[0], z[4], z[1], z[5]);
-        c[1] = encode4<FMT>(z[2], z[6], z[3], z[7]);
+      float x[2 * CP];
+      load_chunk(rows + r * stride, k, false, kv_vec, x);
+      from_order(k.rotated && side, x);
+      double d[2 * CP];
+      if (k.rotated) {
+        float2 cs[CP];
+        load_rope(rope + (lo + r) * half + k.pair, cs);
+        rotate_exact(x, cs, d);
       } else {
-        c[0] = encode4<FMT>(z[0], z[1], z[2], z[3]);
-        c[1] = encode4<FMT>(z[4], z[5], z[6], z[7]);
+#pragma unroll
+        for (int j = 0; j < 2 * CP; ++j) d[j] = x[j];
       }
+#pragma unroll
+      for (int j = 0; j < 2 * CP; ++j) y[it][j] = round_to_odd(d[j] / (double)now);
     }
+    Vec<CP / 4, uint32_t> c[2];
+    float z[2 * CP];
+    to_order(y[it], k.rotated && side, z);
+#pragma unroll
+    for (int j = 0; j < CP / 2; ++j)
+      c[j / (CP / 4)].e[j % (CP / 4)] =
+          bad ? 0u : encode4<FMT>(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
     uint8_t* out = codes + (slot0 + r) * dim;
-    *reinterpret_cast<uint32_t*>(out + k.a) = c[0];
-    *reinterpret_cast<uint32_t*>(out + k.b) = c[1];
+    typedef Vec<CP / 4, uint32_t> Half;
+    if (k.side) {
+      *reinterpret_cast<Vec<2, Half>*>(out + k.a) = Vec<2, Half>{{c[0], c[1]}};
+    } else {
+      *reinterpret_cast<Half*>(out + k.a) = c[0];
+      *reinterpret_cast<Half*>(out + k.b) = c[1];
+    }
   }
 }
 
@@ -345,11 +393,17 @@ static hipError_t append_it(const AppendArgs& a, hipStream_t s) {
   const int64_t by_page = a.b.tokens / a.page_tokens + 2 * (int64_t)a.b.seqs;
   const int per_token = a.b.tokens <= by_page ? 1 : 0;
   const int64_t units = per_token ? a.b.tokens : by_page;
-  const int64_t q_items = (int64_t)a.b.tokens * ((a.q_heads + AP_QH - 1) / AP_QH) * (a.dim / 8);
-  const int64_t blocks = units * a.kv_heads * 2 + (q_items + AP_T - 1) / AP_T;
-  if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-  const int kv_vec = rows_aligned<4, T>(a.k, a.k_stride) && rows_aligned<4, T>(a.v, a.v_stride);
-  const int q_vec = a.q_heads && rows_aligned<4, T>(a.q, a.q_stride) && rows_aligned<4, T>(a.q_out, a.q_out_stride);
+  const int64_t per_wave = 64 / (a.dim / (2 * CP)) * AP_QH;  // heads
+  const int64_t q_waves = (int64_t)a.b.tokens * ((a.q_heads + per_wave - 1) / per_wave);
+  const int64_t kv_blocks = units * a.kv_heads * 2, q_blocks = (q_waves + AP_T / 64 - 1) / (AP_T / 64);
+  const int64_t blocks = kv_blocks + q_blocks;
+  if (blocks > 0x3FFFFFFFll) return hipErrorInvalidValue;  // so that waves count in 32 bits
+  auto vec = [](const void* p, int64_t stride) {
+    return rows_aligned<2 * CP, T>(p, stride) ? 2 * CP : rows_aligned<CP, T>(p, stride) ? CP : 1;
+  };
+  auto less = [](int x, int y) { return x < y ? x : y; };
+  const int kv_vec = less(vec(a.k, a.k_stride), vec(a.v, a.v_stride));
+  const int q_vec = a.q_heads ? less(vec(a.q, a.q_stride), vec(a.q_out, a.q_out_stride)) : 1;
   hipLaunchKernelGGL((k_append<DT, FMT, IT>), dim3((unsigned)blocks), dim3(AP_T), 0, s, a, (int32_t)units,
                      per_token, kv_vec, q_vec);
   return hipGetLastError();
