@@ -6,7 +6,8 @@ knob; the author runs Mistral and Mixtral through it).  These classes only
 sequence calls into libeffort and own the intermediate buffers; every step of
 the arithmetic, the glue included (silu(h1) * h3, the gated expert sum), runs
 in the library's kernels.  A caller that repeats a chain captures `enqueue`
-into a HIP graph.
+into a HIP graph.  DecodeStep takes the attention's results from outside;
+DecoderStep runs whole layers over a paged cache.
 """
 from __future__ import annotations
 
@@ -149,6 +150,113 @@ class DecodeStep:
             L["w2"].matvec(o["g"], e["w2"], o["w2"], main, record=rk((l, "w2")))
         self.head.matvec(self.head_in, _effort_of(effort, None, "head"), self.logits, main,
                          record=rk((None, "head")))
+
+
+class DecoderStep:
+    """One step of whole decoder layers for the new tokens of a batch of
+    sequences (a KVBatch): attention over the paged 8-bit cache included, so
+    that nothing but the embeddings comes from outside.
+
+    `layers` is a list of dicts role -> EffortMatrix with the roles of
+    LAYER_ROLES, `head` the output projection, `caches` one KVCache per layer,
+    `norms` one (before attention, before the feed-forward block) pair of norm
+    weights per layer and `head_norm` the one before the head.  `x` [tokens][dim]
+    holds the embeddings of the new tokens in the order of the batch, `rope` is a
+    table of rope_table (None: no rotation).  Per layer, with the residual
+    stream r (r = x at first):
+      h = norm(r); q, k, v = h Wq, h Wk, h Wv; k and v appended, q and k rotated
+      r += attend(q) Wo; h = norm(r); r += (silu(h W1) * h W3) W2
+    and logits = norm(r) Whead.  `out[l]` keeps what layer l computed.  A matrix
+    needs `batch` >= tokens; a single row goes through the multi-matrix calls.
+
+    The kernels read x, the page table, the lengths and the starts at every
+    step: a captured step is replayed after the caller has updated them in
+    place.  Rows that no sequence has do not touch the cache or other rows;
+    their logits mean nothing.
+    """
+
+    def __init__(self, layers, head, x, caches, batch, norms, head_norm, rope=None, interleaved: bool = False,
+                 window: int = 0, eps: float = 1e-5):
+        import torch
+
+        from .device import EffortGroup
+
+        if len(layers) != len(caches) or len(layers) != len(norms):
+            raise ValueError("one cache and one pair of norm weights per layer")
+        if x.dim() != 2 or x.dtype != torch.float32 or not x.is_contiguous() or x.shape[0] < 1:
+            raise ValueError("x must be a contiguous float32 tensor [tokens][dim]")
+        tokens, dim = x.shape
+        for L, c in zip(layers, caches):
+            qd, kd, hid, hd = L["wq"].out_dim, c.kv_heads * c.head_dim, L["w1"].out_dim, c.head_dim
+            if qd % kd or any((L[r].in_dim, L[r].out_dim) != io for r, io in (
+                    ("wq", (dim, qd)), ("wk", (dim, kd)), ("wv", (dim, kd)), ("wo", (qd, dim)), ("w1", (dim, hid)),
+                    ("w3", (dim, hid)), ("w2", (hid, dim)))):
+                raise ValueError("a layer's matrices do not fit x, its cache or each other")
+        if head.in_dim != dim:
+            raise ValueError("the head does not fit x")
+        short = [m.batch for m in [head] + [L[r] for L in layers for r in LAYER_ROLES] if m.batch < tokens]
+        if short:
+            raise ValueError("a matrix was made for %d vectors a call, the step has %d rows" % (short[0], tokens))
+        self.layers, self.head, self.x = layers, head, x
+        self.caches, self.batch, self.norms, self.head_norm = caches, batch, norms, head_norm
+        self.rope, self.interleaved, self.window, self.eps = rope, interleaved, window, eps
+        # zeros: rows of no sequence are never written by the attention
+        mk = lambda n: torch.zeros((tokens, n), dtype=torch.float32, device=x.device)  # noqa: E731
+        self.out = []
+        for L in layers:
+            o = {r: mk(L[r].out_dim) for r in LAYER_ROLES}
+            o.update(hq=mk(dim), q=mk(L["wq"].out_dim), a=mk(L["wq"].out_dim), r=mk(dim), hf=mk(dim),
+                     g=mk(L["w1"].out_dim))
+            self.out.append(o)
+        self.r, self.h = mk(dim), mk(dim)  # after the last layer: the stream, and its norm
+        self.logits = mk(head.out_dim)
+        self.groups = ([(EffortGroup([L["wq"], L["wk"], L["wv"]]), EffortGroup([L["w1"], L["w3"]]))
+                        for L in layers] if tokens == 1 else None)
+
+    def enqueue(self, effort, stream=None, record=None):
+        """Issue the step on `stream` (None: torch's current stream).  `effort`
+        as in DecodeStep.  With `record` (a Recorder; one row only), every matvec
+        records its parity outputs under (layer, role), the head under (None,
+        "head")."""
+        import torch
+
+        from .layer import norm_residual
+
+        tokens = self.x.shape[0]
+        if record is not None and tokens != 1:
+            raise ValueError("a step of %d rows cannot be recorded" % tokens)
+        main = stream if stream is not None else torch.cuda.current_stream(self.x.device)
+
+        def times(l, roles, x, ys, group=None):
+            mats = [self.layers[l][r] if l is not None else self.head for r in roles]
+            keys = [(l, r) for r in roles]
+            es = [_effort_of(effort, *k) for k in keys]
+            if tokens > 1:
+                for m, e, y in zip(mats, es, ys):
+                    m.matvec_batched(x, e, y, main)
+            elif group is not None:
+                group.matvec(x[0], es, [y[0] for y in ys], main, record=None if record is None else (record, keys))
+            else:
+                mats[0].matvec(x[0], es[0], ys[0][0], main, record=None if record is None else (record, keys[0]))
+
+        r, add = None, self.x
+        for l, (c, (before_attn, before_ffn)) in enumerate(zip(self.caches, self.norms)):
+            o, (qkv, gu) = self.out[l], self.groups[l] if self.groups else (None, None)
+            heads = lambda t: t.view(tokens, -1, c.head_dim)  # noqa: B023,E731
+            norm_residual(add, r, pre_w=before_attn, eps=self.eps, resid_out=self.r, out=o["hq"], stream=main)
+            times(l, ("wq", "wk", "wv"), o["hq"], [o["wq"], o["wk"], o["wv"]], qkv)
+            c.append(self.batch, heads(o["wk"]), heads(o["wv"]), q=heads(o["wq"]), rope=self.rope,
+                     interleaved=self.interleaved, q_out=heads(o["q"]), stream=main)
+            c.attend(self.batch, heads(o["q"]), window=self.window, out=heads(o["a"]), stream=main)
+            times(l, ("wo",), o["a"], [o["wo"]])
+            norm_residual(o["wo"], self.r, pre_w=before_ffn, eps=self.eps, resid_out=o["r"], out=o["hf"], stream=main)
+            times(l, ("w1", "w3"), o["hf"], [o["w1"], o["w3"]], gu)
+            B.effort_silu_mul(o["w1"], o["w3"], o["g"].numel(), o["g"], main)
+            times(l, ("w2",), o["g"], [o["w2"]])
+            r, add = o["r"], o["w2"]
+        norm_residual(add, r, pre_w=self.head_norm, eps=self.eps, resid_out=self.r, out=self.h, stream=main)
+        times(None, ("head",), self.h, [self.logits])
+        return self.logits
 
 
 class DenseDecodeStep:
