@@ -231,8 +231,7 @@ __device__ inline int owner(const AttendArgs& a, const Plan& p, uint64_t c, int 
 // tables of so few tokens that joining would cost more than it saves.
 // `RT`: 16-row tiles of an item, `NW`: waves of a block.
 template <int DT, int FMT, int D, int RT, int NW, bool WHOLE>
-__global__ __launch_bounds__(64 * NW, DT == EFFORT_F32 || RT == 2 ? 2 : 3) void k_attend_split(AttendArgs a,
-                                                                                         float* parts) {
+__global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float* parts) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
   constexpr int KS = D / 32, ND = D / 16, ROWS = 16 * RT, LD = D + 4, THREADS = 64 * NW, STEP = NW * AT_TILE;
@@ -683,7 +682,9 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     return;
   }
   const uint64_t total = make_plan(a, group, ROWS, &s_plan), nb = total < nb32 ? total : nb32;
-  const uint64_t c0 = start_of_seq(a, s_plan, s, group, ROWS) + ((uint64_t)head * q.tiles + tile) * q.chunks, c1 = c0 + q.chunks - 1;
+  const uint64_t c0 = start_of_seq(a, s_plan, s, group, ROWS) +
+                      ((uint64_t)head * q.tiles + tile) * q.chunks;
+  const uint64_t c1 = c0 + q.chunks - 1;
   const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
   if (b0 == b1) return;
   const float* first = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
@@ -696,8 +697,8 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
 // ---------------------------------------------------------------- prompts
 
 // Rows of a block: RT 16-row tiles a wave.  Two for prompts that fill the chip;
-// one where there are not two such blocks a CU, for twice the blocks and (heads
-// of 64 elements) three of them on a CU.
+// one for shorter ones (prompt_shape), for twice the blocks and (heads of 64
+// elements) three of them on a CU.
 template <int RT>
 constexpr int prompt_rows() {
   return 16 * RT * AT_W;
@@ -742,7 +743,7 @@ struct Staged {
 // instructions a step beside 64 products, and they are its time.
 template <int DT, int FMT, int D, bool ONE, int RT>
 __global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 ? 2 : 3) : DT == EFFORT_F32 && D == 128 ? 1 : 2)
-void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec) {
+void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32;
   constexpr int KS = D / 32, ND = D / 16, SUB = PR_SUB, PR_ROWS = prompt_rows<RT>(), WROWS = 16 * RT;
@@ -751,8 +752,10 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens), head = (int)blockIdx.x;
-  const int64_t bt = (int64_t)gridDim.y - 1 - blockIdx.y;  // the last rows see most: they go first
+  const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens);
+  const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
+  const int head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
+  const int64_t bt = (int64_t)tiles - 1 - turn;  // the last rows see most: they go first
   auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
   if (tid == 0) s_seq = a.b.seqs;
   __syncthreads();
@@ -774,7 +777,7 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
   const int32_t from = from64 < to ? (int32_t)from64 : 0, hi = from64 < to ? (int32_t)to : 0;
   const int32_t lo = from & ~(PR_TILE - 1);
   const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
-  const int32_t z = (int32_t)blockIdx.z;
+  const int32_t z = (int32_t)blockIdx.y;
   const int32_t step0 = (int32_t)((int64_t)steps * z / splits), step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
   const int32_t* table = a.b.table + seq * a.b.table_stride;
 
@@ -913,13 +916,15 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
       }
     const int piece = v_q * 4 + v_g;
     s_v[buf][value_piece<D>(v_el, piece)] =
-        join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]), decode2<FMT, false>(e[3]));
+        join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]),
+              decode2<FMT, false>(e[3]));
     s_v[buf][value_piece<D>(v_el + 1, piece)] =
         join8(decode2<FMT, true>(e[0]), decode2<FMT, true>(e[1]), decode2<FMT, true>(e[2]), decode2<FMT, true>(e[3]));
     s_v[buf][value_piece<D>(v_el + 2, piece)] = join8(decode2<FMT, false>(e2[0]), decode2<FMT, false>(e2[1]),
                                                       decode2<FMT, false>(e2[2]), decode2<FMT, false>(e2[3]));
     s_v[buf][value_piece<D>(v_el + 3, piece)] =
-        join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]), decode2<FMT, true>(e2[3]));
+        join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]),
+              decode2<FMT, true>(e2[3]));
   };
   auto there = [&](int32_t pages) {  // bit per sub-tile
     const bool in = (uint32_t)pages < (uint32_t)a.b.pages;
@@ -1013,135 +1018,135 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
     const int passes = !ONE && v_hi > 0x1p10f * v_lo ? SUB : 1;
 #pragma unroll 1
     for (int pass = 0; pass < passes; ++pass) {
-    const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
-    // The fences keep the compiler from loading all pieces at once, for which
-    // there are no registers: those of one sub-tile are loaded while the one
-    // before is multiplied.
-    f4 sc[RT][SUB];
-    h8 kf[2][KS];
+      const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
+      // The fences keep the compiler from loading all pieces at once, for which
+      // there are no registers: those of one sub-tile are loaded while the one
+      // before is multiplied.
+      f4 sc[RT][SUB];
+      h8 kf[2][KS];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k]];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      if (u + 1 < SUB) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          kf[(u + 1) & 1][k] = s_k[buf][k_at[k] + (u + 1) * 16 * (D / 8)];
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], qh[rt][k], sc[rt][u], 0, 0, 0);
-          if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], ql[rt][k], sc[rt][u], 0, 0, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // scores are sc * c
-    float c[RT][SUB];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        c[rt][u] = ONE ? f[rt] * ks_lane : f[rt] * lane_of(ks_lane, u);
-    if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
-        // not to be compared outside this branch: most steps hide nothing
-        asm volatile("" : "+v"(high), "+v"(low));
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          sc[rt][u] *= c[rt][u];
-          c[rt][u] = 1.0f;
-          const int32_t high_u = here >> u & 1 ? high : -PR_TILE;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (16 * u + r > high_u || 16 * u + r <= low) sc[rt][u][r] = -INFINITY;
-        }
-      }
-    }
-    float ref[RT], top[RT];
-    bool over = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      top[rt] = -INFINITY;
+      for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k]];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        float x = max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]);
-        if (!ONE) x *= c[rt][u];
-        top[rt] = max_of(top[rt], x);
+        if (u + 1 < SUB) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            kf[(u + 1) & 1][k] = s_k[buf][k_at[k] + (u + 1) * 16 * (D / 8)];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], qh[rt][k], sc[rt][u], 0, 0, 0);
+            if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], ql[rt][k], sc[rt][u], 0, 0, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      top[rt] = max_of_row(ONE ? top[rt] * c[rt][0] : top[rt]);
-      over = over || top[rt] > m[rt] + kSlack;
-    }
-    if (__any(over)) {
+      // scores are sc * c
+      float c[RT][SUB];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const float mn = fmaxf(top[rt], m[rt]);
-        const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-        m[rt] = mn;
-        l[rt] *= alpha;
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
-      }
-    }
-    // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+        for (int rt = 0; rt < RT; ++rt)
+          c[rt][u] = ONE ? f[rt] * ks_lane : f[rt] * lane_of(ks_lane, u);
+      if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
-    if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
-    float up_lane = 0.0f, back_lane = 1.0f;
-    if (ONE) {
-      if (__float_as_uint(vs_lane) != now_vs) {  // another scale than the last step's
-        now_vs = __float_as_uint(vs_lane);
-        set_unit(vs_lane);
-        const float rel = vs_lane > 0.0f ? vs_lane * per_unit : 1.0f;
-        now_up = uniform(__builtin_amdgcn_logf(rel));
-        now_back = uniform(__builtin_amdgcn_rcpf(rel));
-      }
+        for (int rt = 0; rt < RT; ++rt) {
+          int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+          // not to be compared outside this branch: most steps hide nothing
+          asm volatile("" : "+v"(high), "+v"(low));
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) ref[rt] += now_up;
-    } else {
-      const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
-      set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
-      const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
-      up_lane = __builtin_amdgcn_logf(rel);
-      back_lane = __builtin_amdgcn_rcpf(rel);
-    }
-    float sum[RT];
+          for (int u = 0; u < SUB; ++u) {
+            sc[rt][u] *= c[rt][u];
+            c[rt][u] = 1.0f;
+            const int32_t high_u = here >> u & 1 ? high : -PR_TILE;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
-    h8 ph[RT][2], pl[RT][2];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const float up = ONE ? 0.0f : lane_of(up_lane, u), back = ONE ? 1.0f : lane_of(back_lane, u);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float w[4];
-        const float base = ONE ? ref[rt] : ref[rt] + up;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
-        if (ONE)
-          sum[rt] += (w[0] + w[1]) + (w[2] + w[3]);
-        else
-          l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int e = (u & 1) * 4 + r;
-          ph[rt][u >> 1][e] = (_Float16)w[r];
-          if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
+            for (int r = 0; r < 4; ++r)
+              if (16 * u + r > high_u || 16 * u + r <= low) sc[rt][u][r] = -INFINITY;
+          }
         }
       }
-    }
-    if (ONE) {
+      float ref[RT], top[RT];
+      bool over = false;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+      for (int rt = 0; rt < RT; ++rt) {
+        top[rt] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          float x = max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]);
+          if (!ONE) x *= c[rt][u];
+          top[rt] = max_of(top[rt], x);
+        }
+        top[rt] = max_of_row(ONE ? top[rt] * c[rt][0] : top[rt]);
+        over = over || top[rt] > m[rt] + kSlack;
+      }
+      if (__any(over)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const float mn = fmaxf(top[rt], m[rt]);
+          const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
+          m[rt] = mn;
+          l[rt] *= alpha;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
+        }
+      }
+      // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
+      if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
+      float up_lane = 0.0f, back_lane = 1.0f;
+      if (ONE) {
+        if (__float_as_uint(vs_lane) != now_vs) {  // another scale than the last step's
+          now_vs = __float_as_uint(vs_lane);
+          set_unit(vs_lane);
+          const float rel = vs_lane > 0.0f ? vs_lane * per_unit : 1.0f;
+          now_up = uniform(__builtin_amdgcn_logf(rel));
+          now_back = uniform(__builtin_amdgcn_rcpf(rel));
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) ref[rt] += now_up;
+      } else {
+        const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
+        set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
+        const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
+        up_lane = __builtin_amdgcn_logf(rel);
+        back_lane = __builtin_amdgcn_rcpf(rel);
+      }
+      float sum[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
+      h8 ph[RT][2], pl[RT][2];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        const float up = ONE ? 0.0f : lane_of(up_lane, u), back = ONE ? 1.0f : lane_of(back_lane, u);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float w[4];
+          const float base = ONE ? ref[rt] : ref[rt] + up;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
+          if (ONE)
+            sum[rt] += (w[0] + w[1]) + (w[2] + w[3]);
+          else
+            l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int e = (u & 1) * 4 + r;
+            ph[rt][u >> 1][e] = (_Float16)w[r];
+            if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
+          }
+        }
+      }
+      if (ONE) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       h8 vf[2][4];
       auto load_values = [&](int i, h8* to) {  // products 4 i .. 4 i + 3 of both halves' 2 ND
         const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
@@ -1210,7 +1215,8 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t splits, int32_t out_vec
         *reinterpret_cast<f4*>(mine + (r0 + r) * D + x * 4) = y;
       } else {
         const int row = row0 + r0 + r, tok = row / group;
-        T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride + (int64_t)(head * group + row - tok * group) * D;
+        T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride +
+                 (int64_t)(head * group + row - tok * group) * D;
         const float v[4] = {y[0], y[1], y[2], y[3]};
         store_n<4>(out + x * 4, out_vec != 0, v);
       }
@@ -1249,17 +1255,25 @@ __global__ __launch_bounds__(AT_T) void k_attend_prompt_join(AttendArgs a, const
 
 // Which kernel, by the rows (new tokens times group) of a sequence on average:
 // up to 16 or 32 they fit a wave's one or two row tiles and the call is bound
-// by reading the cache; beyond that blocks of 128 rows share what they read.
+// by reading the cache; beyond that blocks of 64 or 128 rows share what they
+// read.  Rows 20 and 32 of 8 sequences of 8000 tokens, bf16: 37 and 39 us with
+// two row tiles, 53 and 53 with one at a time, 55 and 60 as prompts; of 32
+// sequences: 120 and 124, 211 and 213, 161 and 260.
 static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) {
   const int64_t rows = tokens * group;
   return rows <= 16 * (int64_t)seqs ? 1 : rows <= 32 * (int64_t)seqs ? 2 : 0;
 }
 
-// Blocks that share a call's chunks: as many as the CUs hold at once.
-static int64_t split_blocks(bool f32, int rt) { return (f32 || rt == 2 ? 2 : 3) * (int64_t)cu_count(); }
+// Blocks that share a call's chunks.  Two for each CU reach what memory gives; a
+// third costs bf16 rows 84.5 us instead of 82.2 (one sequence of 200003 tokens)
+// and 212 instead of 199 (64 of 8000), and fp32 rows, which leave no room for
+// it, 259 instead of 203.
+static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
 
 // Tables of up to 1024 tokens: one block of eight waves for each item, in at
-// most four steps, and nothing to join.
+// most four steps, and nothing to join.  Against the split and its join, fp32
+// rows: 8.1 and 11.2 us at 250 tokens of one sequence, 12.2 and 11.1 at 1000;
+// 10.4 and 17.2 at 500 of 16, 32.2 and 36.5 at 1000 of 64.
 constexpr int64_t kWholeTokens = 1024;
 
 // How a prompt is shared out: 16-row tiles of a wave, blocks of rows of a head
@@ -1270,18 +1284,30 @@ struct PromptShape {
   int64_t tiles;
   int32_t splits;
 };
-static PromptShape prompt_shape(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t group) {
+static PromptShape prompt_of(int rt, int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t group) {
   PromptShape p;
-  p.rt = 2;
-  p.tiles = tokens * group / prompt_rows<2>() + seqs;
-  int64_t room = 2 * (int64_t)cu_count();
-  if (p.tiles * kv_heads < room) {
-    p.rt = 1;
-    p.tiles = tokens * group / prompt_rows<1>() + seqs;
-    room = (dim == 64 ? 3 : 2) * (int64_t)cu_count();
-  }
+  p.rt = rt;
+  p.tiles = tokens * group / (rt == 2 ? prompt_rows<2>() : prompt_rows<1>()) + seqs;
+  const int64_t room = (rt == 1 && dim == 64 ? 3 : 2) * (int64_t)cu_count();
   const int64_t z = (room + p.tiles * kv_heads / 2) / (p.tiles * kv_heads);  // the nearest (the tiles are a bound)
   p.splits = (int32_t)(z < 1 ? 1 : z > 32 ? 32 : z);
+  return p;
+}
+// `room`: tokens that a table has room for, all that the host knows of lengths.
+// Blocks of 64 rows where there are not two of 128 for each CU (one prompt of 256
+// tokens: 13 us, with 128 rows 20; 1024: 30 and 38), but for 1024 rows and more
+// before which there may be three times as many tokens: joining more parts of
+// larger blocks then costs less (512 tokens behind 4000: 62 us, with 64 rows 81;
+// 1024: 110 and 133; 256, of 1024 rows: 43 and 46).  A part has 256 tokens or
+// more (64 tokens of one sequence: 9.5 us in one part, 14.9 in as many as fit
+// the chip; 256: 13.4 and 15.6).
+static PromptShape prompt_shape(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t group,
+                                int64_t room) {
+  PromptShape p = prompt_of(2, kv_heads, dim, seqs, tokens, group);
+  const bool deep = tokens * group >= 1024 * (int64_t)seqs && room * seqs >= 4 * tokens;
+  if (p.tiles * kv_heads < 2 * (int64_t)cu_count() && !deep) p = prompt_of(1, kv_heads, dim, seqs, tokens, group);
+  const int64_t most = room / 256;
+  if (p.splits > most) p.splits = most < 1 ? 1 : (int32_t)most;
   return p;
 }
 
@@ -1290,27 +1316,34 @@ uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t t
   if (seqs == 0 || tokens == 0) return 0;
   const int32_t group = q_heads / kv_heads;
   const int rt = row_tiles(seqs, tokens, group);
-  if (rt) return (uint64_t)split_blocks(false, rt) * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
-  const PromptShape p = prompt_shape(kv_heads, dim, seqs, tokens, group);
-  return p.splits == 1 ? 0 : (uint64_t)p.tiles * kv_heads * p.splits * (64 * p.rt) * (dim + 2) * sizeof(float);
+  if (rt) return (uint64_t)split_blocks() * 2 * (uint64_t)(16 * rt * (dim + 2)) * sizeof(float);
+  uint64_t most = 0;
+  for (int r = 1; r <= 2; ++r) {
+    const PromptShape p = prompt_of(r, kv_heads, dim, seqs, tokens, group);
+    const uint64_t rows = (uint64_t)p.tiles * kv_heads * p.splits * (64 * r);
+    const uint64_t n = p.splits == 1 ? 0 : rows * (dim + 2) * sizeof(float);
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 template <int DT, int FMT, int D, int RT>
 static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
-  const int64_t nb = split_blocks(DT == EFFORT_F32, RT);
+  const int64_t nb = split_blocks();
   const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;  // of a head, a bound
   float* parts = static_cast<float*>(a.ws);
   if ((int64_t)a.b.max_pages * a.page_tokens <= kWholeTokens && tiles <= 65535) {
-    hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true>), dim3((unsigned)a.kv_heads, (unsigned)tiles), dim3(512), 0,
-                       s, a, parts);
+    const dim3 grid((unsigned)a.kv_heads, (unsigned)tiles);
+    hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true>), grid, dim3(512), 0, s, a, parts);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, AT_W, false>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // rows of a joining block: one where an item has many parts on average, so
-  // that eight groups share them (one sequence of 200003 tokens, 64 parts: 6 us
-  // against 9 with four rows; 16 sequences, 4 parts: 11 against 7 us)
+  // that eight groups share them (one sequence of 200000 tokens, 64 parts: 86 us
+  // with the split, with four rows 91), four where it has few (16 sequences, 4
+  // parts: 6.0 us, with one 11.1)
   const bool many = nb >= 16 * (int64_t)a.b.seqs * a.kv_heads;
   const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
   if (many)
@@ -1324,21 +1357,26 @@ template <int DT, int FMT, int D, int RT>
 static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream_t s) {
   float* parts = static_cast<float*>(a.ws);
   const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
-  const dim3 grid((unsigned)a.kv_heads, (unsigned)p.tiles, (unsigned)p.splits);
+  if (p.tiles * a.kv_heads > 0xFFFFFF) return hipErrorInvalidValue;  // 2^32 threads of a dimension
+  const int32_t tiles = (int32_t)p.tiles;
+  const dim3 grid((unsigned)(p.tiles * a.kv_heads), (unsigned)p.splits);
   if (a.page_tokens >= PR_TILE)
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT>), grid, dim3(AT_T), 0, s, a, parts, p.splits, out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
+                       out_vec);
   else
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT>), grid, dim3(AT_T), 0, s, a, parts, p.splits, out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
+                       out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL((k_attend_prompt_join<DT, D, RT>), dim3((unsigned)a.kv_heads, (unsigned)(p.tiles * prompt_rows<RT>() / 8)),
-                     dim3(AT_T), 0, s, a, parts, p.splits);
+  const dim3 rows((unsigned)a.kv_heads, (unsigned)(p.tiles * prompt_rows<RT>() / 8));  // splits: few tiles
+  hipLaunchKernelGGL((k_attend_prompt_join<DT, D, RT>), rows, dim3(AT_T), 0, s, a, parts, p.splits);
   return hipGetLastError();
 }
 
 template <int DT, int FMT, int D>
 static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
-  const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads);
+  const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads,
+                                     (int64_t)a.b.max_pages * a.page_tokens);
   return p.rt == 1 ? prompt_rt<DT, FMT, D, 1>(a, p, s) : prompt_rt<DT, FMT, D, 2>(a, p, s);
 }
 

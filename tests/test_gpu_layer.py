@@ -337,6 +337,26 @@ def test_attend_rows_of_nobody_and_bad_pages():
         assert bool((out[-3:] == 77.0).all()) and bool((out[c.starts[6]:c.starts[7]] == 0.0).all())
 
 
+@pytest.mark.parametrize("fmt,dtype,dim,page", [("e4m3", "bf16", 128, 64), ("i8", "f16", 64, 16),
+                                                ("e4m3", "f32", 128, 32)])
+def test_attend_chunk_behind_a_long_prefix(fmt, dtype, dim, page):
+    """Few blocks of 128 rows whose tokens are shared out and joined."""
+    c = Case(51, [1450, 1171], [263, 259], heads=1, group=4, dim=dim, page=page, fmt=fmt, dtype=dtype)
+    c.check_attend(c.rand(4, 2.0))
+    c.check_attend(c.rand(4, 2.0), window=700)
+
+
+def test_attend_more_blocks_of_rows_than_65535():
+    """131100 tokens of 64 query heads: rows here and there against the definition."""
+    c = Case(52, [131100], [131100], heads=1, group=64, dim=64, page=128, dtype="f16", garbage=False)
+    q = torch.randn(131100, 64, 64, device="cuda", dtype=torch.float16)
+    got = c.cache.attend(c.batch, q, window=16)
+    torch.cuda.synchronize()
+    for i in (0, 1, 63, 65534, 65535, 100001, 131070, 131099):
+        ref, tol = L.attend(c.np, c.table, [i + 1], [0, 1], f64(q[i:i + 1]), 64 ** -0.5, 16, "e4m3", "f16")
+        assert (np.abs(f64(got[i:i + 1]) - ref) <= tol).all(), i
+
+
 @pytest.mark.parametrize("new", [[1], [5], [40], [1, 1], [3, 60]])
 @pytest.mark.parametrize("room", [0, 3000])
 def test_rows_before_the_first_sequence(new, room):
