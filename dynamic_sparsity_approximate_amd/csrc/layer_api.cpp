@@ -174,8 +174,8 @@ int effort_norm_residual(int32_t dtype, int64_t rows, int64_t n, const void* x_d
   if (!dtype_ok(dtype) || (resid_dtype != dtype && resid_dtype != EFFORT_F32)) return EFFORT_EINVAL;
   if (rows < 0 || rows > kMaxIndex || n < 1 || n > kMaxNorm || !(eps >= 0.0f) || !isfinite(eps))
     return EFFORT_EINVAL;
+  if (rows == 0) return EFFORT_OK;  // nothing to do: the arrays may be null
   if (!resid_out_dev && !out_dev) return EFFORT_EINVAL;
-  if (rows == 0) return EFFORT_OK;
   const uintptr_t es = bytes_of(dtype), rs = bytes_of(resid_dtype);
   if (!rows_ok(x_dev, x_stride, n, es)) return EFFORT_EINVAL;
   if (resid_dev && !rows_ok(resid_dev, resid_stride, n, rs)) return EFFORT_EINVAL;

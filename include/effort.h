@@ -362,9 +362,11 @@ int effort_axpby(const float* a_dev, float ga, const float* b_dev, float gb, int
 
 /* A paged cache.  Element (page, head, slot, i) of the keys stands for
    k[((page * kv_heads + head) * page_tokens + slot) * head_dim + i], decoded,
-   times k_scale[page * kv_heads + head]; values alike.  Scales are
-   non-negative; a scale that is a NaN or infinite marks its page and head as
-   poisoned: every row that sees a token of it becomes NaN.  Codes behind a
+   times k_scale[page * kv_heads + head]; values alike.  A scale that is
+   negative, a NaN or infinite marks its page and head as poisoned: every row
+   that sees a token of it becomes NaN.  The value scales that a row sees should
+   lie within 2^60 of each other: what is smaller than the largest by more may
+   count as 0.  Codes behind a
    sequence's end, and scales of pages no sequence uses, may hold anything;
    the e4m3 codes 0x7F and 0xFF (NaN) must not occur in a sequence's tokens
    (effort_kv_append writes none). */
@@ -448,7 +450,8 @@ int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_
      out = sum_t w_t value_t / sum_t w_t,  w_t = exp(scale * q . key_t).
    A row that sees nothing becomes 0.  q and out: [tokens][q_heads][head_dim]
    of `dtype`, strides in elements between tokens, heads contiguous; out must
-   not overlap q.  scale: finite.  Scores, weights and sums are held in 32
+   not overlap q.  A row of q with a NaN or an infinity becomes NaN, alone.  scale:
+   finite.  Scores, weights and sums are held in 32
    bits; with EFFORT_F32 the products keep 22 bits or more of q and of the
    weights, with the 16-bit types 11 of the weights and all of q.
    ws_dev: 256-byte aligned, of effort_kv_workspace_bytes; its contents do not
@@ -466,7 +469,8 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
    not stored), out gets the last line in dtype (NULL: not computed, pre_w is
    then unused; NULL pre_w: no weight); at least one of the two is given.  The
    sums and the values between the lines are held in 32 bits; `out` comes from
-   r before it is rounded.  gate: [n], or one row per row of x when gate_stride
+   r before it is rounded.  A row whose sum of squares exceeds 32 bits (elements
+   beyond 2^63 / sqrt(n)) has no norm: 0 or NaN.  gate: [n], or one row per row of x when gate_stride
    > 0 (0: shared).  x, post_w, gate, pre_w and out are of `dtype`; resid and
    resid_out of resid_dtype, which is `dtype` or EFFORT_F32.  Strides are in
    elements between rows.  resid_out may be resid, and out may be x, with the

@@ -98,7 +98,7 @@ def append(cache, table, lens, starts, k, v, cs, inter, fmt):
             for h in range(heads):
                 y, old = new[:, h], float(cache[name + "s"][page, h])
                 fresh = slots[0] == 0
-                if not np.isfinite(y).all() or (not fresh and not math.isfinite(old)):
+                if not np.isfinite(y).all() or (not fresh and (not math.isfinite(old) or np.signbit(old))):
                     cache[name + "s"][page, h] = np.nan
                     cache[name][page, h, slots] = 0
                     continue

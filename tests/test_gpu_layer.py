@@ -201,6 +201,37 @@ def test_append_to_scales_of_another_program():
             c.check_cache()
 
 
+def test_append_to_negative_scales():
+    """They are poisoned: the page becomes NaN unless it is begun anew."""
+    c = Case(64, [20, 40, 32], [3, 5, 32], page=32)
+    for name in ("ks", "vs"):
+        c.np[name][c.table[:, 0]] = [-2.0, -0.0]
+        c.np[name][c.table[1, 1]] = [0.5, -1.0]
+        getattr(c.cache, name[0] + "_scale").copy_(torch.from_numpy(c.np[name]))
+    k, v = c.rand(2), c.rand(2)
+    c.cache.append(c.batch, k, v)
+    L.append(c.np, c.table, c.lens, c.starts, f64(k), f64(v), None, False, "e4m3")
+    assert np.isnan(c.np["ks"][c.table[0, 0]]).all() and np.isfinite(c.np["ks"][c.table[2, 0]]).all()
+    c.check_cache()
+
+
+def test_nothing_to_do():
+    """No rows, no sequences."""
+    d = dev()
+    r, out = E.norm_residual(torch.empty(0, 64, device=d), torch.empty(0, 64, device=d))
+    assert r.shape == out.shape == (0, 64)
+    c = Case(65, [40], [0], page=32)
+    none = torch.empty(0, 2, 128, device=d)
+    q = c.cache.append(c.batch, none, none, q=torch.empty(0, 4, 128, device=d))
+    assert q.shape == (0, 4, 128) and c.cache.attend(c.batch, q).shape == (0, 4, 128)
+    nobody = E.KVBatch(torch.empty(0, 3, dtype=torch.int32, device=d), ints([]), ints([0]))
+    x = c.rand(2, rows=3)
+    out = torch.full((3, 2, 128), 7.0, device=d)
+    assert c.cache.append(nobody, x, x, q=x, q_out=out) is out and (out == 7).all()
+    assert c.cache.attend(nobody, x, out=out) is out and (out == 7).all()
+    c.check_cache()
+
+
 def test_append_rows_of_nobody_and_bad_pages():
     """Padded rows, a negative position, a length behind the table, page ids out
     of range: nothing of them is stored and their q rows stay."""

@@ -169,3 +169,8 @@ def test_python_layer_refuses():
         E.norm_residual(z(2, 4), pre_w=z(5))
     with pytest.raises(ValueError):
         E.norm_residual(z(2, 4), gate=z(3, 4))
+
+
+def test_norm_of_no_rows():
+    call(E.effort_norm_residual, NORM, rows=0, x=None, resid=None, post_w=None, gate=None, pre_w=None, resid_out=None,
+         out=None)
