@@ -27,13 +27,15 @@ def _run(device, stream, call):
     its current stream, costs a microsecond of host time; the contexts cost ten."""
     if device.type != "cuda":
         raise ValueError("the tensors must be on a GPU")
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index == torch._C._cuda_getDevice():
         return call(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if stream is None:
             return call(torch.cuda.current_stream().cuda_stream)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 
@@ -152,11 +154,12 @@ class KVCache:
         def call(handle):
             out, os = None, 0
             if q is not None:
-                out = q_out if q_out is not None else torch.empty((tokens, qh, self.head_dim), dtype=q.dtype,
-                                                                  device=q.device)
-                os, oh = _heads(out, "q_out", tokens, self.head_dim, k)
-                if oh != qh:
-                    raise ValueError("q_out must have q's heads")
+                if q_out is None:
+                    out, os = q.new_empty((tokens, qh, self.head_dim)), qh * self.head_dim
+                else:
+                    out, (os, oh) = q_out, _heads(q_out, "q_out", tokens, self.head_dim, k)
+                    if oh != qh:
+                        raise ValueError("q_out must have q's heads")
             B.effort_kv_append(self.desc, batch.desc(tokens), dt, rope, rows, rot, int(interleaved), q, qs, qh, out,
                                os, k, ks, v, vs, handle)
             return out
@@ -178,10 +181,12 @@ class KVCache:
             scale = self.head_dim ** -0.5
 
         def call(handle):
-            o = out if out is not None else torch.empty((tokens, qh, self.head_dim), dtype=q.dtype, device=q.device)
-            os, oh = _heads(o, "out", tokens, self.head_dim, q)
-            if oh != qh:
-                raise ValueError("out must have q's heads")
+            if out is None:
+                o, os = q.new_empty((tokens, qh, self.head_dim)), qh * self.head_dim
+            else:
+                o, (os, oh) = out, _heads(out, "out", tokens, self.head_dim, q)
+                if oh != qh:
+                    raise ValueError("out must have q's heads")
             key = (batch.seqs, tokens, qh)
             n = self._ws_bytes.get(key)
             if n is None:
@@ -190,7 +195,7 @@ class KVCache:
                     self._ws_bytes.clear()
                 self._ws_bytes[key] = n
             # of this call alone: calls on other streams and other captured graphs have their own
-            ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+            ws = q.new_empty(n, dtype=torch.uint8) if n else None
             B.effort_kv_attention(self.desc, batch.desc(tokens), dt, q, qs, qh, scale, window, o, os, ws, n, handle)
             return o
 
@@ -200,8 +205,9 @@ class KVCache:
 def rope_table(base: float, rows: int, rot_dim: int, device="cuda", stream=None):
     """float32 [rows][rot_dim / 2][2]: (cos, sin) of row * base^(-2 pair / rot_dim)."""
     device = torch.device(device)
-    if device.type == "cuda" and device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+    if device.type == "cuda":
+        current = torch.cuda.current_device()  # (initialises the device)
+        device = torch.device("cuda", current if device.index is None else device.index)
 
     def call(handle):
         table = torch.empty((rows, rot_dim // 2, 2), dtype=torch.float32, device=device)
@@ -254,11 +260,15 @@ def norm_residual(x, resid=None, post_w=None, gate=None, scale: float = 1.0, pre
         r = o = None
         ros = os = 0
         if with_sum:
-            r = resid_out if resid_out is not None else torch.empty(shape, dtype=rdt, device=dev)
-            ros = _rows(r, "resid_out", shape, rdt, dev)
+            if resid_out is None:
+                r, ros = x.new_empty(shape, dtype=rdt), n
+            else:
+                r, ros = resid_out, _rows(resid_out, "resid_out", shape, rdt, dev)
         if with_norm:
-            o = out if out is not None else torch.empty(shape, dtype=xdt, device=dev)
-            os = _rows(o, "out", shape, xdt, dev)
+            if out is None:
+                o, os = x.new_empty(shape), n
+            else:
+                o, os = out, _rows(out, "out", shape, xdt, dev)
         B.effort_norm_residual(dt, rows, n, x, xs, _DTYPES[rdt], resid, rs, post_w, gate, gs, scale, pre_w, eps, r,
                                ros, o, os, handle)
         return r, o
