@@ -43,64 +43,69 @@ constexpr int norm_width() {
   return DT == EFFORT_F32 ? 4 : 8;
 }
 
-template <int E, typename T>
-__device__ inline void load_part(const T* p, int64_t i, int64_t n, bool vec, float* x) {
-  if (vec) {
-    load_n<E>(p + i, true, x);
-  } else {
+// A thread's E elements of part c of a row: pieces of V that memory aligns, all
+// threads' pieces side by side.  V divides n, so that a piece is in the row or not.
+template <int V>
+__device__ inline int piece_at(int c, int h, int pieces) {
+  return ((c * pieces + h) * (int)blockDim.x + (int)threadIdx.x) * V;
+}
+template <int E, int V, typename T>
+__device__ inline void load_part(const T* p, int c, int n, float* x) {
 #pragma unroll
-    for (int k = 0; k < E; ++k) x[k] = i + k < n ? (float)p[i + k] : 0.0f;
+  for (int h = 0; h < E / V; ++h) {
+    const int i = piece_at<V>(c, h, E / V);
+    if (i < n) load_n<V>(p + i, true, x + h * V);
   }
 }
 
-template <int E, typename T>
-__device__ inline void store_part(T* p, int64_t i, int64_t n, bool vec, const float* x) {
-  if (vec) {
-    store_n<E>(p + i, true, x);
-  } else {
+template <int E, int V, typename T>
+__device__ inline void store_part(T* p, int c, int n, const float* x) {
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (i + k < n) p[i + k] = (T)x[k];
+  for (int h = 0; h < E / V; ++h) {
+    const int i = piece_at<V>(c, h, E / V);
+    if (i < n) store_n<V>(p + i, true, x + h * V);
   }
 }
 
-// One block per row, the row in registers: NC pieces of E elements a thread.
+// One block per row, the row in registers: NC parts of E elements a thread.
 // Everything that the outputs need is loaded before the first sum, so that a
 // single row costs one trip to memory and two exchanges over the block (4096 fp32
 // elements: 2.5 us); for many rows the kernel moves each byte once and is bound
-// by that (8191 bf16 rows of 4096 with both norms and a gate: 54 us, 4.9 TB/s).
-template <int DT, int RT, int NC>
-__global__ __launch_bounds__(NM_T) void k_norm(NormArgs a, int32_t vec) {
+// by that (8191 bf16 rows of 4096 with both norms and a gate: 52 us, 5.2 TB/s).
+// Rows of odd widths are read two or one element at a time, neighbouring threads
+// side by side (1248 bf16 rows of 3282: 15.5 us; with a thread's eight elements
+// side by side 39.6).
+template <int DT, int RT, int NC, int V>
+__global__ __launch_bounds__(NM_T) void k_norm(NormArgs a) {
   typedef typename ElemOf<DT>::T T;
   typedef typename ElemOf<RT>::T R;
   constexpr int E = norm_width<DT>();
   __shared__ float red[2][NM_T / 64];
   const int64_t row = blockIdx.x;
+  const int n = (int)a.n;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const R* resid = a.resid ? static_cast<const R*>(a.resid) + row * a.resid_stride : nullptr;
   const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_stride : nullptr;
   const T* post = static_cast<const T*>(a.post_w);
   const T* pre = static_cast<const T*>(a.pre_w);
-  const float inv_n = 1.0f / (float)a.n;
+  const float inv_n = 1.0f / (float)n;
   float r[NC][E], old[NC][E], w[NC][E];
   float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
 #pragma unroll
     for (int k = 0; k < E; ++k) r[c][k] = old[c][k] = 0.0f, w[c][k] = a.scale;
-    if (i >= a.n) continue;
-    load_part<E>(x, i, a.n, vec != 0, r[c]);
-    if (resid) load_part<E>(resid, i, a.n, vec != 0, old[c]);
+    load_part<E, V>(x, c, n, r[c]);
+    if (resid) load_part<E, V>(resid, c, n, old[c]);
     if (post) {
-      float p[E];
-      load_part<E>(post, i, a.n, vec != 0, p);
+      float p[E] = {};
+      load_part<E, V>(post, c, n, p);
 #pragma unroll
       for (int k = 0; k < E; ++k) w[c][k] *= p[k];
     }
     if (gate) {
-      float p[E];
-      load_part<E>(gate, i, a.n, vec != 0, p);
+      float p[E] = {};
+      load_part<E, V>(gate, c, n, p);
 #pragma unroll
       for (int k = 0; k < E; ++k) w[c][k] *= p[k];
     }
@@ -119,29 +124,23 @@ __global__ __launch_bounds__(NM_T) void k_norm(NormArgs a, int32_t vec) {
   if (a.resid_out) {
     R* to = static_cast<R*>(a.resid_out) + row * a.resid_out_stride;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
-      if (i < a.n) store_part<E>(to, i, a.n, vec != 0, r[c]);
-    }
+    for (int c = 0; c < NC; ++c) store_part<E, V>(to, c, n, r[c]);
   }
   if (!a.out) return;
   float p[NC][E];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
 #pragma unroll
     for (int k = 0; k < E; ++k) p[c][k] = 1.0f;
-    if (pre && i < a.n) load_part<E>(pre, i, a.n, vec != 0, p[c]);
+    if (pre) load_part<E, V>(pre, c, n, p[c]);
   }
   const float rr = 1.0f / sqrtf(block_sum(s, red[1]) * inv_n + a.eps);
   T* out = static_cast<T*>(a.out) + row * a.out_stride;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t i = ((int64_t)c * blockDim.x + threadIdx.x) * E;
-    if (i >= a.n) continue;
 #pragma unroll
     for (int k = 0; k < E; ++k) r[c][k] = r[c][k] * rr * p[c][k];
-    store_part<E>(out, i, a.n, vec != 0, r[c]);
+    store_part<E, V>(out, c, n, r[c]);
   }
 }
 
@@ -189,37 +188,47 @@ __global__ __launch_bounds__(NM_T) void k_norm_long(NormArgs a) {
   }
 }
 
+// Whether every row allows pieces of V elements.
+template <int V, typename T, typename R>
+static bool norm_aligned(const NormArgs& a) {
+  return a.n % V == 0 && rows_aligned<V, T>(a.x, a.x_stride) &&
+         (!a.resid || rows_aligned<V, R>(a.resid, a.resid_stride)) &&
+         (!a.resid_out || rows_aligned<V, R>(a.resid_out, a.resid_out_stride)) &&
+         (!a.out || rows_aligned<V, T>(a.out, a.out_stride)) &&
+         (!a.gate || rows_aligned<V, T>(a.gate, a.gate_stride)) && rows_aligned<V, T>(a.post_w, 0) &&
+         rows_aligned<V, T>(a.pre_w, 0);
+}
+
+template <int DT, int RT, int V>
+static hipError_t norm_short(const NormArgs& a, hipStream_t s) {
+  constexpr int E = norm_width<DT>(), NC_MAX = 32 / E;
+  const int64_t parts = (a.n + E - 1) / E;
+  // As many threads as there are parts, up to NM_T: with 16 elements a thread
+  // one fp32 row of 4096 takes 4.7 us in a graph instead of 4.0, 8191 bf16 rows
+  // 57.2 instead of 54.2.
+  int nc = 1;
+  while (parts > (int64_t)nc * NM_T) nc *= 2;
+  const dim3 grid((unsigned)a.rows), block((unsigned)(((parts + nc - 1) / nc + 63) / 64 * 64));
+  switch (nc) {
+    case 1: hipLaunchKernelGGL((k_norm<DT, RT, 1, V>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_norm<DT, RT, 2, V>), grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((k_norm<DT, RT, 4, V>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((k_norm<DT, RT, NC_MAX, V>), grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
 template <int DT, int RT>
 static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   typedef typename ElemOf<DT>::T T;
   typedef typename ElemOf<RT>::T R;
-  constexpr int E = norm_width<DT>(), NC_MAX = 32 / E;
-  const int64_t pieces = (a.n + E - 1) / E;
-  const dim3 grid((unsigned)a.rows);
-  if (pieces > (int64_t)NM_T * NC_MAX) {
-    hipLaunchKernelGGL((k_norm_long<DT, RT>), grid, dim3(NM_T), 0, s, a);
+  constexpr int E = norm_width<DT>();
+  if (a.n > 32 * NM_T) {
+    hipLaunchKernelGGL((k_norm_long<DT, RT>), dim3((unsigned)a.rows), dim3(NM_T), 0, s, a);
     return hipGetLastError();
   }
-  const bool vec = a.n % E == 0 && rows_aligned<E, T>(a.x, a.x_stride) &&
-                   (!a.resid || rows_aligned<E, R>(a.resid, a.resid_stride)) &&
-                   (!a.resid_out || rows_aligned<E, R>(a.resid_out, a.resid_out_stride)) &&
-                   (!a.out || rows_aligned<E, T>(a.out, a.out_stride)) &&
-                   (!a.gate || rows_aligned<E, T>(a.gate, a.gate_stride)) && rows_aligned<E, T>(a.post_w, 0) &&
-                   rows_aligned<E, T>(a.pre_w, 0);
-  // As many threads as there are pieces, up to NM_T: with 16 elements a thread
-  // one fp32 row of 4096 takes 4.7 us in a graph instead of 4.0, 8191 bf16 rows
-  // 57.2 instead of 54.2.
-  int nc = 1;
-  while (pieces > (int64_t)nc * NM_T) nc *= 2;
-  const int64_t threads = ((pieces + nc - 1) / nc + 63) / 64 * 64;
-  const dim3 block((unsigned)threads);
-  switch (nc) {
-    case 1: hipLaunchKernelGGL((k_norm<DT, RT, 1>), grid, block, 0, s, a, (int32_t)vec); break;
-    case 2: hipLaunchKernelGGL((k_norm<DT, RT, 2>), grid, block, 0, s, a, (int32_t)vec); break;
-    case 4: hipLaunchKernelGGL((k_norm<DT, RT, 4>), grid, block, 0, s, a, (int32_t)vec); break;
-    default: hipLaunchKernelGGL((k_norm<DT, RT, NC_MAX>), grid, block, 0, s, a, (int32_t)vec); break;
-  }
-  return hipGetLastError();
+  if (norm_aligned<E, T, R>(a)) return norm_short<DT, RT, E>(a, s);
+  return norm_aligned<2, T, R>(a) ? norm_short<DT, RT, 2>(a, s) : norm_short<DT, RT, 1>(a, s);
 }
 
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, int32_t resid_dtype, hipStream_t s) {

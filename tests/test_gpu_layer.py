@@ -553,6 +553,15 @@ def test_norm(rows, n, dtype, rdt, post, gate, pre, resid):
         assert none is None and torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("n", [2, 9, 1030, 8190, 8193, 16386, 30001, 32766, 32769])
+@pytest.mark.parametrize("dtype,rdt", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+def test_norm_odd_widths(n, dtype, rdt):
+    dev()
+    a = norm_inputs(3, n, dtype, rdt, True, "row", True, True, seed=23)
+    r, out = E.norm_residual(**a, scale=0.7, eps=1e-5)
+    norm_check(a, r, out, dtype, rdt, 0.7, 1e-5)
+
+
 def test_norm_in_place_strided_unaligned():
     dev()
     for dtype in ("f32", "bf16"):
