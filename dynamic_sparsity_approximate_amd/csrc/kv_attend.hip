@@ -1275,11 +1275,13 @@ static int row_tiles(int32_t seqs, int64_t tokens, int32_t group) {
 // it, 259 instead of 203.
 static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
 
-// Tables of up to 1024 tokens: one block of eight waves for each item, in at
-// most four steps, and nothing to join.  Against the split and its join, fp32
+// Tables, or windows, of so few tokens: one block of eight waves for each
+// item, in some four steps, and nothing to join.  Against the split and its join, fp32
 // rows: 8.1 and 11.2 us at 250 tokens of one sequence, 12.2 and 11.1 at 1000;
-// 10.4 and 17.2 at 500 of 16, 32.2 and 36.5 at 1000 of 64.
-constexpr int64_t kWholeTokens = 1024;
+// 10.4 and 17.2 at 500 of 16, 32.2 and 36.5 at 1000 of 64.  Two row tiles (5
+// tokens behind a window of 512, 8 sequences): 14.9 and 22.9, of 64: 42.2 and
+// 40.9; of 896, one sequence: 17.8 and 13.9, 64: 55.1 and 48.8, so 640 there.
+static int64_t whole_tokens(int rt) { return rt == 2 ? 640 : 1024; }
 
 // How a prompt is shared out: 16-row tiles of a wave, blocks of rows of a head
 // (a bound), and in how many parts their tokens are taken so that as many blocks
@@ -1337,7 +1339,9 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const int64_t nb = split_blocks();
   const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;  // of a head, a bound
   float* parts = static_cast<float*>(a.ws);
-  if ((int64_t)a.b.max_pages * a.page_tokens <= kWholeTokens && tiles <= 65535) {
+  int64_t span = (int64_t)a.b.max_pages * a.page_tokens;
+  if (a.window && a.window + (int64_t)AT_CHUNK < span) span = a.window + (int64_t)AT_CHUNK;
+  if (span <= whole_tokens(RT) && tiles <= 65535) {
     const dim3 grid((unsigned)a.kv_heads, (unsigned)tiles);
     hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true>), grid, dim3(512), 0, s, a, parts);
     return hipGetLastError();

@@ -377,6 +377,13 @@ def test_attend_chunk_behind_a_long_prefix(fmt, dtype, dim, page):
     c.check_attend(c.rand(4, 2.0), window=700)
 
 
+@pytest.mark.parametrize("window", [1, 300, 895, 896, 897, 2000])
+@pytest.mark.parametrize("dtype,page,new", [("f32", 64, [1, 1, 1]), ("bf16", 16, [8, 5, 1])])
+def test_attend_window_of_a_long_table(dtype, page, new, window):
+    c = Case(53, [5000, 2777, 40], new, group=4, page=page, dtype=dtype)
+    c.check_attend(c.rand(8, 2.0), window=window)
+
+
 def test_attend_more_blocks_of_rows_than_65535():
     """131100 tokens of 64 query heads: rows here and there against the definition."""
     c = Case(52, [131100], [131100], heads=1, group=64, dim=64, page=128, dtype="f16", garbage=False)
