@@ -225,7 +225,7 @@ class DecoderStep:
         tokens = self.x.shape[0]
         if record is not None and tokens != 1:
             raise ValueError("a step of %d rows cannot be recorded" % tokens)
-        main = stream if stream is not None else torch.cuda.current_stream(self.x.device)
+        main = stream if stream is not None else torch.cuda.current_stream(self.x.device)  # (for the matvecs)
 
         def times(l, roles, x, ys, group=None):
             mats = [self.layers[l][r] if l is not None else self.head for r in roles]
@@ -243,18 +243,18 @@ class DecoderStep:
         for l, (c, (before_attn, before_ffn)) in enumerate(zip(self.caches, self.norms)):
             o, (qkv, gu) = self.out[l], self.groups[l] if self.groups else (None, None)
             heads = lambda t: t.view(tokens, -1, c.head_dim)  # noqa: B023,E731
-            norm_residual(add, r, pre_w=before_attn, eps=self.eps, resid_out=self.r, out=o["hq"], stream=main)
+            norm_residual(add, r, pre_w=before_attn, eps=self.eps, resid_out=self.r, out=o["hq"], stream=stream)
             times(l, ("wq", "wk", "wv"), o["hq"], [o["wq"], o["wk"], o["wv"]], qkv)
             c.append(self.batch, heads(o["wk"]), heads(o["wv"]), q=heads(o["wq"]), rope=self.rope,
-                     interleaved=self.interleaved, q_out=heads(o["q"]), stream=main)
-            c.attend(self.batch, heads(o["q"]), window=self.window, out=heads(o["a"]), stream=main)
+                     interleaved=self.interleaved, q_out=heads(o["q"]), stream=stream)
+            c.attend(self.batch, heads(o["q"]), window=self.window, out=heads(o["a"]), stream=stream)
             times(l, ("wo",), o["a"], [o["wo"]])
-            norm_residual(o["wo"], self.r, pre_w=before_ffn, eps=self.eps, resid_out=o["r"], out=o["hf"], stream=main)
+            norm_residual(o["wo"], self.r, pre_w=before_ffn, eps=self.eps, resid_out=o["r"], out=o["hf"], stream=stream)
             times(l, ("w1", "w3"), o["hf"], [o["w1"], o["w3"]], gu)
             B.effort_silu_mul(o["w1"], o["w3"], o["g"].numel(), o["g"], main)
             times(l, ("w2",), o["g"], [o["w2"]])
             r, add = o["r"], o["w2"]
-        norm_residual(add, r, pre_w=self.head_norm, eps=self.eps, resid_out=self.r, out=self.h, stream=main)
+        norm_residual(add, r, pre_w=self.head_norm, eps=self.eps, resid_out=self.r, out=self.h, stream=stream)
         times(None, ("head",), self.h, [self.logits])
         return self.logits
 
