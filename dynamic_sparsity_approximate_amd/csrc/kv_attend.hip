@@ -109,6 +109,13 @@ __device__ inline float power_of_row(float top) {
   return __uint_as_float((uint32_t)(up + 127) << 23);
 }
 
+// What the products of a row scaled so, with codes, are multiplied by to be scores
+// in base 2, but for a key's scale: NaN for a row with an infinity, whose products
+// alone could all be -inf, as if the row saw nothing.
+__device__ inline float factor_of_row(float scale, float top, float by) {
+  return top < INFINITY ? fabsf(scale) * kLog2e / by : __uint_as_float(0x7FC00000u);
+}
+
 // The tokens after `low`, up to `high`, that a row at `pos` sees of `to` tokens.
 struct Sight {
   int32_t low, high;
@@ -369,8 +376,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
-      const float by = power_of_row(max_of_row(top));
-      f[rt] = fabsf(a.scale) * kLog2e / by;
+      top = max_of_row(top);
+      const float by = power_of_row(top);
+      f[rt] = factor_of_row(a.scale, top, by);
       const float mul = a.scale < 0.0f ? -by : by;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -980,8 +988,9 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
     // the scale's sign goes into q: what is left of it keeps the scores' order
-    const float by = power_of_row(max_of_row(top));
-    f[rt] = fabsf(a.scale) * kLog2e / by;
+    top = max_of_row(top);
+    const float by = power_of_row(top);
+    f[rt] = factor_of_row(a.scale, top, by);
     const float mul = a.scale < 0.0f ? -by : by;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {

@@ -1,0 +1,38 @@
+"""Edges of the operators between a decoder layer's matvecs: what a call's
+documentation allows beside the usual (test_gpu_layer.py), against the same
+64-bit definitions."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import _layer as L  # noqa: E402
+import dynamic_sparsity_approximate_amd as E  # noqa: E402
+from test_gpu_layer import Case  # noqa: E402
+
+
+# ---------------------------------------------------------------- attention: values
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("lens,new,page,room", [([5, 70], [1, 1], 16, 0), ([5, 70], [1, 1], 64, 3000),
+                                                ([40, 9], [5, 4], 32, 3000), ([130, 65], [130, 65], 32, 0),
+                                                ([130, 65], [130, 65], 64, 0), ([1400], [130], 64, 0)])
+def test_attend_infinite_queries(dtype, lens, new, page, room):
+    """A row of q with an infinity is NaN whatever sign it gives the scores,
+    also where every score would be -inf; its neighbours are as ever."""
+    c = Case(71, lens, new, group=4, page=page, dtype=dtype, room=room)
+    c.np["k"][..., 0] = L.encode(96.0, "e4m3")  # with a key of this sign, q[0] = -inf makes every score -inf
+    c.cache.k.copy_(torch.from_numpy(c.np["k"]))
+    q = c.rand(8, 1.5)
+    n = len(q)
+    hit = {(0, 0): [(0, -np.inf)], (0, 3): [(0, np.inf)], (n - 1, 5): [(0, -np.inf), (9, -np.inf)],
+           (n // 2, 6): [(0, np.nan)], (n // 2, 7): [(0, -np.inf), (64, np.nan)]}
+    for (row, h), at in hit.items():
+        for i, x in at:
+            q[row, h, i] = x
+    with np.errstate(invalid="ignore"):
+        got, _ = c.check_attend(q)
+    for row, h in hit:
+        assert torch.isnan(got[row, h]).all(), (row, h)
+    assert int(torch.isnan(got).any(-1).sum()) == len(hit)
