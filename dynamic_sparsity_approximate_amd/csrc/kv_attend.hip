@@ -407,7 +407,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
     float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
 
     for (int32_t t = t_begin; t < t_end; t += STEP) {
-      const bool ok0 = there(now.p[0]), ok1 = there(now.p[1]);
+      // a half that no row sees counts as absent: its page may have any scale
+      const bool ok0 = there(now.p[0]) && t + 15 > see0.low && t <= see1.high;
+      const bool ok1 = there(now.p[1]) && t + 31 > see0.low && t + 16 <= see1.high;
       f4 sc[RT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -828,12 +830,13 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
     }
   };
 
-  // page of the step at t, or of its sub-tile lane & 3; -1: none, or behind the
-  // block's last step
+  // page of the step at t, or of its sub-tile lane & 3; -1: none, behind the
+  // block's last step, or a sub-tile before what the rows see, whose page may have
+  // any scale
   const int32_t stop = lo + step1 * PR_TILE < hi ? lo + step1 * PR_TILE : hi;
   auto page_at = [&](int32_t t) {
     const int32_t tok = ONE ? t : t + 16 * (lane & 3);
-    return tok < stop ? table[tok >> shift] : -1;
+    return tok < stop && (ONE || tok + 15 >= from) ? table[tok >> shift] : -1;
   };
   const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
   const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);

@@ -36,3 +36,27 @@ def test_attend_infinite_queries(dtype, lens, new, page, room):
     for row, h in hit:
         assert torch.isnan(got[row, h]).all(), (row, h)
     assert int(torch.isnan(got).any(-1).sum()) == len(hit)
+
+
+@pytest.mark.parametrize("lens,new,page,window,within", [
+    ([200], [1], 16, 50, 1), ([3000], [1], 16, 1500, 1), ([3000, 1510], [5, 3], 16, 1500, 1),
+    ([700, 333], [60, 41], 16, 100, 1), ([700, 353], [60, 41], 32, 90, 1), ([4000], [64], 32, 90, 0),
+    ([4000], [64], 32, 60, 1)])
+@pytest.mark.parametrize("dtype,fmt", [("f32", "e4m3"), ("bf16", "i8")])
+def test_attend_scales_in_front_of_the_window(lens, new, page, window, within, dtype, fmt):
+    """Pages that the window has left hold anything: here finite scales of 1e30
+    and codes that are NaN."""
+    c = Case(72, lens, new, group=4, page=page, fmt=fmt, dtype=dtype)
+    inside = 0  # pages that nobody sees in a step of 32 or 64 tokens that somebody does
+    for s, (t, n) in enumerate(zip(lens, new)):
+        first = max(0, t - n + 1 - window)
+        old = c.table[s, :first // page]
+        inside += first // page > (first & ~(31 if n * 4 <= 32 else 63)) // page
+        for name in "kv":
+            c.np[name + "s"][old] = 1e30
+            c.np[name][old] = 0x7F if fmt == "e4m3" else 0x80
+            getattr(c.cache, name).copy_(torch.from_numpy(c.np[name]))
+            getattr(c.cache, name + "_scale").copy_(torch.from_numpy(c.np[name + "s"]))
+    assert bool(inside) == bool(within)
+    got, _ = c.check_attend(c.rand(8, 1.5), window=window)
+    assert bool((got != 0).any(-1).all())
