@@ -54,12 +54,34 @@ def _heads(t, name, tokens, dim, like):
     return (strides[0] if shape[0] > 1 else h * dim), h
 
 
-class KVBatch:
+class _Kept:
+    """An object whose calls use the addresses and sizes that it was made with:
+    the attributes of `_kept` cannot be replaced, or a tensor's memory could be
+    freed while calls still use it."""
+
+    _kept = frozenset()
+
+    def __setattr__(self, name, value):
+        # the same object may be assigned again: that is how `x.t += 1`, in place, ends
+        if name in self._kept and self.__dict__.get(name, value) is not value:
+            raise AttributeError("%s cannot be replaced, only written in place" % name)
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._kept:
+            raise AttributeError("%s cannot be taken away" % name)
+        object.__delattr__(self, name)
+
+
+class KVBatch(_Kept):
     """The new tokens of a call and where they belong: int32 tensors on one
     device, page_table [seqs][max_pages], kv_lens [seqs] (lengths with the new
     tokens), q_starts [seqs + 1] (rows of q, k, v of each sequence).  Their
     contents are read by the kernels at every call, so a program (or a
-    captured graph) may update them in place between calls."""
+    captured graph) may update them in place between calls; other tensors need
+    another KVBatch."""
+
+    _kept = frozenset(("page_table", "kv_lens", "q_starts", "device", "seqs"))
 
     def __init__(self, page_table, kv_lens, q_starts):
         for t, n in ((page_table, "page_table"), (kv_lens, "kv_lens"), (q_starts, "q_starts")):
@@ -80,6 +102,9 @@ class KVBatch:
         self._ptrs = (stride, page_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr())
         self._descs = {}
 
+    def __reduce__(self):  # copies of the tensors have other addresses
+        return KVBatch, (self.page_table, self.kv_lens, self.q_starts)
+
     def desc(self, tokens: int):
         """The C descriptor for a call with that many rows."""
         d = self._descs.get(tokens)
@@ -90,11 +115,14 @@ class KVBatch:
         return d
 
 
-class KVCache:
+class KVCache(_Kept):
     """A paged cache of keys and values held in 8 bits, with one scale per
     (page, head): codes k, v uint8 [pages][kv_heads][page_tokens][head_dim],
     k_scale, v_scale float32 [pages][kv_heads].  `append` writes new tokens,
-    `attend` reads."""
+    `attend` reads.  The tensors may be written in place, not replaced."""
+
+    _kept = frozenset(("k", "v", "k_scale", "v_scale", "format", "pages", "kv_heads", "page_tokens", "head_dim",
+                       "device", "desc"))
 
     def __init__(self, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64,
                  format: int = B.EFFORT_KV_E4M3, device="cuda"):
@@ -125,6 +153,9 @@ class KVCache:
         self.desc = B.effort_kv_cache(format, self.kv_heads, self.head_dim, self.page_tokens, self.pages,
                                       k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self._ws_bytes = {}
+
+    def __reduce__(self):
+        return KVCache.wrap, (self.k, self.v, self.k_scale, self.v_scale, self.format)
 
     def _place(self, batch):
         if batch.device != self.device:
