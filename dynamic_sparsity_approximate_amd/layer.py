@@ -20,6 +20,12 @@ def _dtype(t, name):
     return d
 
 
+def _i32(x, name):
+    """ctypes would pass on the low 32 bits of a larger number."""
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError("%s: %d does not fit 32 bits" % (name, x))
+
+
 def _run(device, stream, call):
     """call(handle) on the tensors' own device with `stream` (None: that
     device's current stream), both made current, so that what the call
@@ -208,6 +214,7 @@ class KVCache(_Kept):
         qs, qh = _heads(q, "q", None, self.head_dim, q)
         if q.device != self.device:
             raise ValueError("q is on %s, the cache on %s" % (q.device, self.device))
+        _i32(window, "window")
         if scale is None:
             scale = self.head_dim ** -0.5
 
@@ -235,6 +242,7 @@ class KVCache(_Kept):
 
 def rope_table(base: float, rows: int, rot_dim: int, device="cuda", stream=None):
     """float32 [rows][rot_dim / 2][2]: (cos, sin) of row * base^(-2 pair / rot_dim)."""
+    _i32(rot_dim, "rot_dim")
     device = torch.device(device)
     if device.type == "cuda":
         current = torch.cuda.current_device()  # (initialises the device)

@@ -51,3 +51,14 @@ def test_copies_have_their_own_addresses():
     e = copy.deepcopy(c)
     assert e.desc.format == E.EFFORT_KV_I8 and e.desc.k == e.k.data_ptr() != c.k.data_ptr()
     assert copy.copy(c).desc.v == c.v.data_ptr() and copy.copy(b).kv_lens is b.kv_lens
+
+
+@pytest.mark.parametrize("big", [1 << 31, 1 << 32, (1 << 32) + 64, -(1 << 31) - 1])
+def test_numbers_beyond_32_bits(big):
+    """A window of 2^32 must not be taken for 0, nor 2^32 + 64 for 64."""
+    c = E.KVCache(4, 2, 64, page_tokens=16, device="cpu")
+    b = E.KVBatch(ints(2, 3), ints(2), ints(3))
+    with pytest.raises(ValueError, match="window"):
+        c.attend(b, torch.zeros(2, 4, 64), window=big)
+    with pytest.raises(ValueError, match="rot_dim"):
+        E.rope_table(1e4, 1, big, "cpu")
