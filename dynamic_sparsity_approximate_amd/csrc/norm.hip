@@ -231,14 +231,34 @@ static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   return norm_aligned<2, T, R>(a) ? norm_short<DT, RT, 2>(a, s) : norm_short<DT, RT, 1>(a, s);
 }
 
+// A launch has less than 2^32 threads: rows are taken so many at a time.
+constexpr int64_t NM_ROWS = 0xFFFFFFFFll / NM_T;
+
+template <int DT, int RT>
+static hipError_t norm_rows(NormArgs a, hipStream_t s) {
+  typedef typename ElemOf<DT>::T T;
+  typedef typename ElemOf<RT>::T R;
+  for (int64_t left = a.rows; left > 0; left -= NM_ROWS) {
+    a.rows = left < NM_ROWS ? left : NM_ROWS;
+    const hipError_t e = norm_launch<DT, RT>(a, s);
+    if (e != hipSuccess) return e;
+    a.x = static_cast<const T*>(a.x) + a.rows * a.x_stride;
+    if (a.resid) a.resid = static_cast<const R*>(a.resid) + a.rows * a.resid_stride;
+    if (a.gate) a.gate = static_cast<const T*>(a.gate) + a.rows * a.gate_stride;
+    if (a.resid_out) a.resid_out = static_cast<R*>(a.resid_out) + a.rows * a.resid_out_stride;
+    if (a.out) a.out = static_cast<T*>(a.out) + a.rows * a.out_stride;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, int32_t resid_dtype, hipStream_t s) {
   const bool f32 = resid_dtype == EFFORT_F32;
   switch (dtype) {
-    case EFFORT_F32: return norm_launch<EFFORT_F32, EFFORT_F32>(a, s);
+    case EFFORT_F32: return norm_rows<EFFORT_F32, EFFORT_F32>(a, s);
     case EFFORT_F16:
-      return f32 ? norm_launch<EFFORT_F16, EFFORT_F32>(a, s) : norm_launch<EFFORT_F16, EFFORT_F16>(a, s);
+      return f32 ? norm_rows<EFFORT_F16, EFFORT_F32>(a, s) : norm_rows<EFFORT_F16, EFFORT_F16>(a, s);
     case EFFORT_BF16:
-      return f32 ? norm_launch<EFFORT_BF16, EFFORT_F32>(a, s) : norm_launch<EFFORT_BF16, EFFORT_BF16>(a, s);
+      return f32 ? norm_rows<EFFORT_BF16, EFFORT_F32>(a, s) : norm_rows<EFFORT_BF16, EFFORT_BF16>(a, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
-from test_gpu_layer import Case  # noqa: E402
+from test_gpu_layer import Case, dev, f64  # noqa: E402
 
 
 # ---------------------------------------------------------------- attention: values
@@ -60,3 +60,39 @@ def test_attend_scales_in_front_of_the_window(lens, new, page, window, within, d
     assert bool(inside) == bool(within)
     got, _ = c.check_attend(c.rand(8, 1.5), window=window)
     assert bool((got != 0).any(-1).all())
+
+
+# ---------------------------------------------------------------- sizes of one launch and more
+
+def test_norm_of_more_rows_than_one_launch_has():
+    """2^26 + 5 narrow rows, which one launch (2^32 threads) could not have:
+    strided rows, a gate of its own for each, the first and last rows and those
+    around every border of a launch's rows against the definition, all of them
+    against torch in 32 bits."""
+    dev()
+    rows, n = (1 << 26) + 5, 4
+    g = torch.Generator(device="cuda").manual_seed(91)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float16)  # noqa: E731
+    x, resid, gate = rand(rows, n + 2)[:, :n], rand(rows, n), rand(rows, n + 1)[:, :n]
+    post, pre = 1 + 0.25 * rand(n), 1 + 0.25 * rand(n)
+    out = torch.full((rows, n + 2), 7.0, dtype=torch.float16, device="cuda")
+    r, h = E.norm_residual(x, resid.float(), post_w=post, gate=gate, scale=0.5, pre_w=pre, out=out[:, :n])
+    torch.cuda.synchronize()
+    assert bool((out[:, n:] == 7.0).all())
+    step = ((1 << 32) - 1) // 1024
+    at = torch.tensor(sorted({i + d for i in range(0, rows, step) for d in (-1, 0) if i + d >= 0} | {rows - 1}), device="cuda")
+    ref_r, ref, size = L.norm(f64(x[at]), f64(resid[at]), f64(post), f64(gate[at]), 0.5, f64(pre), 1e-5)
+    # a sum of 4 squares, a mean, a root, a quotient and three products: within 2^-20 of their values
+    err = 2.0 ** -20 * size
+    assert (np.abs(f64(r[at]) - ref_r) <= err).all()
+    rms = np.sqrt((ref_r * ref_r).mean(-1, keepdims=True) + 1e-5)
+    slack = (err + np.sqrt((err * err).mean(-1, keepdims=True)) * np.abs(ref_r) / rms) / rms * f64(pre)
+    assert (np.abs(f64(h[at]) - ref) <= slack + (2.0 ** -20 + 2.0 ** -11) * np.abs(ref) + 2.0 ** -25).all()
+    for i in range(0, rows, 1 << 23):
+        j = slice(i, i + (1 << 23))
+        t = x[j].float()
+        t = t * torch.rsqrt(t.square().mean(-1, keepdim=True) + 1e-5) * post.float()
+        t = resid[j].float() + 0.5 * gate[j].float() * t
+        # both sides round each of at most three terms of magnitude up to 2^5 a few times
+        assert float((r[j] - t).abs().max()) <= 2.0 ** -14
+    torch.cuda.empty_cache()
