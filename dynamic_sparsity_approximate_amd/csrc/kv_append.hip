@@ -164,7 +164,7 @@ constexpr int AP_QH = 4;
 // 44, caches warm), a single token (4.3 us) by the chain starts -> page -> scale;
 // the new rows are therefore asked for before the page is known.
 template <int DT, int FMT, int IT>
-__global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, int32_t per_token,
+__global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token,
                                                  int32_t kv_vec, int32_t q_vec) {
   typedef typename ElemOf<DT>::T T;
   const int tid = (int)threadIdx.x;
@@ -173,13 +173,14 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
   const float2* rope = reinterpret_cast<const float2*>(a.rope);
   const int half = a.rot / 2;
   const uint32_t kv_blocks = (uint32_t)units * (uint32_t)a.kv_heads * 2;
+  const uint32_t block = first + blockIdx.x;
 
-  if (blockIdx.x >= kv_blocks) {
+  if (block >= kv_blocks) {
     // a wave has 64 / chunks of a row * AP_QH heads of one token: all that leads
     // to its place is scalar (looked up by every lane, it took as long as the rest)
     const uint32_t slots = 64u >> cpr_log, per_wave = slots * AP_QH;
     const uint32_t parts = ((uint32_t)a.q_heads + per_wave - 1) / per_wave;  // waves of a token
-    const uint32_t w = (blockIdx.x - kv_blocks) * (AP_T / 64) +
+    const uint32_t w = (block - kv_blocks) * (AP_T / 64) +
                        (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t tok = (int32_t)(w / parts);
     if (tok >= a.b.tokens) return;
@@ -234,8 +235,8 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, int32_t units, in
     return;
   }
 
-  const int32_t ph = (int32_t)(blockIdx.x / (uint32_t)units);
-  const int32_t u = (int32_t)(blockIdx.x - (uint32_t)ph * (uint32_t)units);
+  const int32_t ph = (int32_t)(block / (uint32_t)units);
+  const int32_t u = (int32_t)(block - (uint32_t)ph * (uint32_t)units);
   const int head = ph >> 1;
   const bool is_k = (ph & 1) == 0;
   __shared__ int s_seq;
@@ -401,16 +402,23 @@ static hipError_t append_it(const AppendArgs& a, hipStream_t s) {
   const int64_t q_waves = (int64_t)a.b.tokens * ((a.q_heads + per_wave - 1) / per_wave);
   const int64_t kv_blocks = units * a.kv_heads * 2, q_blocks = (q_waves + AP_T / 64 - 1) / (AP_T / 64);
   const int64_t blocks = kv_blocks + q_blocks;
-  if (blocks > 0x3FFFFFFFll) return hipErrorInvalidValue;  // so that waves count in 32 bits
+  if (blocks > 0x3FFFFFFFll) return hipErrorInvalidValue;  // waves count in 32 bits (2^40 bytes of queries)
   auto vec = [](const void* p, int64_t stride) {
     return rows_aligned<2 * CP, T>(p, stride) ? 2 * CP : rows_aligned<CP, T>(p, stride) ? CP : 1;
   };
   auto less = [](int x, int y) { return x < y ? x : y; };
   const int kv_vec = less(vec(a.k, a.k_stride), vec(a.v, a.v_stride));
   const int q_vec = a.q_heads ? less(vec(a.q, a.q_stride), vec(a.q_out, a.q_out_stride)) : 1;
-  hipLaunchKernelGGL((k_append<DT, FMT, IT>), dim3((unsigned)blocks), dim3(AP_T), 0, s, a, (int32_t)units,
-                     per_token, kv_vec, q_vec);
-  return hipGetLastError();
+  // a launch has less than 2^32 threads
+  constexpr int64_t most = 0xFFFFFFFFll / AP_T;
+  for (int64_t first = 0; first < blocks; first += most) {
+    const int64_t n = blocks - first < most ? blocks - first : most;
+    hipLaunchKernelGGL((k_append<DT, FMT, IT>), dim3((unsigned)n), dim3(AP_T), 0, s, a, (uint32_t)first,
+                       (int32_t)units, per_token, kv_vec, q_vec);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Chunks of a page per thread: a page's rows, or the call's if those are fewer.

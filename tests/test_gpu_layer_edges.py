@@ -96,3 +96,52 @@ def test_norm_of_more_rows_than_one_launch_has():
         # both sides round each of at most three terms of magnitude up to 2^5 a few times
         assert float((r[j] - t).abs().max()) <= 2.0 ** -14
     torch.cuda.empty_cache()
+
+
+def test_append_of_more_pages_than_one_launch_has():
+    """2^24 tokens of 8 heads in pages of 16: (pages, heads, keys or values) and
+    the queries behind them need more blocks than one launch (2^32 threads) has.
+    Pages and queries here and there against the definition, every scale against torch."""
+    d = dev()
+    T, H, D, rot = 16, 8, 64, 8
+    tokens, pages = 1 << 24, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(92)
+    part = torch.randn(1 << 20, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.empty(tokens, H, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for i in range(16):
+        k[i << 20:(i + 1) << 20] = part * (1.0 + 0.25 * i)
+        v[i << 20:(i + 1) << 20] = part.flip(0) * 2.0 ** i
+    del part
+    q = k.clone()
+    cache = E.KVCache(pages, H, D, page_tokens=T)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    batch = E.KVBatch(table, torch.tensor([tokens], dtype=torch.int32, device="cuda"),
+                      torch.tensor([0, tokens], dtype=torch.int32, device="cuda"))
+    rope = E.rope_table(10000.0, tokens, rot, d)
+    got = cache.append(batch, k, v, q=q, rope=rope, q_out=q)
+    torch.cuda.synchronize()
+    assert got is q
+    # the scales of values, which are not rotated: least powers of two (of bf16 sizes, exact in fp32)
+    for i in range(0, pages, 1 << 16):
+        top = v[i * T:(i + (1 << 16)) * T].view(1 << 16, T, H, D).abs().amax((1, 3)).float()
+        e = torch.frexp(top / 448.0)[1]
+        e = torch.where(top <= 448.0 * torch.ldexp(torch.ones_like(top), e - 1), e - 1, e)
+        want = torch.ldexp(torch.ones_like(top), e)
+        assert torch.equal(cache.v_scale.flip(0)[i:i + (1 << 16)], want)
+    for pg in (0, 1, 77777, pages // 2 - 1, pages // 2, pages - 2, pages - 1):
+        at = slice(pg * T, (pg + 1) * T)
+        cs = rope[at].cpu().numpy()
+        want = {n: np.zeros((1, H, T, D), np.uint8) for n in "kv"}
+        want.update({n: np.zeros((1, H), np.float32) for n in ("ks", "vs")})
+        rows = [(r, 0, r) for r in range(T)]
+        L.append(want, np.array([[0]]), [T], [0, T], f64(k[at]), f64(v[at]), cs, False, "e4m3")
+        mine = pages - 1 - pg
+        for name, t, s in (("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale)):
+            assert np.array_equal(s[mine].cpu().numpy(), want[name + "s"][0]), (pg, name)
+            assert L.same_codes(t[mine].cpu().numpy(), want[name][0], "e4m3"), (pg, name)
+        for r, _, p in rows:
+            x = f64(k[pg * T + r])
+            ref = L.rotate(x, cs[p], False)
+            assert (np.abs(f64(got[pg * T + r]) - ref) <= 2.0 ** -22 * np.abs(x).max() + 2.0 ** -8 * np.abs(ref)).all()
+    del k, v, q, got, cache, rope
+    torch.cuda.empty_cache()
