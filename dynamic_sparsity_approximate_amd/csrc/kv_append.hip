@@ -11,8 +11,8 @@ constexpr int AP_T = 256;
 // ---------------------------------------------------------------- table
 
 // Angles are reduced in double: at row 2^20 a float angle would be off by 0.03.
-__global__ void k_rope_table(double base, int64_t rows, int half, float2* table) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+__global__ void k_rope_table(double base, int64_t first, int64_t rows, int half, float2* table) {
+  const int64_t i = first + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= rows * half) return;
   const int64_t row = i / half;
   const int pair = (int)(i - row * half);
@@ -22,13 +22,17 @@ __global__ void k_rope_table(double base, int64_t rows, int half, float2* table)
 }
 
 hipError_t launch_rope_table(double base, int64_t rows, int32_t rot, float* table, hipStream_t s) {
-  // row slices, so that a grid stays below 2^31 blocks
   const int half = rot / 2;
-  const int64_t blocks = (rows * half + 255) / 256;
-  if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(k_rope_table, dim3((unsigned)blocks), dim3(256), 0, s, base, rows, half,
-                     reinterpret_cast<float2*>(table));
-  return hipGetLastError();
+  const int64_t total = rows * half;
+  constexpr int64_t most = 1ll << 31;  // entries of a launch, which has less than 2^32 threads
+  for (int64_t first = 0; first < total; first += most) {
+    const int64_t n = total - first < most ? total - first : most;
+    hipLaunchKernelGGL(k_rope_table, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, base, first, rows, half,
+                       reinterpret_cast<float2*>(table));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------------------- append

@@ -145,3 +145,21 @@ def test_append_of_more_pages_than_one_launch_has():
             assert (np.abs(f64(got[pg * T + r]) - ref) <= 2.0 ** -22 * np.abs(x).max() + 2.0 ** -8 * np.abs(ref)).all()
     del k, v, q, got, cache, rope
     torch.cuda.empty_cache()
+
+
+def test_rope_table_of_more_entries_than_one_launch_has():
+    """2^26 + 9 rows of 64 pairs: rows at the borders of a launch's 2^31 entries."""
+    d = dev()
+    rows, rot = (1 << 26) + 9, 128
+    table = torch.full((rows, rot // 2, 2), 7.0, device=d)
+    E.effort_rope_table(1e6, rows, rot, table, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert not any(bool((table[i:i + (1 << 22)] == 7.0).any()) for i in range(0, rows, 1 << 22))
+    at = np.array([0, 1, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, (1 << 26) - 1, 1 << 26, rows - 1])
+    ang = at[:, None].astype(np.float64) * 1e6 ** (-np.arange(0, rot, 2) / rot)
+    got = f64(table[torch.from_numpy(at).to(d)])
+    # the angle, up to 2^26, is off by three roundings in double, the result by one in fp32
+    bound = 3 * 2.0 ** -53 * 2.0 ** 26 + 2.0 ** -24
+    assert np.abs(got - np.stack([np.cos(ang), np.sin(ang)], -1)).max() <= bound
+    del table
+    torch.cuda.empty_cache()
