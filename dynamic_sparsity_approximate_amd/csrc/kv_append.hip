@@ -350,8 +350,12 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, i
     }
   }
   // A power of two divides exactly.  By another scale (a cache that this
-  // kernel did not begin) the elements are rotated again and divided in double.
-  const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+  // kernel did not begin) the elements are rotated again and divided in double;
+  // so they are where the largest is the largest fp32 number: rotated ones may
+  // lie beyond it (the scale is the same up to 1.75 times 2^128, which also is
+  // what the codes reach).
+  const bool pow2 = (__float_as_uint(now) & 0x7FFFFFu) == 0 && top != 0x7F7FFFFFu;
+  const double most = FMT == EFFORT_KV_I8 ? 127.0 : 448.0;
   const float per = (float)(1.0 / (double)now);
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
@@ -375,7 +379,8 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, i
         for (int j = 0; j < 2 * CP; ++j) d[j] = x[j];
       }
 #pragma unroll
-      for (int j = 0; j < 2 * CP; ++j) y[it][j] = round_to_odd(d[j] / (double)now);
+      for (int j = 0; j < 2 * CP; ++j)
+        y[it][j] = round_to_odd(__builtin_fmin(__builtin_fmax(d[j] / (double)now, -most), most));
     }
     Vec<CP / 4, uint32_t> c[2];
     float z[2 * CP];

@@ -426,7 +426,9 @@ int effort_rope_table(double base, int64_t rows, int32_t rot_dim, float* table_d
    then its older tokens become the nearest codes to code * s / 2^e (ties to
    even) and its scale 2^e.  New elements become the nearest code to x / scale
    (ties to even), with x rotated in double and not rounded before that: the
-   codes are the exact ones.  For e4m3 a larger scale loses nothing of the
+   codes are the exact ones, also where a rotated key lies beyond fp32 (up to
+   1.75 times 2^128; what a table with numbers above 1 brings further counts as
+   the largest code).  For e4m3 a larger scale loses nothing of the
    older codes but what falls under its least exponent.
    A new element that is a NaN or infinite poisons its page and head: the scale
    becomes a NaN until the page is started anew, its new codes are 0.

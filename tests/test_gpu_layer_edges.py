@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
-from test_gpu_layer import Case, dev, f64  # noqa: E402
+from test_gpu_layer import DT, Case, dev, f64  # noqa: E402
 
 
 # ---------------------------------------------------------------- attention: values
@@ -163,3 +163,40 @@ def test_rope_table_of_more_entries_than_one_launch_has():
     assert np.abs(got - np.stack([np.cos(ang), np.sin(ang)], -1)).max() <= bound
     del table
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dtype,inter,rot", [("f32", False, 128), ("f32", True, 64), ("bf16", False, 24)])
+def test_append_keys_that_grow_beyond_fp32(fmt, dtype, inter, rot):
+    """Rotation makes an element up to 2^0.5 times larger: beyond the largest
+    fp32 number its code is still the nearest one."""
+    c = Case(75, [40, 33], [40, 9], fmt=fmt, dtype=dtype)
+    k, v = c.rand(2), c.rand(2)
+    big = torch.finfo(DT[dtype]).max
+    k[:20] = big * torch.sign(k[:20])
+    k[20:40] *= 5e37
+    k[41:44] = big * torch.sign(k[41:44])
+    k[44:] *= 1e-42  # their scale is a far larger one's, or their codes 0
+    rope = L.rope_rows(10000.0, c.table.shape[1] * c.page, rot)
+    c.cache.append(c.batch, k, v, rope=torch.from_numpy(rope).cuda(), interleaved=inter)
+    L.append(c.np, c.table, c.lens, c.starts, f64(k), f64(v), rope, inter, fmt)
+    assert np.isfinite(c.np["ks"][c.table[:, 0]]).all()
+    c.check_cache()
+
+
+def test_append_with_a_table_above_one():
+    """Cosines and sines of another program, times 3: keys that end beyond what
+    any scale takes have the largest code, none is a NaN."""
+    c = Case(76, [40], [40])
+    k, v = c.rand(2), c.rand(2)
+    k[3] = 3.4e38 * torch.sign(k[3])
+    rope = 3 * L.rope_rows(10000.0, c.table.shape[1] * c.page, 128)
+    c.cache.append(c.batch, k, v, rope=torch.from_numpy(rope).cuda())
+    pg = c.table[0, 0]
+    assert bool((c.cache.k_scale[pg] == 2.0 ** 120).all())
+    codes = c.cache.k[pg].cpu().numpy()
+    y = np.stack([L.rotate(f64(k[t]), rope[t], False) for t in range(32)])
+    want = L.encode(np.clip(y.transpose(1, 0, 2) / 2.0 ** 120, -448, 448), "e4m3")
+    assert L.same_codes(codes, want, "e4m3") and int((L.decode(codes, "e4m3") == 448).sum()) > 0
