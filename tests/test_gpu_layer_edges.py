@@ -9,7 +9,9 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
-from test_gpu_layer import DT, Case, dev, f64  # noqa: E402
+from _parity import REL_L2_TOL, rel_l2  # noqa: E402
+from test_gpu_decoder import Stack  # noqa: E402
+from test_gpu_layer import DT, Case, dev, f64, ints, say  # noqa: E402
 
 
 # ---------------------------------------------------------------- attention: values
@@ -200,3 +202,231 @@ def test_append_with_a_table_above_one():
     y = np.stack([L.rotate(f64(k[t]), rope[t], False) for t in range(32)])
     want = L.encode(np.clip(y.transpose(1, 0, 2) / 2.0 ** 120, -448, 448), "e4m3")
     assert L.same_codes(codes, want, "e4m3") and int((L.decode(codes, "e4m3") == 448).sum()) > 0
+
+
+# ---------------------------------------------------------------- attention: shared out and joined
+
+def parts_of(c, window, rt):
+    """The (block, slot) that the split must leave parts in: blocks take the
+    items' 128-token chunks evenly, in order of sequence, head, row tile."""
+    blocks = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    items, cap = [], c.table.shape[1] * c.page
+    for s, t in enumerate(c.lens):
+        n = c.starts[s + 1] - c.starts[s]
+        first, end = max(0, t - n + 1 - window) if window else 0, min(t, cap)
+        if n > 0 and end > first:
+            items += [-(-(end - first // 32 * 32) // 128)] * (c.heads * -(-n * c.group // (16 * rt)))
+    total = sum(items)
+    assert total > blocks, "every block must have several chunks"
+    edges = [total * b // blocks for b in range(blocks + 1)]
+    want, b, at = set(), 0, 0
+    whole = 0
+    for n in items:
+        while edges[b + 1] <= at:
+            b += 1
+        i = b
+        whole += edges[i + 1] >= at + n
+        while edges[i + 1] < at + n or edges[i] > at:
+            want.add((i, 1 if edges[i] <= at else 0))
+            if edges[i + 1] >= at + n:
+                break
+            i += 1
+        at += n
+    return want, whole, blocks
+
+
+def split_call(c, q, window):
+    """attend with a workspace of the test's own: (out, (block, slot) of the
+    parts found in it, row tiles)."""
+    need = E.effort_kv_workspace_bytes(c.cache.desc, len(c.lens), len(q), c.heads * c.group)
+    blocks = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    tile = blocks * 2 * 16 * (c.dim + 2) * 4
+    assert need in (tile, 2 * tile), "not a call that is split over blocks"
+    ws = torch.full((need // 4,), 0x7FC0BEEF, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    stride = q.shape[1] * c.dim
+    E.effort_kv_attention(c.cache.desc, c.batch.desc(len(q)), {"f32": 0, "f16": 1, "bf16": 2}[c.dtype], q, stride,
+                          q.shape[1], c.dim ** -0.5, window, out, stride, ws, need,
+                          stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    first = ws.view(blocks, 2, -1)[:, :, 0].cpu().numpy()
+    return out, {(int(b), int(s)) for b, s in zip(*np.nonzero(first != 0x7FC0BEEF))}, need // tile
+
+
+def wide(c, tokens):
+    """The same batch in a page table with room for `tokens`."""
+    more = -(-tokens // c.page) - c.table.shape[1]
+    if more > 0:
+        c.table = np.concatenate([c.table, np.full((len(c.lens), more), -7)], 1)
+        c.batch = E.KVBatch(torch.from_numpy(c.table.astype(np.int32)).cuda(), ints(c.lens), ints(c.starts))
+    return c
+
+
+LONG = [8192, 1000, 0, 7001, 129, 4097, 6000, 1, 2500, 3333, 5120, 1537, 7777, 640, 4500, 2999]
+SPLIT = [
+    # lens, new, heads, group, dim, page, fmt, dtype, window, four rows a joining block
+    (LONG, [1] * 16, 4, 4, 64, 64, "i8", "f32", 0, True),
+    (LONG, [1] * 16, 4, 8, 128, 128, "i8", "bf16", 0, True),
+    (LONG, [1] * 16, 8, 2, 64, 16, "e4m3", "f16", 1500, True),
+    (LONG, [7, 5, 0, 8, 8, 1, 3, 1, 6, 8, 2, 8, 0, 8, 5, 8], 4, 4, 64, 32, "i8", "bf16", 0, True),
+    (LONG, [7, 5, 0, 8, 8, 1, 3, 1, 6, 8, 2, 8, 0, 8, 5, 8], 4, 4, 128, 16, "i8", "f32", 2000, True),
+    ([40000], [1], 3, 4, 64, 64, "i8", "f32", 0, False),
+    ([9000, 31000], [7, 5], 2, 4, 128, 128, "i8", "f16", 0, False),
+    ([9000, 31000, 2000, 4000], [60, 1, 1, 2], 2, 1, 64, 64, "i8", "f32", 0, False),
+]
+
+
+@pytest.mark.parametrize("lens,new,heads,group,dim,page,fmt,dtype,window,four", SPLIT)
+def test_attend_several_chunks_a_block(lens, new, heads, group, dim, page, fmt, dtype, window, four):
+    """More chunks than blocks: blocks that go on from one item, and one
+    sequence, to the next, that have items whole, that leave both of their parts."""
+    c = Case(73, lens, new, heads=heads, group=group, dim=dim, page=page, fmt=fmt, dtype=dtype)
+    q = c.rand(heads * group, 1.5)
+    out, parts, rt = split_call(c, q, window)
+    want, whole, blocks = parts_of(c, window, rt)
+    assert parts == want
+    both = any((b, 1) in parts for b, s in parts if s == 0)
+    assert four == (16 * len(lens) * heads > blocks) and (not four or (both and whole))
+    _, worst = c.check_attend(q, window=window, got=out)
+    say("%d parts, %d items whole: %.3f of the bound" % (len(parts), whole, worst))
+    assert torch.equal(out, c.cache.attend(c.batch, q, window=window))
+
+
+def test_attend_many_sequences_in_a_wide_table():
+    """700 and 1024 sequences share out their chunks: entries of the plan hold
+    three and four of them, many without tokens."""
+    for seqs, window, dtype in ((700, 0, "f16"), (1024, 1400, "f32")):
+        rng = np.random.default_rng(seqs)
+        lens = [int(x) for x in rng.integers(0, 60, seqs)]
+        for s in (0, 255, 300, seqs - 1):
+            lens[s] = 2000 + s
+        new = [min(t, int(x)) for t, x in zip(lens, rng.integers(0, 3, seqs))]
+        new[300] = 5
+        c = wide(Case(seqs, lens, new, heads=2, group=2, dim=64, page=16, fmt="i8", dtype=dtype), 4000)
+        q = c.rand(4)
+        out, parts, rt = split_call(c, q, window)
+        assert parts == parts_of(c, window, rt)[0] and rt == 1
+        c.check_attend(q, window=window, got=out)
+
+
+@pytest.mark.parametrize("lens,new,page,dtype,window", [
+    ([3000, 2500, 1, 700], [512, 1, 1, 1], 64, "bf16", 0), ([3000, 2500, 1, 700], [512, 1, 1, 1], 16, "f32", 0),
+    ([900] + [1200 + 37 * i for i in range(15)], [150] + [1] * 15, 32, "f16", 0),
+    ([3000, 2500, 1, 700], [512, 1, 1, 3], 32, "f32", 600)])
+def test_attend_a_prompt_beside_single_tokens(lens, new, page, dtype, window):
+    c = Case(74, lens, new, group=4, dim=64, page=page, fmt="i8", dtype=dtype)
+    c.check_attend(c.rand(8, 1.5), window=window)
+
+
+@pytest.mark.parametrize("lens,new,heads", [([30000], [1], 3), ([9000, 7000, 8000], [2, 1, 4], 4)])
+def test_attend_holes_and_poison_among_the_parts(lens, new, heads):
+    """Parts that see nothing (absent pages), and parts that are NaN, are joined
+    with others: only the poisoned heads of rows that see the page are NaN."""
+    for name in ("ks", "vs"):
+        c = Case(77, lens, new, heads=heads, group=4, dim=64, page=32, fmt="i8")
+        c.table[0, 60:150] = -1
+        c.table[-1, 3:9] = c.pages
+        c.np[name][c.table[0, 200], 1] = np.inf
+        c.np[name][c.table[-1, 1], 0] = np.nan
+        getattr(c.cache, name[0] + "_scale").copy_(torch.from_numpy(c.np[name]))
+        c.batch.page_table.copy_(torch.from_numpy(c.table.astype(np.int32)))
+        q = c.rand(4 * heads, 1.5)
+        out, parts, rt = split_call(c, q, 0)
+        assert parts == parts_of(c, 0, rt)[0]
+        c.check_attend(q, got=out)
+        nan = torch.isnan(out).any(-1)
+        assert nan[:new[0], 4:8].all() and nan[-new[-1]:, :4].all() and int(nan.sum()) == 4 * (new[0] + new[-1])
+
+
+# ---------------------------------------------------------------- attention: streams and graphs
+
+def overlapping():
+    """Two calls that leave parts in their workspaces, split and prompt, with their results alone."""
+    cs = [Case(80, LONG, [1] * 16, heads=4, group=4, dim=64, page=64, fmt="i8"),
+          Case(81, LONG[::-1], [1] * 16, heads=4, group=4, dim=64, page=64, fmt="i8"),
+          Case(82, [3000], [100], heads=2, group=4, dim=64, page=64, fmt="i8"),
+          Case(83, [2900], [100], heads=2, group=4, dim=64, page=64, fmt="i8")]
+    qs = [c.rand(c.heads * c.group) for c in cs]
+    for c, q in zip(cs, qs):
+        assert E.effort_kv_workspace_bytes(c.cache.desc, len(c.lens), len(q), c.heads * c.group) > 0
+    alone = [c.check_attend(q)[0] for c, q in zip(cs, qs)]
+    return [[(c, q, a) for c, q, a in zip(cs[i:i + 2], qs[i:i + 2], alone[i:i + 2])] for i in (0, 2)]
+
+
+def test_workspaces_of_two_streams():
+    for pair in overlapping():
+        streams = [torch.cuda.Stream() for _ in pair]
+        outs = []
+        for _ in range(20):
+            outs += [(c.cache.attend(c.batch, q, stream=s), a) for (c, q, a), s in zip(pair, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, a) for o, a in outs)
+
+
+def test_workspaces_of_two_graphs():
+    for pair in overlapping():
+        graphs = []
+        for c, q, a in pair:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs = [c.cache.attend(c.batch, q) for _ in range(5)]
+            graphs.append((g, outs, a))
+        streams = [torch.cuda.Stream() for _ in pair]
+        for _ in range(4):
+            for _, outs, _ in graphs:
+                for o in outs:
+                    o.fill_(float("nan"))
+            torch.cuda.synchronize()
+            for (g, _, _), s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            torch.cuda.synchronize()
+            for _, outs, a in graphs:
+                assert all(torch.equal(o, a) for o in outs)
+
+
+@pytest.mark.parametrize("new,window,heads", [([1] * 4, 0, 3), ([1] * 4, 2500, 8), ([8] * 4, 0, 3), ([20] * 4, 0, 2)])
+def test_replays_follow_the_lengths(new, window, heads):
+    """One captured call of a wide table, split and joined, or a prompt's: its
+    chunks are fewer than the blocks, then more, then fewer."""
+    c = Case(84, [8192] * 4, new, heads=heads, group=4, dim=64, page=64, fmt="i8", garbage=False)
+    q = c.rand(4 * heads)
+    g = torch.cuda.CUDAGraph()
+    c.cache.attend(c.batch, q, window=window)  # loads the kernels
+    with torch.cuda.graph(g):
+        out = c.cache.attend(c.batch, q, window=window)
+    for lens in ([40, 100, 0, 700], [8192, 8100, 7000, 5000], [1, 8192, 8192, 8192], [300, 41, 8000, 2], [8192] * 4):
+        c.lens = lens
+        c.batch.kv_lens.copy_(ints(lens))
+        q.copy_(c.rand(4 * heads, 1.5))
+        out.fill_(float("nan"))
+        g.replay()
+        c.check_attend(q, window=window, got=out)
+        assert torch.equal(out, c.cache.attend(c.batch, q, window=window))
+
+
+# ---------------------------------------------------------------- whole layers
+
+@pytest.mark.parametrize("rows", [3, 9])
+def test_rows_of_nobody_stay_out_of_a_step(rows):
+    """What the rows behind the last sequence hold, NaN and infinities included,
+    changes nothing of the others and of the caches."""
+    runs = []
+    for fill in (0.0, float("nan"), float("inf")):
+        s = Stack([3, 7], [1, 1], rows, seed=5)
+        for _ in range(2):
+            s.next_x()
+            s.x[2:] = fill
+            s.step.enqueue(0.4)
+            s.advance(1)
+        torch.cuda.synchronize()
+        stored = [(L.decode(t.cpu().numpy(), "e4m3"), f64(scale)) for c in s.step.caches
+                  for t, scale in ((c.k, c.k_scale), (c.v, c.v_scale))]
+        runs.append((f64(s.step.logits[:2]), stored))
+    for logits, stored in runs[1:]:
+        assert rel_l2(logits, runs[0][0]) <= REL_L2_TOL
+        for (codes, scale), (codes0, scale0) in zip(stored, runs[0][1]):
+            assert np.array_equal(scale == 0, scale0 == 0)
+            # sums in another order may move a value by a step of its code, 2^-3 of it
+            x, x0 = (c * s[:, :, None, None] for c, s in ((codes, scale), (codes0, scale0)))
+            assert rel_l2(x, x0) <= 2.0 ** -3
