@@ -11,8 +11,13 @@
 // leave their lane, and a row's maximum, sum and rescaling are the lane's own
 // but for two exchanges across the four lanes of a row.
 // Codes become fp16 exactly (8 bits fit its 11); q is scaled per row by a power
-// of two into fp16's upper range.  With fp32 rows, q and the weights are taken
-// as two fp16 parts each (22 bits) and the products run twice.
+// of two into fp16's upper range.  fp32 rows of q, and the weights, are taken as
+// two fp16 parts each (22 bits) and the products run twice.  Only prompts with
+// 16-bit rows take the weights' upper part alone (11 bits, fewer below 2^-20 of
+// the reference): the other costs k_attend_split, which waits for memory, 0.2 to
+// 3 per cent, but two bf16 prompts of 4096 tokens 426 us instead of 317, for
+// errors of 2.07e-4 instead of 2.7e-4 (fp16) or 1.65e-3 instead of 1.66e-3 (bf16)
+// of the outputs, most of which is their own last rounding.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
@@ -500,7 +505,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = w[rt][i] * (i < 4 ? rel0 : rel1);
           ph[rt] = weights8(y);
-          if (SPLIT) pl[rt] = rest8(y, ph[rt]);
+          pl[rt] = rest8(y, ph[rt]);
         }
         // weighted values: element n * ND + d of a head is row n of product d
 #pragma unroll
@@ -526,7 +531,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
             for (int rt = 0; rt < RT; ++rt) {
               f4& acc = o[rt][x * 4 + d];
               acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], ph[rt], acc, 0, 0, 0);
-              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pl[rt], acc, 0, 0, 0);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pl[rt], acc, 0, 0, 0);
             }
         }
       }

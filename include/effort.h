@@ -453,9 +453,11 @@ int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_
    A row that sees nothing becomes 0.  q and out: [tokens][q_heads][head_dim]
    of `dtype`, strides in elements between tokens, heads contiguous; out must
    not overlap q.  A row of q with a NaN or an infinity becomes NaN, alone.  scale:
-   finite.  Scores, weights and sums are held in 32
-   bits; with EFFORT_F32 the products keep 22 bits or more of q and of the
-   weights, with the 16-bit types 11 of the weights and all of q.
+   finite.  Scores, weights and sums are held in 32 bits; the products keep all
+   of 16-bit q, 22 bits or more of fp32 q, and 22 bits or more of the weights.
+   Prompts of 16-bit rows (more than 32 rows, new tokens times query heads of a
+   group, a sequence on average) keep 11 bits of the weights, fewer of those
+   below 2^-20 of the row's largest.
    ws_dev: 256-byte aligned, of effort_kv_workspace_bytes; its contents do not
    matter.  Calls that may overlap need one each. */
 int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,

@@ -430,3 +430,21 @@ def test_rows_of_nobody_stay_out_of_a_step(rows):
             # sums in another order may move a value by a step of its code, 2^-3 of it
             x, x0 = (c * s[:, :, None, None] for c, s in ((codes, scale), (codes0, scale0)))
             assert rel_l2(x, x0) <= 2.0 ** -3
+
+
+# ---------------------------------------------------------------- attention: what 16-bit rows keep
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new,page,room", [([333, 1000, 17], [1, 1, 1], 64, 0), ([333, 1000, 17], [1, 1, 1], 16, 3000),
+                                                ([500, 77], [5, 8], 32, 0), ([9000, 4000], [5, 8], 32, 0)])
+def test_attend_keeps_the_weights_of_16_bit_rows(dtype, lens, new, page, room):
+    """Up to 32 rows a sequence: what fp32 rows are held to, and one rounding of
+    the output (small scores, which add little to that)."""
+    c = Case(78, lens, new, group=4, page=page, dtype=dtype, room=room)
+    q = c.rand(8, 0.01)
+    got = f64(c.cache.attend(c.batch, q))
+    ref, tol = L.attend(c.np, c.table, c.lens, c.starts, f64(q), c.dim ** -0.5, 0, "e4m3", "f32")
+    # rounding moves a result by half a step of what is rounded, itself within tol of ref
+    tol = tol + L.HALF_STEP[dtype] * (np.abs(ref) + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    worst = float((np.abs(got - ref) / tol).max())
+    assert worst <= 1.0, worst
