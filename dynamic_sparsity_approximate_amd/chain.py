@@ -220,11 +220,19 @@ class DecoderStep:
         "head")."""
         import torch
 
+        if record is not None and self.x.shape[0] != 1:
+            raise ValueError("a step of %d rows cannot be recorded" % self.x.shape[0])
+        if self.x.device.type != "cuda" or self.x.device.index == torch._C._cuda_getDevice():
+            return self._enqueue(effort, stream, record)
+        with torch.cuda.device(self.x.device):  # the matvecs launch on the current device
+            return self._enqueue(effort, stream, record)
+
+    def _enqueue(self, effort, stream, record):
+        import torch
+
         from .layer import norm_residual
 
         tokens = self.x.shape[0]
-        if record is not None and tokens != 1:
-            raise ValueError("a step of %d rows cannot be recorded" % tokens)
         main = stream if stream is not None else torch.cuda.current_stream(self.x.device)  # (for the matvecs)
 
         def times(l, roles, x, ys, group=None):

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
+from dynamic_sparsity_approximate_amd import binding as B  # noqa: E402
 from _parity import REL_L2_TOL, rel_l2  # noqa: E402
 from test_gpu_decoder import Stack  # noqa: E402
 from test_gpu_layer import DT, Case, dev, f64, ints, say  # noqa: E402
@@ -448,3 +449,37 @@ def test_attend_keeps_the_weights_of_16_bit_rows(dtype, lens, new, page, room):
     tol = tol + L.HALF_STEP[dtype] * (np.abs(ref) + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
     worst = float((np.abs(got - ref) / tol).max())
     assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_a_step_on_another_device_than_the_current_one(rows, monkeypatch):
+    """With one device at hand: when torch says that another one is current, every
+    call of the step is made with the tensors' own device made current."""
+    s = Stack([3, 15, 30][:rows], [1] * rows, rows, seed=6)
+    s.next_x()
+    current = [1]
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            self.was, current[0] = current[0], self.idx
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            current[0] = self.was
+            return super().__exit__(*a)
+
+    calls = []
+    for name in ("effort_matvec", "effort_matvec_multi", "effort_matvec_batched", "effort_silu_mul", "effort_kv_append",
+                 "effort_kv_attention", "effort_norm_residual"):
+        def call(*a, of=getattr(B, name), name=name, **kw):
+            calls.append((name, current[0] == s.x.device.index))
+            return of(*a, **kw)
+        monkeypatch.setattr(B, name, call)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    s.step.enqueue(0.25)
+    monkeypatch.undo()
+    # two layers and the head; q k v, and w1 w3, are one call each for a single row
+    assert len(calls) == (2 * 9 + 2 if rows == 1 else 2 * 12 + 2)
+    assert all(ok for _, ok in calls), [n for n, ok in calls if not ok]
+    s.check(0.25)
