@@ -194,7 +194,13 @@ class DecoderStep:
                 raise ValueError("a layer's matrices do not fit x, its cache or each other")
         if head.in_dim != dim:
             raise ValueError("the head does not fit x")
-        short = [m.batch for m in [head] + [L[r] for L in layers for r in LAYER_ROLES] if m.batch < tokens]
+        weights = [w for pair in norms for w in pair] + [head_norm]
+        if any(w.shape != (dim,) or w.dtype != torch.float32 or not w.is_contiguous() for w in weights):
+            raise ValueError("norm weights must be contiguous float32 tensors [dim]")
+        mats = [head] + [L[r] for L in layers for r in LAYER_ROLES]
+        if any(t.device != x.device for t in [m.layout for m in mats] + [*caches, batch] + weights):
+            raise ValueError("matrices, caches, batch and norm weights must be on x's device, %s" % x.device)
+        short = [m.batch for m in mats if m.batch < tokens]
         if short:
             raise ValueError("a matrix was made for %d vectors a call, the step has %d rows" % (short[0], tokens))
         self.layers, self.head, self.x = layers, head, x

@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
+from test_decoder_host import DIM, parts  # noqa: E402
 
 
 def ints(*shape):
@@ -62,3 +63,28 @@ def test_numbers_beyond_32_bits(big):
         c.attend(b, torch.zeros(2, 4, 64), window=big)
     with pytest.raises(ValueError, match="rot_dim"):
         E.rope_table(1e4, 1, big, "cpu")
+
+
+def on_meta():
+    """Parts of a step with one of them on another device."""
+    one, far = torch.ones(DIM), torch.ones(DIM, device="meta")
+    cache = E.KVCache(4, 2, 64, page_tokens=16, device="cpu")
+    yield dict(x=torch.zeros(2, DIM, device="meta"))  # the matrices, among others
+    yield dict(caches=[cache, E.KVCache(4, 2, 64, page_tokens=16, device="meta")])
+    yield dict(batch=E.KVBatch(*(torch.zeros(s, dtype=torch.int32, device="meta") for s in ((2, 2), (2,), (3,)))))
+    yield dict(norms=[(one, one), (one, far)])
+    yield dict(head_norm=far)
+
+
+@pytest.mark.parametrize("change", list(on_meta()))
+def test_a_step_on_two_devices(change):
+    with pytest.raises(ValueError, match="device"):
+        E.DecoderStep(**dict(parts(), **change))
+
+
+@pytest.mark.parametrize("bad", [torch.ones(DIM - 1), torch.ones(1, DIM), torch.ones(DIM).half(), torch.ones(2 * DIM)[::2]])
+def test_norm_weights_that_do_not_fit_a_step(bad):
+    one = torch.ones(DIM)
+    for change in (dict(norms=[(one, one), (bad, one)]), dict(norms=[(one, bad)] * 2), dict(head_norm=bad)):
+        with pytest.raises(ValueError, match="norm weights"):
+            E.DecoderStep(**dict(parts(), **change))
