@@ -140,7 +140,9 @@ __device__ inline uint32_t encode4(float y0, float y1, float y2, float y3) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, w, true);
 }
 
-// The rotation of one chunk's queries, rounded once in fp32.
+// The rotation of one chunk's queries in fp32: one product and the sum are
+// rounded, 2^-24 of each.  The scores they go into are sums of fp32 products
+// anyway; only codes, where the nearest one is promised, are worth double.
 __device__ inline void rotate_near(const float* x, const float2* cs, float* y) {
 #pragma unroll
   for (int j = 0; j < CP; ++j) {
@@ -164,9 +166,11 @@ constexpr int AP_QH = 4;
 // first (spread evenly among the queries' blocks: 54.3 us instead of 50.1).  A
 // page's block keeps its new elements in registers between the search for the
 // largest magnitude and the codes: IT chunks a thread, up to a whole page.  A
-// prompt is bound by its bytes (3.2 TB/s; without rotation 30 us instead of
-// 44, caches warm), a single token (4.3 us) by the chain starts -> page -> scale;
-// the new rows are therefore asked for before the page is known.
+// prompt (3.2 TB/s) waits for its bytes and for the rotation: caches warm, 44 us,
+// without rotation 30; of those 14 the keys, in double, have 5 and the queries,
+// whose blocks have the registers of a page's, 9.  A single token (4.1 us) waits
+// for the chain starts -> page -> scale; the new rows are therefore asked for
+// before the page is known.
 template <int DT, int FMT, int IT>
 __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token,
                                                  int32_t kv_vec, int32_t q_vec) {
