@@ -172,7 +172,8 @@ class KVCache(_Kept):
         """Rotates k (and q) by their positions and appends k and v.  k, v
         [tokens][kv_heads][head_dim], q [tokens][q_heads][head_dim]; `rope` is a
         table of rope_table (None: no rotation).  Returns the rotated q (None
-        without q); `q_out` may be q."""
+        without q); `q_out` may be q.  Rows that no sequence has are not written:
+        in a new tensor they hold anything."""
         self._place(batch)
         tokens = k.shape[0]
         dt = _dtype(k, "k")
@@ -207,7 +208,8 @@ class KVCache(_Kept):
         """Causal attention of the new tokens' (rotated) queries over the cache,
         `append`ed tokens included.  q [tokens][q_heads][head_dim]; scale
         defaults to 1 / sqrt(head_dim); window 0: unlimited.  Returns out, of
-        q's shape and type."""
+        q's shape and type.  Rows that no sequence has are not written: in a new
+        tensor they hold anything."""
         self._place(batch)
         tokens = q.shape[0]
         dt = _dtype(q, "q")

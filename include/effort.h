@@ -365,9 +365,9 @@ int effort_axpby(const float* a_dev, float ga, const float* b_dev, float gb, int
    times k_scale[page * kv_heads + head]; values alike.  A scale that is
    negative, a NaN or infinite marks its page and head as poisoned: every row
    that sees a token of it becomes NaN.  The value scales that a sequence's rows
-   of a call see should lie within 2^60 of each other: what is smaller than the
-   largest by more may count as 0.  Codes behind a sequence's end or in front of
-   what its rows see, and scales of pages that none of them sees, may hold anything;
+   of a call see should be at least 2^-100, and at least 2^-60 times the largest of
+   them: a smaller one may count as 0.  Codes behind a sequence's end or in front
+   of what its rows see, and scales of pages that none of them sees, may hold anything;
    the e4m3 codes 0x7F and 0xFF (NaN) must not occur in a sequence's tokens
    (effort_kv_append writes none). */
 typedef struct effort_kv_cache {

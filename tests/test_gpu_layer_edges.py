@@ -483,3 +483,16 @@ def test_a_step_on_another_device_than_the_current_one(rows, monkeypatch):
     assert len(calls) == (2 * 9 + 2 if rows == 1 else 2 * 12 + 2)
     assert all(ok for _, ok in calls), [n for n, ok in calls if not ok]
     s.check(0.25)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [-97, 105])
+@pytest.mark.parametrize("new,page,room", [([1, 1], 16, 0), ([1, 3], 64, 3000), ([90, 40], 16, 0), ([90, 40], 64, 0)])
+def test_attend_tiny_and_huge_value_scales(dtype, exponent, new, page, room):
+    """Scales of 2^-100 to 2^-94, and of 2^102 to 2^108."""
+    c = Case(79, [300, 77], new, group=4, page=page, dtype=dtype, room=room, garbage=False, spread=3)
+    c.np["ks"][:] = 2.0 ** -6
+    c.np["vs"] = (c.np["vs"].astype(np.float64) * 2.0 ** (6 + exponent)).astype(np.float32)
+    c.cache.k_scale.copy_(torch.from_numpy(c.np["ks"]))
+    c.cache.v_scale.copy_(torch.from_numpy(c.np["vs"]))
+    c.check_attend(c.rand(8, 1.5))
