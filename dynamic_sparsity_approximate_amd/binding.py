@@ -64,6 +64,7 @@ EFFORT_F32, EFFORT_F16, EFFORT_BF16 = 0, 1, 2
 EFFORT_KV_E4M3, EFFORT_KV_I8 = 0, 1
 EFFORT_KV_MIN_EXP = -64
 EFFORT_KV_MAX_SEQS = 1024
+EFFORT_KV_MAX_TREE = 512
 
 
 class effort_kv_cache(ctypes.Structure):
@@ -127,6 +128,10 @@ _PROTOS = {
     "effort_rope_table": ([_f64, _i64, _i32, _p, _p], ctypes.c_int),
     "effort_kv_append": ([_KC, _KB, _i32, _p, _i64, _i32, _i32, _p, _i64, _i32, _p, _i64, _p, _i64, _p, _i64,
                           _p], ctypes.c_int),
+    "effort_kv_append_ex": ([_KC, _KB, _p, _i32, _p, _i64, _i32, _i32, _p, _i64, _p, _i64, _f64, _p, _i64, _i32, _p,
+                             _i64, _p, _i64, _p, _i64, _p], ctypes.c_int),
+    "effort_kv_attention_tree": ([_KC, _KB, _p, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
+                                 ctypes.c_int),
     "effort_kv_workspace_bytes": ([_KC, _i32, _i64, _i32, ctypes.POINTER(_u64)], ctypes.c_int),
     "effort_kv_attention": ([_KC, _KB, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
                             ctypes.c_int),
@@ -418,6 +423,15 @@ def effort_kv_append(cache, batch, dtype: int, rope, rope_rows: int, rot_dim: in
                                  k_stride, _ptr(v), v_stride, _stream(stream)), "effort_kv_append")
 
 
+def effort_kv_append_ex(cache, batch, parents, dtype: int, rope, rope_rows: int, rot_dim: int, interleaved: int, q_norm,
+                        q_norm_stride: int, k_norm, k_norm_stride: int, eps: float, q, q_stride: int, q_heads: int,
+                        q_out, q_out_stride: int, k, k_stride: int, v, v_stride: int, stream=None):
+    _check(_lib.effort_kv_append_ex(ctypes.byref(cache), ctypes.byref(batch), _ptr(parents), dtype, _ptr(rope),
+                                    rope_rows, rot_dim, interleaved, _ptr(q_norm), q_norm_stride, _ptr(k_norm),
+                                    k_norm_stride, eps, _ptr(q), q_stride, q_heads, _ptr(q_out), q_out_stride,
+                                    _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)), "effort_kv_append_ex")
+
+
 def effort_kv_workspace_bytes(cache, seqs: int, tokens: int, q_heads: int) -> int:
     b = _u64()
     _check(_lib.effort_kv_workspace_bytes(ctypes.byref(cache), seqs, tokens, q_heads, ctypes.byref(b)),
@@ -430,6 +444,13 @@ def effort_kv_attention(cache, batch, dtype: int, q, q_stride: int, q_heads: int
     _check(_lib.effort_kv_attention(ctypes.byref(cache), ctypes.byref(batch), dtype, _ptr(q), q_stride, q_heads,
                                     scale, window, _ptr(out), out_stride, _ptr(ws), ws_bytes, _stream(stream)),
            "effort_kv_attention")
+
+
+def effort_kv_attention_tree(cache, batch, parents, dtype: int, q, q_stride: int, q_heads: int, scale: float,
+                             window: int, out, out_stride: int, ws, ws_bytes: int, stream=None):
+    _check(_lib.effort_kv_attention_tree(ctypes.byref(cache), ctypes.byref(batch), _ptr(parents), dtype, _ptr(q),
+                                         q_stride, q_heads, scale, window, _ptr(out), out_stride, _ptr(ws), ws_bytes,
+                                         _stream(stream)), "effort_kv_attention_tree")
 
 
 def effort_norm_residual(dtype: int, rows: int, n: int, x, x_stride: int, resid_dtype: int, resid,

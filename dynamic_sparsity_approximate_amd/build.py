@@ -34,8 +34,10 @@ DEVICE = ["--offload-arch=" + ARCH, "-munsafe-fp-atomics", "-fno-gpu-flush-denor
 
 SOURCES = [
     ("kernels.hip", DEVICE + ["-x", "hip"]),
-    ("kv_append.hip", DEVICE + ["-x", "hip"]),
     ("kv_attend.hip", DEVICE + ["-x", "hip"]),
+    ("kv_attend_tree.hip", DEVICE + ["-x", "hip"]),
+    ("kv_append.hip", DEVICE + ["-x", "hip"]),
+    ("kv_append_ex.hip", DEVICE + ["-x", "hip"]),
     ("norm.hip", DEVICE + ["-x", "hip"]),
     ("api.cpp", ["-D__HIP_PLATFORM_AMD__"]),
     ("layer_api.cpp", ["-D__HIP_PLATFORM_AMD__"]),

@@ -27,6 +27,11 @@ struct AppendArgs {
   uint8_t *kc, *vc;
   float *ks, *vs;
   int32_t rot, interleaved, q_heads, kv_heads, dim, page_tokens, format;
+  // launch_append_ex: each may be null
+  const int32_t* parents;
+  const void *q_norm, *k_norm;  // [dim], of head h at h * stride
+  int64_t q_norm_stride, k_norm_stride;
+  double eps;
 };
 
 struct AttendArgs {
@@ -40,6 +45,7 @@ struct AttendArgs {
   int32_t window, q_heads, kv_heads, dim, page_tokens, format;
   int32_t q_vec;  // q's rows are aligned to 8 elements
   void* ws;
+  const int32_t* parents;  // launch_attend_tree
 };
 
 struct NormArgs {
@@ -51,8 +57,10 @@ struct NormArgs {
 
 hipError_t launch_rope_table(double base, int64_t rows, int32_t rot, float* table, hipStream_t s);
 hipError_t launch_append(const AppendArgs& a, int32_t dtype, hipStream_t s);
+hipError_t launch_append_ex(const AppendArgs& a, int32_t dtype, hipStream_t s);
 uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads);
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, hipStream_t s);
+hipError_t launch_attend_tree(const AttendArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, int32_t resid_dtype, hipStream_t s);
 
 }  // namespace effort

@@ -74,15 +74,20 @@ int effort_rope_table(double base, int64_t rows, int32_t rot_dim, float* table_d
   return status_of(launch_rope_table(base, rows, rot_dim, table_dev, static_cast<hipStream_t>(stream)));
 }
 
-int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
-                     const float* rope_dev, int64_t rope_rows, int32_t rot_dim, int32_t interleaved,
-                     const void* q_dev, int64_t q_stride, int32_t q_heads, void* q_out_dev,
-                     int64_t q_out_stride, const void* k_dev, int64_t k_stride, const void* v_dev,
-                     int64_t v_stride, void* stream) {
+int effort_kv_append_ex(const effort_kv_cache* cache, const effort_kv_batch* batch, const int32_t* parents_dev,
+                        int32_t dtype, const float* rope_dev, int64_t rope_rows, int32_t rot_dim,
+                        int32_t interleaved, const void* q_norm_dev, int64_t q_norm_stride,
+                        const void* k_norm_dev, int64_t k_norm_stride, double eps, const void* q_dev,
+                        int64_t q_stride, int32_t q_heads, void* q_out_dev, int64_t q_out_stride,
+                        const void* k_dev, int64_t k_stride, const void* v_dev, int64_t v_stride, void* stream) {
   if (!cache_ok(cache) || !batch_ok(batch, cache->page_tokens) || !dtype_ok(dtype)) return EFFORT_EINVAL;
   if (interleaved != 0 && interleaved != 1) return EFFORT_EINVAL;
   if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 8) return EFFORT_EINVAL;
   if (q_dev && !heads_ok(q_heads, cache->kv_heads)) return EFFORT_EINVAL;
+  if (!(eps >= 0.0) || !isfinite(eps) || !aligned(parents_dev, 4)) return EFFORT_EINVAL;
+  for (int64_t stride : {q_norm_dev ? q_norm_stride : 0, k_norm_dev ? k_norm_stride : 0})
+    if (stride != 0 && stride < cache->head_dim) return EFFORT_EINVAL;
+  if (!aligned(q_norm_dev, bytes_of(dtype)) || !aligned(k_norm_dev, bytes_of(dtype))) return EFFORT_EINVAL;
   if (batch->seqs == 0 || batch->tokens == 0) return EFFORT_OK;
   if (rot_dim && (!rope_dev || !aligned(rope_dev, 8) ||
                   rope_rows < (int64_t)batch->max_pages * cache->page_tokens))
@@ -118,7 +123,25 @@ int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch,
   a.dim = cache->head_dim;
   a.page_tokens = cache->page_tokens;
   a.format = cache->format;
-  return status_of(launch_append(a, dtype, static_cast<hipStream_t>(stream)));
+  a.parents = parents_dev;
+  a.q_norm = q_dev ? q_norm_dev : nullptr;
+  a.k_norm = k_norm_dev;
+  a.q_norm_stride = q_norm_stride;
+  a.k_norm_stride = k_norm_stride;
+  a.eps = eps;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool plain = !parents_dev && !a.q_norm && !a.k_norm;
+  return status_of(plain ? launch_append(a, dtype, s) : launch_append_ex(a, dtype, s));
+}
+
+int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
+                     const float* rope_dev, int64_t rope_rows, int32_t rot_dim, int32_t interleaved,
+                     const void* q_dev, int64_t q_stride, int32_t q_heads, void* q_out_dev,
+                     int64_t q_out_stride, const void* k_dev, int64_t k_stride, const void* v_dev,
+                     int64_t v_stride, void* stream) {
+  return effort_kv_append_ex(cache, batch, nullptr, dtype, rope_dev, rope_rows, rot_dim, interleaved, nullptr, 0,
+                             nullptr, 0, 0.0, q_dev, q_stride, q_heads, q_out_dev, q_out_stride, k_dev, k_stride,
+                             v_dev, v_stride, stream);
 }
 
 int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
@@ -130,10 +153,11 @@ int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_
   return EFFORT_OK;
 }
 
-int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
-                        const void* q_dev, int64_t q_stride, int32_t q_heads, float scale,
-                        int32_t window, void* out_dev, int64_t out_stride, void* ws_dev,
-                        uint64_t ws_bytes, void* stream) {
+// parents_dev NULL: no trees.
+static int attention(const effort_kv_cache* cache, const effort_kv_batch* batch, const int32_t* parents_dev,
+                     int32_t dtype, const void* q_dev, int64_t q_stride, int32_t q_heads, float scale,
+                     int32_t window, void* out_dev, int64_t out_stride, void* ws_dev, uint64_t ws_bytes,
+                     void* stream) {
   if (!cache_ok(cache) || !batch_ok(batch, cache->page_tokens) || !dtype_ok(dtype)) return EFFORT_EINVAL;
   if (!heads_ok(q_heads, cache->kv_heads) || !isfinite(scale) || window < 0) return EFFORT_EINVAL;
   if (batch->seqs == 0 || batch->tokens == 0) return EFFORT_OK;
@@ -163,7 +187,27 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
   a.format = cache->format;
   a.q_vec = aligned(q_dev, 8 * es) && q_stride % 8 == 0;
   a.ws = ws_dev;
-  return status_of(launch_attend(a, dtype, static_cast<hipStream_t>(stream)));
+  a.parents = parents_dev;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(parents_dev ? launch_attend_tree(a, dtype, s) : launch_attend(a, dtype, s));
+}
+
+int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,
+                        const void* q_dev, int64_t q_stride, int32_t q_heads, float scale,
+                        int32_t window, void* out_dev, int64_t out_stride, void* ws_dev,
+                        uint64_t ws_bytes, void* stream) {
+  return attention(cache, batch, nullptr, dtype, q_dev, q_stride, q_heads, scale, window, out_dev, out_stride, ws_dev,
+                   ws_bytes, stream);
+}
+
+int effort_kv_attention_tree(const effort_kv_cache* cache, const effort_kv_batch* batch,
+                             const int32_t* parents_dev, int32_t dtype, const void* q_dev, int64_t q_stride,
+                             int32_t q_heads, float scale, int32_t window, void* out_dev, int64_t out_stride,
+                             void* ws_dev, uint64_t ws_bytes, void* stream) {
+  // with nothing to do the arrays may be null
+  if ((!parents_dev && batch && batch->seqs > 0 && batch->tokens > 0) || !aligned(parents_dev, 4)) return EFFORT_EINVAL;
+  return attention(cache, batch, parents_dev, dtype, q_dev, q_stride, q_heads, scale, window, out_dev, out_stride,
+                   ws_dev, ws_bytes, stream);
 }
 
 int effort_norm_residual(int32_t dtype, int64_t rows, int64_t n, const void* x_dev, int64_t x_stride,

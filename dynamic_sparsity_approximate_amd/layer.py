@@ -85,11 +85,19 @@ class KVBatch(_Kept):
     tokens), q_starts [seqs + 1] (rows of q, k, v of each sequence).  Their
     contents are read by the kernels at every call, so a program (or a
     captured graph) may update them in place between calls; other tensors need
-    another KVBatch."""
+    another KVBatch.
 
-    _kept = frozenset(("page_table", "kv_lens", "q_starts", "device", "seqs"))
+    With `parents` (int32 [rows or more]) the new tokens of a sequence are a tree:
+    parents[q_starts[s] + i] is the number, among the sequence's new tokens, of
+    the one that token i continues, -1 the last committed one.  Token i is stored
+    in the slot of position base + i (base: the committed tokens), rotated as the
+    position base + its ancestors among the new tokens, and sees the committed
+    tokens, those ancestors and itself.  A tree has at most EFFORT_KV_MAX_TREE
+    tokens; `kv_accept` keeps one path of it."""
 
-    def __init__(self, page_table, kv_lens, q_starts):
+    _kept = frozenset(("page_table", "kv_lens", "q_starts", "parents", "device", "seqs"))
+
+    def __init__(self, page_table, kv_lens, q_starts, parents=None):
         for t, n in ((page_table, "page_table"), (kv_lens, "kv_lens"), (q_starts, "q_starts")):
             if t.dtype != torch.int32 or t.device != page_table.device:
                 raise ValueError("%s must be an int32 tensor on page_table's device" % n)
@@ -100,6 +108,10 @@ class KVBatch(_Kept):
         if (page_table.shape[1] > 1 and page_table.stride(1) != 1) or not (
                 kv_lens.is_contiguous() and q_starts.is_contiguous()):
             raise ValueError("page_table's rows, kv_lens and q_starts must be contiguous")
+        if parents is not None and (parents.dim() != 1 or parents.dtype != torch.int32 or
+                                    parents.device != page_table.device or not parents.is_contiguous()):
+            raise ValueError("parents must be a contiguous int32 tensor [rows] on page_table's device")
+        self.parents = parents
         self.page_table, self.kv_lens, self.q_starts = page_table, kv_lens, q_starts
         self.device = page_table.device
         stride = page_table.stride(0) if seqs > 1 else page_table.shape[1]
@@ -109,12 +121,14 @@ class KVBatch(_Kept):
         self._descs = {}
 
     def __reduce__(self):  # copies of the tensors have other addresses
-        return KVBatch, (self.page_table, self.kv_lens, self.q_starts)
+        return KVBatch, (self.page_table, self.kv_lens, self.q_starts, self.parents)
 
     def desc(self, tokens: int):
         """The C descriptor for a call with that many rows."""
         d = self._descs.get(tokens)
         if d is None:
+            if self.parents is not None and self.parents.shape[0] < tokens:
+                raise ValueError("a call with %d rows, but only %d parents" % (tokens, self.parents.shape[0]))
             if len(self._descs) >= 64:
                 self._descs.clear()
             d = self._descs[tokens] = B.effort_kv_batch(*self._args, tokens, *self._ptrs)
@@ -168,10 +182,12 @@ class KVCache(_Kept):
             raise ValueError("the batch is on %s, the cache on %s" % (batch.device, self.device))
 
     def append(self, batch: KVBatch, k, v, q=None, rope=None, interleaved: bool = False, q_out=None,
-               stream=None):
+               stream=None, q_norm=None, k_norm=None, eps: float = 1e-5):
         """Rotates k (and q) by their positions and appends k and v.  k, v
         [tokens][kv_heads][head_dim], q [tokens][q_heads][head_dim]; `rope` is a
-        table of rope_table (None: no rotation).  Returns the rotated q (None
+        table of rope_table (None: no rotation).  With `q_norm`, `k_norm`
+        ([head_dim], or one row per head) each head is x / rms(x) * weight first,
+        rms with `eps` under its root.  Returns the rotated q (None
         without q); `q_out` may be q.  Rows that no sequence has are not written:
         in a new tensor they hold anything."""
         self._place(batch)
@@ -181,6 +197,8 @@ class KVCache(_Kept):
         vs, vh = _heads(v, "v", tokens, self.head_dim, k)
         if kh != self.kv_heads or vh != kh or k.device != self.device:
             raise ValueError("k and v must have the cache's %d heads and be on %s" % (self.kv_heads, self.device))
+        norms = (self._norm(q_norm, "q_norm", k, q.shape[1] if q is not None else None) +
+                 self._norm(k_norm, "k_norm", k, kh))
         rows = rot = 0
         if rope is not None:
             if rope.dim() != 3 or rope.shape[2] != 2 or rope.dtype != torch.float32 or \
@@ -198,11 +216,27 @@ class KVCache(_Kept):
                     out, (os, oh) = q_out, _heads(q_out, "q_out", tokens, self.head_dim, k)
                     if oh != qh:
                         raise ValueError("q_out must have q's heads")
-            B.effort_kv_append(self.desc, batch.desc(tokens), dt, rope, rows, rot, int(interleaved), q, qs, qh, out,
-                               os, k, ks, v, vs, handle)
+            if batch.parents is None and q_norm is None and k_norm is None:
+                B.effort_kv_append(self.desc, batch.desc(tokens), dt, rope, rows, rot, int(interleaved), q, qs, qh,
+                                   out, os, k, ks, v, vs, handle)
+            else:
+                B.effort_kv_append_ex(self.desc, batch.desc(tokens), batch.parents, dt, rope, rows, rot,
+                                      int(interleaved), *norms, eps, q, qs, qh, out, os, k, ks, v, vs, handle)
             return out
 
         return _run(self.device, stream, call)
+
+    def _norm(self, w, name, like, heads):
+        """(weights, stride between heads)."""
+        if w is None:
+            return None, 0
+        if heads is None:
+            raise ValueError("q_norm without q")
+        if w.dtype != like.dtype or w.device != like.device or not w.is_contiguous() or \
+                w.shape not in ((self.head_dim,), (heads, self.head_dim)):
+            raise ValueError("%s: %s %s on %s, wanted contiguous %s [%d] or [%d][%d] on %s" % (
+                name, w.dtype, tuple(w.shape), w.device, like.dtype, self.head_dim, heads, self.head_dim, like.device))
+        return w, self.head_dim if w.dim() == 2 else 0
 
     def attend(self, batch: KVBatch, q, window: int = 0, scale=None, out=None, stream=None):
         """Causal attention of the new tokens' (rotated) queries over the cache,
@@ -236,7 +270,11 @@ class KVCache(_Kept):
                 self._ws_bytes[key] = n
             # of this call alone: calls on other streams and other captured graphs have their own
             ws = q.new_empty(n, dtype=torch.uint8) if n else None
-            B.effort_kv_attention(self.desc, batch.desc(tokens), dt, q, qs, qh, scale, window, o, os, ws, n, handle)
+            if batch.parents is None:
+                B.effort_kv_attention(self.desc, batch.desc(tokens), dt, q, qs, qh, scale, window, o, os, ws, n, handle)
+            else:
+                B.effort_kv_attention_tree(self.desc, batch.desc(tokens), batch.parents, dt, q, qs, qh, scale, window,
+                                           o, os, ws, n, handle)
             return o
 
         return _run(self.device, stream, call)

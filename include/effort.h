@@ -359,6 +359,7 @@ int effort_axpby(const float* a_dev, float ga, const float* b_dev, float gb, int
 
 #define EFFORT_KV_MIN_EXP (-64)   /* least exponent of a scale that effort_kv_append writes */
 #define EFFORT_KV_MAX_SEQS 1024   /* sequences of one call */
+#define EFFORT_KV_MAX_TREE 512    /* new tokens of a sequence that are a tree */
 
 /* A paged cache.  Element (page, head, slot, i) of the keys stands for
    k[((page * kv_heads + head) * page_tokens + slot) * head_dim + i], decoded,
@@ -441,7 +442,32 @@ int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch,
                      int64_t q_out_stride, const void* k_dev, int64_t k_stride, const void* v_dev,
                      int64_t v_stride, void* stream);
 
-/* Workspace bytes of effort_kv_attention for `seqs` sequences and `tokens` new
+/* effort_kv_append with norms of the heads, and of trees of new tokens.
+   Norms: q_norm_dev not NULL: each head of q becomes x / rms(x) * w before its
+   rotation, rms(x) = sqrt(mean(x^2) + eps) over the head_dim elements and w =
+   q_norm_dev[head * q_norm_stride ..] of `dtype` (stride 0: shared by the heads,
+   else at least head_dim); k alike with k_norm_dev.  A key's norm is taken in
+   double like its rotation and not rounded before its code; a query's is
+   rounded to 32 bits.  A head with a NaN or an infinity is a NaN throughout,
+   and so is one of zeros when eps is 0.
+   Trees: parents_dev not NULL: int32 [tokens]; row q_starts[s] + i's entry is
+   the number, among sequence s's new tokens, of the token that i continues;
+   what is no earlier token of the sequence (-1, say) means the last committed
+   one.  Token i still has the slot of position base + i, base = kv_lens[s] - n,
+   but is rotated as the position base + d, d the number of its ancestors among
+   the new tokens.  A sequence of more than EFFORT_KV_MAX_TREE new tokens, or of
+   more than its length, is no tree: nothing of it is stored and none of its q
+   rows is written.
+   EINVAL also: eps negative or not finite, a weight stride that is neither 0 nor
+   at least head_dim, misaligned weights or parents. */
+int effort_kv_append_ex(const effort_kv_cache* cache, const effort_kv_batch* batch, const int32_t* parents_dev,
+                        int32_t dtype, const float* rope_dev, int64_t rope_rows, int32_t rot_dim,
+                        int32_t interleaved, const void* q_norm_dev, int64_t q_norm_stride,
+                        const void* k_norm_dev, int64_t k_norm_stride, double eps, const void* q_dev,
+                        int64_t q_stride, int32_t q_heads, void* q_out_dev, int64_t q_out_stride,
+                        const void* k_dev, int64_t k_stride, const void* v_dev, int64_t v_stride, void* stream);
+
+/* Workspace bytes of effort_kv_attention (and effort_kv_attention_tree) for `seqs` sequences and `tokens` new
    tokens of q_heads query heads (a multiple of kv_heads, at most 64 times it). */
 int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
                               int32_t q_heads, uint64_t* bytes);
@@ -464,6 +490,16 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
                         const void* q_dev, int64_t q_stride, int32_t q_heads, float scale,
                         int32_t window, void* out_dev, int64_t out_stride, void* ws_dev,
                         uint64_t ws_bytes, void* stream);
+
+/* effort_kv_attention of trees of new tokens (parents_dev as in
+   effort_kv_append_ex): a new token sees the positions in front of its
+   sequence's new ones, its ancestors among these and itself; with window > 0
+   only those whose position is greater than its own minus window, positions
+   being base + d.  A sequence that is no tree sees nothing: its rows become 0. */
+int effort_kv_attention_tree(const effort_kv_cache* cache, const effort_kv_batch* batch,
+                             const int32_t* parents_dev, int32_t dtype, const void* q_dev, int64_t q_stride,
+                             int32_t q_heads, float scale, int32_t window, void* out_dev, int64_t out_stride,
+                             void* ws_dev, uint64_t ws_bytes, void* stream);
 
 /* The end of one block and the start of the next, for rows x[rows][n]:
      t = x / rms(x) * post_w     (post_w NULL: t = x)
