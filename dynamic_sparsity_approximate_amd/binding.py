@@ -65,6 +65,8 @@ EFFORT_KV_E4M3, EFFORT_KV_I8 = 0, 1
 EFFORT_KV_MIN_EXP = -64
 EFFORT_KV_MAX_SEQS = 1024
 EFFORT_KV_MAX_TREE = 512
+EFFORT_KV_MAX_CACHES = 4096
+EFFORT_BEAM_MAX, EFFORT_BEAM_MAX_KEEP = 64, 128
 
 
 class effort_kv_cache(ctypes.Structure):
@@ -77,6 +79,13 @@ class effort_kv_batch(ctypes.Structure):
     _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
                 ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
                 ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p)]
+
+
+class effort_kv_book(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("info", ctypes.c_void_p)]
 
 
 if not os.path.exists(LIB_PATH):
@@ -94,6 +103,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _p, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _D = ctypes.POINTER(effort_desc)
 _KC, _KB, _f64 = ctypes.POINTER(effort_kv_cache), ctypes.POINTER(effort_kv_batch), ctypes.c_double
+_KP = ctypes.POINTER(effort_kv_book)
 _PROTOS = {
     "effort_strerror": ([ctypes.c_int], ctypes.c_char_p),
     "effort_last_hip_error": ([], ctypes.c_char_p),
@@ -135,6 +145,15 @@ _PROTOS = {
     "effort_kv_workspace_bytes": ([_KC, _i32, _i64, _i32, ctypes.POINTER(_u64)], ctypes.c_int),
     "effort_kv_attention": ([_KC, _KB, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
                             ctypes.c_int),
+    "effort_kv_fork": ([_KP, _p, _p, _p], ctypes.c_int),
+    "effort_kv_grow_workspace_bytes": ([_KP, ctypes.POINTER(_u64)], ctypes.c_int),
+    "effort_kv_grow": ([_KP, _KC, _i32, _p, _i32, _p, _u64, _p], ctypes.c_int),
+    "effort_kv_copy_pages": ([_KC, _i32, _p, _p, _i64, _p], ctypes.c_int),
+    "effort_kv_accept_workspace_bytes": ([_i32, ctypes.POINTER(_u64)], ctypes.c_int),
+    "effort_kv_accept": ([_KC, _i32, _KB, _p, _p, _p, _p, _u64, _p], ctypes.c_int),
+    "effort_beam_workspace_bytes": ([_i64, _i32, _i64, ctypes.POINTER(_u64)], ctypes.c_int),
+    "effort_beam_select": ([_i32, _p, _i64, _p, _p, _i32, _i64, _i32, _i64, _i32, _p, _p, _p, _p, _u64, _p],
+                           ctypes.c_int),
     "effort_norm_residual": ([_i32, _i64, _i64, _p, _i64, _i32, _p, _i64, _p, _p, _i64, _f32, _p, _f32, _p,
                               _i64, _p, _i64, _p], ctypes.c_int),
     "effort_event_create": ([ctypes.POINTER(_p)], ctypes.c_int),
@@ -451,6 +470,58 @@ def effort_kv_attention_tree(cache, batch, parents, dtype: int, q, q_stride: int
     _check(_lib.effort_kv_attention_tree(ctypes.byref(cache), ctypes.byref(batch), _ptr(parents), dtype, _ptr(q),
                                          q_stride, q_heads, scale, window, _ptr(out), out_stride, _ptr(ws), ws_bytes,
                                          _stream(stream)), "effort_kv_attention_tree")
+
+
+def kv_caches(caches):
+    """The C array of some caches' descriptors."""
+    arr = (effort_kv_cache * max(len(caches), 1))()
+    for i, c in enumerate(caches):
+        arr[i] = c
+    return arr
+
+
+def effort_kv_fork(book, source, lens=None, stream=None):
+    _check(_lib.effort_kv_fork(ctypes.byref(book), _ptr(source), _ptr(lens), _stream(stream)), "effort_kv_fork")
+
+
+def effort_kv_grow_workspace_bytes(book) -> int:
+    b = _u64()
+    _check(_lib.effort_kv_grow_workspace_bytes(ctypes.byref(book), ctypes.byref(b)), "effort_kv_grow_workspace_bytes")
+    return int(b.value)
+
+
+def effort_kv_grow(book, caches, count: int, more_of, more: int, ws, ws_bytes: int, stream=None):
+    """`caches` is an array of kv_caches."""
+    _check(_lib.effort_kv_grow(ctypes.byref(book), caches, count, _ptr(more_of), more, _ptr(ws), ws_bytes,
+                               _stream(stream)), "effort_kv_grow")
+
+
+def effort_kv_copy_pages(caches, count: int, src, dst, n: int, stream=None):
+    _check(_lib.effort_kv_copy_pages(caches, count, _ptr(src), _ptr(dst), n, _stream(stream)), "effort_kv_copy_pages")
+
+
+def effort_kv_accept_workspace_bytes(seqs: int) -> int:
+    b = _u64()
+    _check(_lib.effort_kv_accept_workspace_bytes(seqs, ctypes.byref(b)), "effort_kv_accept_workspace_bytes")
+    return int(b.value)
+
+
+def effort_kv_accept(caches, count: int, batch, parents, leaf, lens_out, ws, ws_bytes: int, stream=None):
+    _check(_lib.effort_kv_accept(caches, count, ctypes.byref(batch), _ptr(parents), _ptr(leaf), _ptr(lens_out), _ptr(ws),
+                                 ws_bytes, _stream(stream)), "effort_kv_accept")
+
+
+def effort_beam_workspace_bytes(items: int, beams: int, vocab: int) -> int:
+    b = _u64()
+    _check(_lib.effort_beam_workspace_bytes(items, beams, vocab, ctypes.byref(b)), "effort_beam_workspace_bytes")
+    return int(b.value)
+
+
+def effort_beam_select(dtype: int, logits, stride: int, scores, ended, end_token: int, items: int, beams: int,
+                       vocab: int, keep: int, out_scores, out_parents, out_tokens, ws, ws_bytes: int, stream=None):
+    _check(_lib.effort_beam_select(dtype, _ptr(logits), stride, _ptr(scores), _ptr(ended), end_token, items, beams,
+                                   vocab, keep, _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens), _ptr(ws),
+                                   ws_bytes, _stream(stream)), "effort_beam_select")
 
 
 def effort_norm_residual(dtype: int, rows: int, n: int, x, x_stride: int, resid_dtype: int, resid,

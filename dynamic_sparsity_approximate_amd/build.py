@@ -38,6 +38,8 @@ SOURCES = [
     ("kv_attend_tree.hip", DEVICE + ["-x", "hip"]),
     ("kv_append.hip", DEVICE + ["-x", "hip"]),
     ("kv_append_ex.hip", DEVICE + ["-x", "hip"]),
+    ("kv_pages.hip", DEVICE + ["-x", "hip"]),
+    ("beam.hip", DEVICE + ["-x", "hip"]),
     ("norm.hip", DEVICE + ["-x", "hip"]),
     ("api.cpp", ["-D__HIP_PLATFORM_AMD__"]),
     ("layer_api.cpp", ["-D__HIP_PLATFORM_AMD__"]),
@@ -56,7 +58,7 @@ def _compile(src, extra):
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=6) as ex:
+    with ThreadPoolExecutor(max_workers=8) as ex:
         objs = list(ex.map(lambda s: _compile(*s), SOURCES))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + ["-lpthread"]

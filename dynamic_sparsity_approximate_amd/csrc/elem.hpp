@@ -74,4 +74,27 @@ __device__ inline float decode(uint32_t code) {
   return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
 }
 
+// x (double) to the float that rounds to the same code: the nearest one, and if
+// that is inexact and its last bit 0, the neighbour on x's side (its last bit is
+// 1).  A later rounding to fewer bits, ties to even, then gives what rounding x
+// at once would: only an exact value can still look like a tie.
+__device__ inline float round_to_odd(double x) {
+  const float f = (float)x;
+  const double rest = x - (double)f;  // exact; NaN for an infinite x, -+inf where f overflowed
+  const int32_t bits = __float_as_int(f);
+  const int32_t step = f == 0.0f || (rest > 0.0) == (f > 0.0f) ? 1 : -1;
+  return (rest > 0.0 || rest < 0.0) && (bits & 1) == 0 ? __int_as_float(bits + step) : f;
+}
+
+// Four codes of y, nearest, ties to even; |y| is at most the largest code.
+template <int FMT>
+__device__ inline uint32_t encode4(float y0, float y1, float y2, float y3) {
+  if (FMT == EFFORT_KV_I8) {
+    auto c = [](float y) { return (uint32_t)(int)__builtin_rintf(y) & 0xFFu; };
+    return c(y0) | c(y1) << 8 | c(y2) << 16 | c(y3) << 24;
+  }
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, w, true);
+}
+
 }  // namespace effort

@@ -73,18 +73,6 @@ __device__ inline void to_order(const float* x, bool pairs, float* y) {
   }
 }
 
-// x (double) to the float that rounds to the same code: the nearest one, and if
-// that is inexact and its last bit 0, the neighbour on x's side (its last bit is
-// 1).  A later rounding to fewer bits, ties to even, then gives what rounding x
-// at once would: only an exact value can still look like a tie.
-__device__ inline float round_to_odd(double x) {
-  const float f = (float)x;
-  const double rest = x - (double)f;  // exact; NaN for an infinite x, -+inf where f overflowed
-  const int32_t bits = __float_as_int(f);
-  const int32_t step = f == 0.0f || (rest > 0.0) == (f > 0.0f) ? 1 : -1;
-  return (rest > 0.0 || rest < 0.0) && (bits & 1) == 0 ? __int_as_float(bits + step) : f;
-}
-
 // The chunk rotated; a key's products and sum are exact to 2^-53, so that its
 // code is the nearest one even where the sum nearly cancels.
 template <typename X>
@@ -104,17 +92,6 @@ __device__ inline int scale_exp(uint32_t amax_bits) {
   const int e = (int)(amax_bits >> 23) - 127 - (FMT == EFFORT_KV_I8 ? 6 : 8) +
                 ((amax_bits & 0x7FFFFFu) > top ? 1 : 0);
   return e < EFFORT_KV_MIN_EXP ? EFFORT_KV_MIN_EXP : e;  // also for zero and subnormals
-}
-
-// Four codes of y, nearest, ties to even; |y| is at most the largest code.
-template <int FMT>
-__device__ inline uint32_t encode4(float y0, float y1, float y2, float y3) {
-  if (FMT == EFFORT_KV_I8) {
-    auto c = [](float y) { return (uint32_t)(int)__builtin_rintf(y) & 0xFFu; };
-    return c(y0) | c(y1) << 8 | c(y2) << 16 | c(y3) << 24;
-  }
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, w, true);
 }
 
 // The rotation of one chunk's queries in fp32: one product and the sum are

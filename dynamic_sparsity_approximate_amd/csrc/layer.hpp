@@ -48,6 +48,37 @@ struct AttendArgs {
   const int32_t* parents;  // launch_attend_tree
 };
 
+// The caches of a model's layers, as many as a launch takes.
+#define EFFORT_KV_SET 64
+struct CacheArgs {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int32_t heads, dim, format, unused;
+};
+struct CacheSet {
+  CacheArgs c[EFFORT_KV_SET];
+  int64_t pages;
+  int32_t count, page_tokens;
+};
+
+// effort_kv_book
+struct BookArgs {
+  int32_t *table, *lens, *refs, *info;
+  int64_t table_stride, pages;
+  int32_t seqs, max_pages, page_tokens;
+};
+
+struct BeamArgs {
+  const void* logits;
+  int64_t stride;  // elements between rows
+  const float* scores;
+  const uint8_t* ended;
+  int32_t items, beams, vocab, keep, end_token;
+  float* out_scores;
+  int32_t *out_parents, *out_tokens;
+  void* ws;
+};
+
 struct NormArgs {
   const void *x, *resid, *post_w, *gate, *pre_w;
   void *resid_out, *out;
@@ -61,6 +92,17 @@ hipError_t launch_append_ex(const AppendArgs& a, int32_t dtype, hipStream_t s);
 uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads);
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_attend_tree(const AttendArgs& a, int32_t dtype, hipStream_t s);
+hipError_t launch_fork(const BookArgs& b, const int32_t* source, const int32_t* keep, hipStream_t s);
+uint64_t grow_workspace(const BookArgs& b);
+hipError_t launch_grow(const BookArgs& b, const effort_kv_cache* caches, int32_t count, const int32_t* more_of,
+                       int32_t more, void* ws, hipStream_t s);
+hipError_t launch_copy(const effort_kv_cache* caches, int32_t count, int64_t n, const int32_t* from, const int32_t* to,
+                       hipStream_t s);
+uint64_t accept_workspace(int32_t seqs);
+hipError_t launch_accept(const effort_kv_cache* caches, int32_t count, const BatchArgs& b, const int32_t* parents,
+                         const int32_t* leaf, int32_t* lens_out, void* ws, hipStream_t s);
+uint64_t beam_workspace(int64_t rows, int64_t vocab);
+hipError_t launch_beam(const BeamArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, int32_t resid_dtype, hipStream_t s);
 
 }  // namespace effort

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = 1ll << 24;
 constexpr int64_t kMaxNorm = 1ll << 20;
+constexpr int64_t kMaxVocab = 1ll << 20;  // tokens count in 20 bits
 constexpr int64_t kMaxIndex = 0x7FFFFFFFll;
 constexpr int64_t kMaxLength = 1ll << 30;  // kernels step past a length in 32 bits
 constexpr int32_t kMaxKvHeads = 256, kMaxGroup = 64;
@@ -58,6 +59,43 @@ BatchArgs batch_args(const effort_kv_batch* b, int64_t pages) {
 
 bool rows_ok(const void* p, int64_t stride, int64_t width, uintptr_t bytes) {
   return p && aligned(p, bytes) && stride >= width;
+}
+
+bool page_tokens_ok(int32_t t) { return t == 16 || t == 32 || t == 64 || t == 128; }
+
+bool book_ok(const effort_kv_book* b) {
+  if (!b || b->seqs < 0 || b->seqs > EFFORT_KV_MAX_SEQS || b->reserved != 0 || !page_tokens_ok(b->page_tokens))
+    return false;
+  if (b->max_pages < 1 || (int64_t)b->max_pages * b->page_tokens > kMaxLength || b->table_stride < b->max_pages ||
+      b->pages < 1 || b->pages > kMaxIndex)
+    return false;
+  if (b->seqs == 0) return true;
+  return b->page_table && b->kv_lens && b->refs && b->info && aligned(b->page_table, 4) && aligned(b->kv_lens, 4) &&
+         aligned(b->refs, 4) && aligned(b->info, 4);
+}
+
+BookArgs book_args(const effort_kv_book* b) {
+  return BookArgs{b->page_table, b->kv_lens, b->refs, b->info, b->table_stride, b->pages, b->seqs, b->max_pages,
+                  b->page_tokens};
+}
+
+// Caches of one number of pages and one page_tokens.
+bool caches_ok(const effort_kv_cache* c, int32_t count) {
+  if (count < 0 || count > EFFORT_KV_MAX_CACHES || (count > 0 && !c)) return false;
+  for (int32_t i = 0; i < count; ++i)
+    if (!cache_ok(c + i) || c[i].pages != c[0].pages || c[i].page_tokens != c[0].page_tokens) return false;
+  return true;
+}
+
+// 0, or why the workspace does not do.
+int space_of(const void* ws, uint64_t bytes, uint64_t need) {
+  if (need && (!ws || !aligned(ws, 256))) return EFFORT_EINVAL;
+  return bytes < need ? EFFORT_ENOSPACE : EFFORT_OK;
+}
+
+bool beam_sizes_ok(int64_t items, int32_t beams, int64_t vocab) {
+  return items >= 0 && items <= kMaxTokens && beams >= 1 && beams <= EFFORT_BEAM_MAX && items * beams <= kMaxTokens &&
+         vocab >= 1 && vocab <= kMaxVocab;
 }
 
 bool heads_ok(int32_t q_heads, int32_t kv_heads) {
@@ -208,6 +246,96 @@ int effort_kv_attention_tree(const effort_kv_cache* cache, const effort_kv_batch
   if ((!parents_dev && batch && batch->seqs > 0 && batch->tokens > 0) || !aligned(parents_dev, 4)) return EFFORT_EINVAL;
   return attention(cache, batch, parents_dev, dtype, q_dev, q_stride, q_heads, scale, window, out_dev, out_stride,
                    ws_dev, ws_bytes, stream);
+}
+
+int effort_kv_fork(const effort_kv_book* book, const int32_t* source_dev, const int32_t* lens_dev, void* stream) {
+  if (!book_ok(book)) return EFFORT_EINVAL;
+  if (book->seqs == 0) return EFFORT_OK;
+  if (!source_dev || !aligned(source_dev, 4) || !aligned(lens_dev, 4)) return EFFORT_EINVAL;
+  return status_of(launch_fork(book_args(book), source_dev, lens_dev, static_cast<hipStream_t>(stream)));
+}
+
+int effort_kv_grow_workspace_bytes(const effort_kv_book* book, uint64_t* bytes) {
+  if (!bytes || !book_ok(book)) return EFFORT_EINVAL;
+  *bytes = grow_workspace(book_args(book));
+  return EFFORT_OK;
+}
+
+int effort_kv_grow(const effort_kv_book* book, const effort_kv_cache* caches, int32_t count,
+                   const int32_t* more_dev, int32_t more, void* ws_dev, uint64_t ws_bytes, void* stream) {
+  if (!book_ok(book) || !caches_ok(caches, count) || !aligned(more_dev, 4)) return EFFORT_EINVAL;
+  if (count > 0 && (caches[0].pages != book->pages || caches[0].page_tokens != book->page_tokens))
+    return EFFORT_EINVAL;
+  if (book->seqs == 0) return EFFORT_OK;
+  const BookArgs b = book_args(book);
+  const int bad = space_of(ws_dev, ws_bytes, grow_workspace(b));
+  if (bad) return bad;
+  return status_of(launch_grow(b, caches, count, more_dev, more, ws_dev, static_cast<hipStream_t>(stream)));
+}
+
+int effort_kv_copy_pages(const effort_kv_cache* caches, int32_t count, const int32_t* from_dev,
+                         const int32_t* to_dev, int64_t n, void* stream) {
+  if (!caches_ok(caches, count) || n < 0 || n > kMaxIndex) return EFFORT_EINVAL;
+  if (count == 0 || n == 0) return EFFORT_OK;
+  if (!from_dev || !to_dev || !aligned(from_dev, 4) || !aligned(to_dev, 4)) return EFFORT_EINVAL;
+  return status_of(launch_copy(caches, count, n, from_dev, to_dev, static_cast<hipStream_t>(stream)));
+}
+
+int effort_kv_accept_workspace_bytes(int32_t seqs, uint64_t* bytes) {
+  if (!bytes || seqs < 0 || seqs > EFFORT_KV_MAX_SEQS) return EFFORT_EINVAL;
+  *bytes = accept_workspace(seqs);
+  return EFFORT_OK;
+}
+
+int effort_kv_accept(const effort_kv_cache* caches, int32_t count, const effort_kv_batch* batch,
+                     const int32_t* parents_dev, const int32_t* leaf_dev, int32_t* lens_out_dev, void* ws_dev,
+                     uint64_t ws_bytes, void* stream) {
+  if (count < 1 || !caches_ok(caches, count) || !batch_ok(batch, caches[0].page_tokens)) return EFFORT_EINVAL;
+  if (batch->seqs == 0) return EFFORT_OK;
+  if (batch->tokens == 0 && (!batch->kv_lens || !batch->q_starts || !batch->page_table)) return EFFORT_EINVAL;
+  if (!leaf_dev || !lens_out_dev || !aligned(leaf_dev, 4) || !aligned(lens_out_dev, 4) || !aligned(parents_dev, 4))
+    return EFFORT_EINVAL;
+  if (parents_dev) {
+    const int bad = space_of(ws_dev, ws_bytes, accept_workspace(batch->seqs));
+    if (bad) return bad;
+  }
+  return status_of(launch_accept(caches, count, batch_args(batch, caches[0].pages), parents_dev, leaf_dev, lens_out_dev,
+                                 ws_dev, static_cast<hipStream_t>(stream)));
+}
+
+int effort_beam_workspace_bytes(int64_t items, int32_t beams, int64_t vocab, uint64_t* bytes) {
+  if (!bytes || !beam_sizes_ok(items, beams, vocab)) return EFFORT_EINVAL;
+  *bytes = items == 0 ? 0 : beam_workspace(items * beams, vocab);
+  return EFFORT_OK;
+}
+
+int effort_beam_select(int32_t dtype, const void* logits_dev, int64_t stride, const float* scores_dev,
+                       const uint8_t* ended_dev, int32_t end_token, int64_t items, int32_t beams, int64_t vocab,
+                       int32_t keep, float* out_scores_dev, int32_t* out_parents_dev, int32_t* out_tokens_dev,
+                       void* ws_dev, uint64_t ws_bytes, void* stream) {
+  if (!dtype_ok(dtype) || !beam_sizes_ok(items, beams, vocab) || keep < 1 || keep > EFFORT_BEAM_MAX_KEEP)
+    return EFFORT_EINVAL;
+  if (items == 0) return EFFORT_OK;  // nothing to do: the arrays may be null
+  if (!rows_ok(logits_dev, stride, vocab, bytes_of(dtype)) || !scores_dev || !aligned(scores_dev, 4)) return EFFORT_EINVAL;
+  for (const void* p : {(const void*)out_scores_dev, (const void*)out_parents_dev, (const void*)out_tokens_dev})
+    if (!p || !aligned(p, 4)) return EFFORT_EINVAL;
+  const int bad = space_of(ws_dev, ws_bytes, beam_workspace(items * beams, vocab));
+  if (bad) return bad;
+  BeamArgs a;
+  a.logits = logits_dev;
+  a.stride = stride;
+  a.scores = scores_dev;
+  a.ended = ended_dev;
+  a.items = (int32_t)items;
+  a.beams = beams;
+  a.vocab = (int32_t)vocab;
+  a.keep = keep;
+  a.end_token = end_token;
+  a.out_scores = out_scores_dev;
+  a.out_parents = out_parents_dev;
+  a.out_tokens = out_tokens_dev;
+  a.ws = ws_dev;
+  return status_of(launch_beam(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
 int effort_norm_residual(int32_t dtype, int64_t rows, int64_t n, const void* x_dev, int64_t x_stride,

@@ -501,6 +501,113 @@ int effort_kv_attention_tree(const effort_kv_cache* cache, const effort_kv_batch
                              int32_t q_heads, float scale, int32_t window, void* out_dev, int64_t out_stride,
                              void* ws_dev, uint64_t ws_bytes, void* stream);
 
+/* Who holds the pages of a set of caches (a model's layers: one page id stands
+   for that page in each of them).  An entry of the table outside [0, pages)
+   holds nothing; refs[p] is the number of entries that hold page p, in all the
+   tables that share refs.  Entries behind a sequence's end are pages that it
+   keeps for later tokens. */
+typedef struct effort_kv_book {
+  int32_t seqs;         /* 0..EFFORT_KV_MAX_SEQS */
+  int32_t max_pages;    /* columns of the page table; max_pages * page_tokens <= 2^30 */
+  int32_t page_tokens;  /* 16, 32, 64 or 128 */
+  int32_t reserved;     /* 0 */
+  int64_t pages;        /* 1..2^31 - 1 */
+  int64_t table_stride; /* elements between the rows of the page table, >= max_pages */
+  int32_t* page_table;  /* device [seqs][max_pages] */
+  int32_t* kv_lens;     /* device [seqs] */
+  int32_t* refs;        /* device [pages] */
+  int32_t* info;        /* device [4], zero at first; info[0]: pages missing at the last effort_kv_grow;
+                           the others are the library's */
+} effort_kv_book;
+#define EFFORT_KV_MAX_CACHES 4096 /* caches of one call */
+
+/* Sequence s becomes a copy of sequence source_dev[s] as it was before the
+   call, cut to its first lens_dev[s] tokens (lens_dev NULL: uncut; a number
+   beyond its length does not lengthen it, a negative one counts as 0): its
+   length, and the pages that hold these tokens; no entry behind them stays.  A
+   source outside [0, seqs) leaves the sequence empty.  Pages are shared, not
+   copied: refs follows, and a page whose count becomes 0 is free. */
+int effort_kv_fork(const effort_kv_book* book, const int32_t* source_dev, const int32_t* lens_dev, void* stream);
+
+/* Room for more_dev[s] (NULL: `more`) new tokens of each sequence: lengths grow
+   by it (by nothing where it is negative), and every column that the new tokens
+   fall into gets a page that no other entry holds:
+    - the page that holds the sequence's last tokens, where it is not full, is
+      kept if no other entry holds it; else its first kv_lens mod page_tokens
+      slots and its scales are copied to a free page, in all the caches.  If all
+      its holders are such pages of sequences that grow in this call, the last
+      of these keeps it;
+    - an entry of a later column is kept if no other entry holds its page;
+    - an absent page (outside [0, pages)) of a column that holds older tokens
+      stays absent.
+   Free pages, those of count 0, are given out in the order of sequences and
+   columns, the lowest first.  If there are too few, or a sequence would grow
+   beyond its table, nothing changes and info[0] says how many pages are missing
+   (else 0): the new tokens must then not be appended.
+   caches: host array of `count` caches of the book's pages and page_tokens (0:
+   no copies).  ws_dev: 256-byte aligned, of effort_kv_grow_workspace_bytes. */
+int effort_kv_grow_workspace_bytes(const effort_kv_book* book, uint64_t* bytes);
+int effort_kv_grow(const effort_kv_book* book, const effort_kv_cache* caches, int32_t count,
+                   const int32_t* more_dev, int32_t more, void* ws_dev, uint64_t ws_bytes, void* stream);
+
+/* Copies pages from_dev[i] to to_dev[i], i < n, codes and scales, in each of the
+   caches (of one number of pages and one page_tokens).  Pairs with an id outside
+   [0, pages) or of one page are passed over.  No page may be written twice, nor
+   be written and read. */
+int effort_kv_copy_pages(const effort_kv_cache* caches, int32_t count, const int32_t* from_dev,
+                         const int32_t* to_dev, int64_t n, void* stream);
+
+/* Of each sequence's new tokens keeps a path of their tree (parents_dev as in
+   effort_kv_append_ex; NULL: each continues the one before it): leaf_dev[s], a
+   number among its new tokens, its ancestors and the committed tokens; with a
+   leaf outside [0, n) the committed tokens alone.  A path ends in front of its
+   first token that is in no page, or would be in none.  Its tokens move to the
+   slots of the positions base, base + 1, ... of every cache, and lens_out_dev[s],
+   which may be batch->kv_lens, becomes base plus their number (for a sequence
+   that is no tree, or has no new tokens, kv_lens[s]).  Keys were rotated by
+   those positions and do not change.  A page that gets tokens of another page
+   takes the scale that effort_kv_append would give it for their values: the
+   larger of its own and the least power of two that they need; if it grows, the
+   page's older tokens and its own of the path become the nearest codes to their
+   values, and the others' are the nearest codes in any case.  Tokens of a
+   poisoned page poison a page that they move to.  Slots behind the path, and
+   pages that get no token, stay as they were.
+   caches: host array of `count` caches of one number of pages and one
+   page_tokens, whose pages with new tokens stand in one table once.  ws_dev:
+   256-byte aligned, of effort_kv_accept_workspace_bytes(seqs) (unused without
+   parents). */
+int effort_kv_accept_workspace_bytes(int32_t seqs, uint64_t* bytes);
+int effort_kv_accept(const effort_kv_cache* caches, int32_t count, const effort_kv_batch* batch,
+                     const int32_t* parents_dev, const int32_t* leaf_dev, int32_t* lens_out_dev, void* ws_dev,
+                     uint64_t ws_bytes, void* stream);
+
+#define EFFORT_BEAM_MAX 64       /* beams of an item */
+#define EFFORT_BEAM_MAX_KEEP 128 /* continuations that are kept */
+
+/* Beam search's selection.  Row i * beams + b of the logits belongs to beam b of
+   item i, scores_dev [items][beams] are the beams' scores so far.  Of an item's
+   candidates (b, t), t < vocab, the `keep` best by
+     scores[b] + logit[b][t] - log(sum_u exp(logit[b][u])),
+   the best first: the score rounded once to out_scores, the row i * beams + b in
+   out_parents, t in out_tokens, each [items][keep].  Scores are compared in
+   double, the logarithm's sum has 2^-22 or less of error; equal scores stand in
+   the order of beams, a beam's by falling logits, and equal logits by rising
+   tokens.  A beam with ended_dev[b] != 0 has one candidate: itself, with its
+   score unchanged and the token end_token.  A logit of -inf is no candidate; a
+   row with a NaN, +inf or nothing but -inf, or with a score that is not finite,
+   has none.  Where there are fewer than `keep`, the rest are -inf, -1, -1.
+   Logits: of `dtype`, `stride` elements between rows.  EINVAL: null or misaligned
+   pointers, items outside 0..2^24, beams outside 1..EFFORT_BEAM_MAX (2^24 rows
+   at most), keep outside 1..EFFORT_BEAM_MAX_KEEP, vocab outside 1..2^20, a
+   stride below vocab.  ended_dev may be NULL; out_scores_dev may be scores_dev
+   if keep == beams, no other overlap of an output is allowed.  ws_dev: 256-byte aligned, of
+   effort_beam_workspace_bytes. */
+int effort_beam_workspace_bytes(int64_t items, int32_t beams, int64_t vocab, uint64_t* bytes);
+int effort_beam_select(int32_t dtype, const void* logits_dev, int64_t stride, const float* scores_dev,
+                       const uint8_t* ended_dev, int32_t end_token, int64_t items, int32_t beams, int64_t vocab,
+                       int32_t keep, float* out_scores_dev, int32_t* out_parents_dev, int32_t* out_tokens_dev,
+                       void* ws_dev, uint64_t ws_bytes, void* stream);
+
 /* The end of one block and the start of the next, for rows x[rows][n]:
      t = x / rms(x) * post_w     (post_w NULL: t = x)
      r = resid + scale * gate * t  (resid NULL: no sum; gate NULL: 1)
