@@ -143,6 +143,7 @@ _PROTOS = {
     "effort_kv_attention_tree": ([_KC, _KB, _p, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
                                  ctypes.c_int),
     "effort_kv_workspace_bytes": ([_KC, _i32, _i64, _i32, ctypes.POINTER(_u64)], ctypes.c_int),
+    "effort_kv_tree_workspace_bytes": ([_KC, _i32, _i64, _i32, ctypes.POINTER(_u64)], ctypes.c_int),
     "effort_kv_attention": ([_KC, _KB, _i32, _p, _i64, _i32, _f32, _i32, _p, _i64, _p, _u64, _p],
                             ctypes.c_int),
     "effort_kv_fork": ([_KP, _p, _p, _p], ctypes.c_int),
@@ -463,6 +464,13 @@ def effort_kv_attention(cache, batch, dtype: int, q, q_stride: int, q_heads: int
     _check(_lib.effort_kv_attention(ctypes.byref(cache), ctypes.byref(batch), dtype, _ptr(q), q_stride, q_heads,
                                     scale, window, _ptr(out), out_stride, _ptr(ws), ws_bytes, _stream(stream)),
            "effort_kv_attention")
+
+
+def effort_kv_tree_workspace_bytes(cache, seqs: int, tokens: int, q_heads: int) -> int:
+    b = _u64()
+    _check(_lib.effort_kv_tree_workspace_bytes(ctypes.byref(cache), seqs, tokens, q_heads, ctypes.byref(b)),
+           "effort_kv_tree_workspace_bytes")
+    return int(b.value)
 
 
 def effort_kv_attention_tree(cache, batch, parents, dtype: int, q, q_stride: int, q_heads: int, scale: float,

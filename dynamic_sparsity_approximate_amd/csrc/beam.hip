@@ -23,9 +23,9 @@ constexpr int BM_T = 256;                // threads of a reading block
 constexpr int BP_T = 1024;               // of a picking one
 constexpr int BM_SMALL = 512, BM_LARGE = 2048;  // logits of a wave, for few rows and for many
 
-// Workspace: maxima of groups [rows][groups], then (maximum, sum) of waves [rows][parts].
+// Workspace: maxima of groups [rows][groups], then the parts of waves [rows][parts].
 struct Part {
-  double sum;  // of exp(x - top)
+  double sum;  // of exp(x - ref_of(top))
   float top, unused;
 };
 static int64_t groups_of(int64_t vocab) { return (vocab + BM_GROUP - 1) / BM_GROUP; }
@@ -39,18 +39,20 @@ uint64_t beam_workspace(int64_t rows, int64_t vocab) {
 
 // ---------------------------------------------------------------- reading
 
-// exp(t) for t <= 0 to about an ulp: t log2(e) as a sum of two floats, the smaller one's
-// effect to first order.
-__device__ inline float exp_near(float t) {
-  const float hi = t * 1.4426950408889634f;
-  const float lo = __builtin_fmaf(t, 1.4426950408889634f, -hi) + t * 1.925963033500995e-8f;  // log2(e) beyond fp32
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return hi < -150.0f ? 0.0f : __builtin_fmaf(e, lo * 0.6931471805599453f, e);  // a NaN stays one
-}
+// NaN-propagating.
+__device__ inline float top_of(float x, float y) { return __builtin_elementwise_maximum(x, y); }
 
 template <int CTRL>
 __device__ inline float dpp_top(float x) {
-  return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), CTRL, 0xF, 0xF, false)));
+  return top_of(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), CTRL, 0xF, 0xF, false)));
+}
+
+constexpr float kHi = 1.4426950408889634f, kLo = 1.925963033500995e-8f;  // log2(e)
+// What a wave's exponentials are relative to: about its largest number, as a power of two
+// that fp32 has; numbers whose products would overflow, and -inf and NaN, stand for themselves.
+__device__ inline bool has_power(float top) { return fabsf(top) <= 0x1p120f; }
+__device__ inline double ref_of(float top) {
+  return has_power(top) ? (double)(top * kHi) * 0.6931471805599453 : (double)top;
 }
 
 // N elements at any address of T's alignment.
@@ -64,8 +66,9 @@ __device__ inline void load_any(const T* p, float* x) {
   for (int i = 0; i < N; ++i) x[i] = (float)t.e[i];
 }
 
-// Waits for memory where there are many rows.  A wave works alone: nothing in here waits for
-// another one.
+// A wave works alone: nothing in here waits for another one.  An exponential is two
+// products, exact but for 2^-24 of the exponent, whose reference is a number of base 2
+// that the sum is kept with, and the instruction's ulp.
 template <int DT, int WAVE>
 __global__ __launch_bounds__(BM_T) void k_beam_read(BeamArgs a, float* maxima, Part* parts, int64_t first, int64_t waves,
                                                     int64_t per_row, int64_t groups) {
@@ -96,11 +99,11 @@ __global__ __launch_bounds__(BM_T) void k_beam_read(BeamArgs a, float* maxima, P
   for (int it = 0; it < IT; ++it) {
     float t = y[it][0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) t = fmaxf(t, y[it][i]);
+    for (int i = 1; i < N; ++i) t = top_of(t, y[it][i]);
     t = dpp_top<0xB1>(t);                    // quad_perm 1032
     t = dpp_top<0x4E>(t);                    // quad_perm 2301
     if (LANES == 8) t = dpp_top<0x141>(t);   // row_half_mirror
-    top = fmaxf(top, t);
+    top = top_of(top, t);
     if ((lane & (LANES - 1)) == it % LANES) out = t;
     if (it % LANES == LANES - 1 || it == IT - 1) {  // lane i of a group has the maximum of the i-th of these pieces
       const int my = it - it % LANES + (lane & (LANES - 1));
@@ -109,19 +112,27 @@ __global__ __launch_bounds__(BM_T) void k_beam_read(BeamArgs a, float* maxima, P
     }
   }
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float ref = top == -INFINITY ? 0.0f : top;
+  for (int d = 32; d >= 1; d >>= 1) top = top_of(top, __shfl_xor(top, d));
   double sum = 0.0;
+  if (has_power(top)) {
+    const float c = top * kHi;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    float s[N];
+    for (int it = 0; it < IT; ++it) {
+      float s[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = exp_near(y[it][i] - ref);
+      for (int i = 0; i < N; ++i)
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[it][i], kLo, __builtin_fmaf(y[it][i], kHi, -c)));
 #pragma unroll
-    for (int d = N / 2; d >= 1; d >>= 1)
+      for (int d = N / 2; d >= 1; d >>= 1)
 #pragma unroll
-      for (int i = 0; i < d; ++i) s[i] += s[i + d];
-    sum += (double)s[0];
+        for (int i = 0; i < d; ++i) s[i] += s[i + d];
+      sum += (double)s[0];
+    }
+  } else if (top != -INFINITY) {  // (inf - inf is a NaN)
+#pragma unroll
+    for (int it = 0; it < IT; ++it)
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += (double)expf(y[it][i] - top);
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
@@ -153,30 +164,40 @@ __device__ inline uint64_t low_of(int beam, float logit, uint32_t at) {
 
 constexpr int BP_LIST = 4224;  // room of a list: all elements of EFFORT_BEAM_MAX_KEEP groups, and ended beams
 constexpr int BP_STEP = 2048;  // groups between two looks at the list's length
+constexpr int BP_RUNS = 2048;  // room for runs
+constexpr int BP_FLY = 4;      // maxima of a thread that are on their way together
+constexpr int BP_BITS = 14;    // bits of the first bound that are not looked for
 static_assert(EFFORT_BEAM_MAX_KEEP * BM_GROUP + EFFORT_BEAM_MAX <= BP_LIST, "the list holds them");
 static_assert(EFFORT_BEAM_MAX_KEEP + BP_STEP <= BP_LIST, "the list takes a step more");
 static_assert(EFFORT_BEAM_MAX <= 64, "six bits of a beam");
 
-// Calls put(rank, candidate) for each of the list's `n` that has a rank below `keep`.
+// Calls put(rank, candidate) for each of the list's `n` that has a rank below `keep`; 32
+// lanes compare one candidate with the others.
 template <typename Put>
 __device__ inline void rank_list(const Cand* list, int n, int keep, Put put) {
-  for (int i = (int)threadIdx.x; i < n; i += BP_T) {
-    const Cand c = list[i];
+  const int lane = (int)threadIdx.x & 31, high = (int)threadIdx.x & 32;
+  for (int i0 = 0; i0 < n; i0 += BP_T / 32) {
+    const int i = i0 + ((int)threadIdx.x >> 5);
+    const Cand c = list[i < n ? i : 0];
     int rank = 0;
-    for (int j = 0; j < n && rank < keep; ++j) rank += list[j] > c;
-    if (rank < keep) put(rank, c);
+    for (int j = 0; j < n; j += 32) {
+      const uint64_t above = __ballot(j + lane < n && list[j + lane < n ? j + lane : 0] > c);
+      rank += __popc((uint32_t)(above >> high));
+    }
+    if (i < n && rank < keep && lane == 0) put(rank, c);
   }
 }
 
 template <int DT>
 __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* maxima, const Part* parts, int32_t per_row,
-                                                    int32_t groups) {
+                                                    int32_t groups, int32_t wave_size) {
   typedef typename ElemOf<DT>::T T;
   __shared__ Cand s_list[BP_LIST], s_best[EFFORT_BEAM_MAX_KEEP];
   __shared__ double s_add[EFFORT_BEAM_MAX];  // score minus log of the sum; -inf: continues nothing
+  __shared__ float s_near[EFFORT_BEAM_MAX], s_reach[EFFORT_BEAM_MAX];
   __shared__ uint32_t s_top[BP_T / 4];
-  __shared__ uint32_t s_least;
-  __shared__ int s_n;
+  __shared__ int s_n, s_runs;
+  __shared__ int32_t s_run[BP_RUNS];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, beams = a.beams, keep = a.keep;
   const int64_t row0 = (int64_t)blockIdx.x * beams;
   auto live = [&](int b) {
@@ -185,73 +206,107 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
 
   // a wave for each beam: the sum over its parts
   for (int b = wave; b < beams; b += BP_T / 64) {
-    double add = -INFINITY;
-    if (live(b)) {
-      const Part* p = parts + (row0 + b) * per_row;
-      float top = -INFINITY;
-      for (int i = lane; i < per_row; i += 64) top = fmaxf(top, p[i].top);
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      double sum = 0.0;
-      for (int i = lane; i < per_row; i += 64) {
-        const Part q = p[i];
-        sum += q.top == -INFINITY ? q.sum : q.sum * exp((double)q.top - (double)top);
-      }
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-      // all of a row forbidden (0), a NaN or an infinity among it (NaN)
-      if (sum > 0.0 && top < INFINITY) add = (double)a.scores[row0 + b] - ((double)top + log(sum));
+    const Part* p = parts + (row0 + b) * per_row;
+    const Part mine = p[lane < per_row ? lane : 0];  // on its way with the score
+    const bool lives = live(b);
+    auto part = [&](int i) { return i < 64 ? mine : p[i]; };
+    double ref = -INFINITY, sum = 0.0;
+    bool bad = !lives;
+    for (int i = lane; lives && i < per_row; i += 64) {
+      const Part q = part(i);
+      bad = bad || q.sum != q.sum;  // a NaN or an infinity among the logits
+      if (q.sum > 0.0 && ref_of(q.top) > ref) ref = ref_of(q.top);
     }
-    if (lane == 0) s_add[b] = add;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const double o = __shfl_xor(ref, d);
+      ref = o > ref ? o : ref;
+    }
+    for (int i = lane; lives && i < per_row; i += 64) {
+      const Part q = part(i);
+      if (q.sum > 0.0) sum += q.sum * exp(ref_of(q.top) - ref);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    // (0 where all of the row is forbidden)
+    const double add = !__any(bad) && sum > 0.0 ? (double)a.scores[row0 + b] - (ref + log(sum)) : -INFINITY;
+    if (lane == 0) {
+      s_add[b] = add;
+      s_near[b] = add > -INFINITY ? fmaxf((float)add, -3.4e38f) : -INFINITY;
+    }
   }
   __syncthreads();
 
-  const int n = beams * groups;  // at most 2^21
-  auto group = [&](int i, Cand* c) {  // whether group i of the item holds a candidate, and its best
-    const int b = i / groups, g = i - b * groups;
-    const double add = s_add[b];
-    if (!(add > -INFINITY)) return false;
-    const float x = maxima[(row0 + b) * groups + g];
-    if (!(x > -INFINITY)) return false;
-    *c = Cand{order_of(add + (double)x), low_of(b, x, (uint32_t)g)};
-    return true;
+  // Runs of neighbouring groups: those of a reading wave, or single groups where there are
+  // not many runs for each that is kept.  A first bound, a little too low: of the largest
+  // scores that four threads see together, in 32 bits, the keep-th.  Its bits, but for the
+  // last ones, are found by one wave.
+  const bool coarse = beams * per_row >= 4 * keep;
+  const int runs = coarse ? per_row : groups, n = beams * runs;  // at most 2^21
+  auto largest = [&](int i) {
+    return coarse ? parts[row0 * per_row + i].top : maxima[row0 * groups + i];
   };
-  // A first bound: of the largest scores that four threads see together, rounded to 32
-  // bits, the keep-th (rounding keeps the order).  Its bits are found by one wave.
-  uint32_t top = 0;
-  for (int i = tid; i < n; i += BP_T) {
-    Cand c;
-    if (!group(i, &c)) continue;
-    const uint32_t o = order_of((float)number_of(c.hi));
-    top = o > top ? o : top;
-  }
-  for (int d = 1; d <= 2; d <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
-    top = o > top ? o : top;
-  }
+  // do(largest, beam, run) for the runs i0 .. i1 - 1; neighbours fall to different fours of threads
+  auto each_run = [&](int i0, int i1, auto run) __attribute__((always_inline)) {
+    const int own = (tid >> 2) + (tid & 3) * (BP_T / 4);
+    int b = (i0 + own) / runs, r = i0 + own - b * runs;
+    const int db = BP_T / runs, dr = BP_T % runs;
+    for (int i = i0 + own; i < i1; i += BP_FLY * BP_T) {
+      float x[BP_FLY];
+#pragma unroll
+      for (int u = 0; u < BP_FLY; ++u) x[u] = i + u * BP_T < i1 ? largest(i + u * BP_T) : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < BP_FLY; ++u) {
+        if (i + u * BP_T < i1) run(x[u], b, r);
+        b += db;
+        r += dr;
+        if (r >= runs) {
+          r -= runs;
+          ++b;
+        }
+      }
+    }
+  };
+  float best = -INFINITY;
+  each_run(0, n, [&](float x, int b, int) __attribute__((always_inline)) { best = fmaxf(best, x + s_near[b]); });
+  best = fmaxf(best, __shfl_xor(best, 1));
+  best = fmaxf(best, __shfl_xor(best, 2));
+  const uint32_t top = order_of(best);
   if ((tid & 3) == 0) s_top[tid >> 2] = top;
-  if (tid == 0) s_n = 0;
+  if (tid == 0) s_n = s_runs = 0;
   __syncthreads();
   if (wave == 0) {
     uint32_t mine[BP_T / 256];
 #pragma unroll
     for (int u = 0; u < BP_T / 256; ++u) mine[u] = s_top[u * 64 + lane];
-    uint32_t least = 0;  // the largest number that `keep` of them reach
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = least | 1u << bit;
-      int count = 0;
+    uint32_t least = 0;  // the largest number that `keep` of them reach, two bits at a time
+    for (int bit = 30; bit >= BP_BITS; bit -= 2) {
+      uint32_t next = least;
 #pragma unroll
-      for (int u = 0; u < BP_T / 256; ++u) count += __popcll(__ballot(mine[u] >= t));
-      if (count >= keep) least = t;
+      for (uint32_t t = 1; t <= 3; ++t) {
+        int count = 0;
+#pragma unroll
+        for (int u = 0; u < BP_T / 256; ++u) count += __popcll(__ballot(mine[u] >= (least | t << bit)));
+        if (count >= keep) next = least | t << bit;
+      }
+      least = next;
     }
-    if (lane == 0) s_least = least;
+    // By beam (a lane each), what a group's maximum has to be: less by more than the
+    // roundings, 2^-24 of each of the numbers, of any beam.  A NaN lets nothing pass.
+    const bool any = least > order_of(-INFINITY);
+    const float bound = fminf(__uint_as_float(least >> 31 ? least & 0x7FFFFFFFu : ~least), 3.0e38f);
+    const float add = lane < beams ? s_near[lane] : -INFINITY;
+    float most = add > -INFINITY ? fabsf(add) : 0.0f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+    const float at = any ? bound - add - 0x1p-20f * (fabsf(bound) + most) : -INFINITY;
+    if (lane < beams) s_reach[lane] = add > -INFINITY ? at : __uint_as_float(0x7FC00000u);
   }
   __syncthreads();
-  const uint32_t least = s_least;
 
-  // the groups that reach it, and as the list fills up only those that beat its keep-th
+  // the groups that reach it, and where they are too many only those that beat the keep-th so far
   Cand bound = {0, 0};
-  auto shrink = [&]() {  // to the list's `keep` best, in order
+  auto shrink = [&]() __attribute__((always_inline)) {  // to the list's `keep` best, in order
     const int count = s_n;
     rank_list(s_list, count, keep, [&](int rank, const Cand& c) { s_best[rank] = c; });
     __syncthreads();
@@ -261,14 +316,40 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     if (left == keep) bound = s_best[keep - 1];
     __syncthreads();
   };
-  for (int i0 = 0; i0 < n; i0 += BP_STEP) {
-#pragma unroll
-    for (int u = 0; u < BP_STEP / BP_T; ++u) {
-      const int i = i0 + u * BP_T + tid;
-      Cand c;
-      if (i < n && group(i, &c) && order_of((float)number_of(c.hi)) >= least && c > bound) s_list[atomicAdd(&s_n, 1)] = c;
-    }
-    if (i0 + BP_STEP < n) {
+  auto take = [&](float x, int b, int g) __attribute__((always_inline)) {
+    if (!(x >= s_reach[b]) || x == -INFINITY) return;
+    const Cand c = {order_of(s_add[b] + (double)x), low_of(b, x, (uint32_t)g)};
+    if (!(c > bound)) return;
+    const int at = atomicAdd(&s_n, 1);
+    if (at < BP_LIST) s_list[at] = c;
+  };
+  if (coarse) {
+    each_run(0, n, [&](float x, int b, int r) __attribute__((always_inline)) {
+      if (!(x >= s_reach[b]) || x == -INFINITY) return;
+      const int at = atomicAdd(&s_runs, 1);
+      if (at < BP_RUNS) s_run[at] = b << 16 | r;
+    });
+    __syncthreads();
+    const int each = wave_size / BM_GROUP, found = s_runs;
+    if (found <= BP_RUNS)
+      for (int i = tid / each; i < found; i += BP_T / each) {
+        const int b = s_run[i] >> 16, g = (s_run[i] & 0xFFFF) * each + tid % each;
+        if (g < groups) take(maxima[(row0 + b) * groups + g], b, g);
+      }
+    __syncthreads();
+    if (found > BP_RUNS && tid == 0) s_n = BP_LIST + 1;
+  } else {
+    each_run(0, n, take);
+  }
+  __syncthreads();
+  if (s_n > BP_LIST) {  // too many alike: step by step
+    __syncthreads();
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    const int all = beams * groups;
+    for (int i0 = 0; i0 < all; i0 += BP_STEP) {
+      for (int i = i0 + tid; i < i0 + BP_STEP && i < all; i += BP_T)
+        take(maxima[row0 * groups + i], i / groups, i % groups);
       __syncthreads();
       if (s_n > BP_LIST - BP_STEP) shrink();
       __syncthreads();
@@ -331,7 +412,7 @@ static hipError_t beam_wave(const BeamArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((k_beam_pick<DT>), dim3((unsigned)a.items), dim3(BP_T), 0, s, a, maxima, parts, (int32_t)per_row,
-                     (int32_t)groups);
+                     (int32_t)groups, WAVE);
   return hipGetLastError();
 }
 

@@ -42,6 +42,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 constexpr int AT_T = 256, AT_W = AT_T / 64;
 constexpr int AT_TILE = 32;              // tokens of one step of a wave
 constexpr int AT_CHUNK = AT_W * AT_TILE; // tokens of one step of a block
+constexpr int PR_TILE = 64;              // tokens of one step of a block whose waves share them
 constexpr float kLog2e = 1.4426950408889634f;
 // Weights are held times 2^6 relative to a row's reference score, which follows
 // the row's maximum only when that is 2^8 times larger (most steps then rescale
@@ -165,13 +166,15 @@ __device__ inline uint64_t line_bits(const Sight& see, const Branch& br, const i
 struct Seq {
   int32_t first, n;   // its rows of q
   int64_t pos;        // position of its first new token
-  int32_t lo, hi;     // tokens that any row sees, lo a multiple of AT_TILE
+  int32_t lo, hi;     // tokens that any row sees, lo a multiple of AT_TILE at least
   int32_t tiles;      // row tiles of `rows` rows
-  int32_t chunks;     // of AT_CHUNK tokens
+  int32_t chunks;
 };
 
-template <bool TREE>
+// Chunks of CH tokens: AT_CHUNK, or PR_TILE (then lo is a multiple of that).
+template <bool TREE, int CH>
 __device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
+  constexpr int ALIGN = CH < AT_CHUNK ? CH : AT_TILE;
   Seq q;
   const int32_t s0 = start_of(a.b, s), s1 = start_of(a.b, s + 1);
   q.first = s0;
@@ -184,18 +187,21 @@ __device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
   q.chunks = 0;
   q.lo = q.hi = 0;
   if (q.n > 0 && to > from && (!TREE || is_tree(q.n, q.pos))) {
-    q.lo = (int32_t)(from & ~(int64_t)(AT_TILE - 1));
+    q.lo = (int32_t)(from & ~(int64_t)(ALIGN - 1));
     q.hi = (int32_t)to;
-    q.chunks = (int32_t)((to - q.lo + AT_CHUNK - 1) / AT_CHUNK);
+    q.chunks = (int32_t)((to - q.lo + CH - 1) / CH);
   }
   return q;
 }
 
-template <bool TREE>
+template <bool TREE, int CH>
 __device__ inline uint64_t chunks_of(const AttendArgs& a, int s, int group, int rows) {
-  const Seq q = seq_of<TREE>(a, s, group, rows);
+  const Seq q = seq_of<TREE, CH>(a, s, group, rows);
   return (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
 }
+
+// Blocks that share a call's chunks: no block has nothing.
+__device__ inline uint64_t sharing_blocks(uint64_t steps, uint32_t grid) { return steps < grid ? steps : grid; }
 
 // Chunks before the sequences, one entry for `per` of them (one each up to 256
 // sequences); every block computes it from the lengths, so that a captured call
@@ -207,13 +213,13 @@ struct Plan {
 __device__ inline int per_entry(const AttendArgs& a) { return (a.b.seqs + AT_T - 1) / AT_T; }
 
 // Returns all sequences' chunks; for one sequence that is all there is to know.
-template <bool TREE>
+template <bool TREE, int CH>
 __device__ uint64_t make_plan(const AttendArgs& a, int group, int rows, Plan* p) {
-  if (a.b.seqs == 1) return chunks_of<TREE>(a, 0, group, rows);
+  if (a.b.seqs == 1) return chunks_of<TREE, CH>(a, 0, group, rows);
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, per = per_entry(a);
   uint64_t sum = 0;
   for (int i = 0; i < per; ++i)
-    if (tid * per + i < a.b.seqs) sum += chunks_of<TREE>(a, tid * per + i, group, rows);
+    if (tid * per + i < a.b.seqs) sum += chunks_of<TREE, CH>(a, tid * per + i, group, rows);
   uint64_t run = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -231,17 +237,17 @@ __device__ uint64_t make_plan(const AttendArgs& a, int group, int rows, Plan* p)
 }
 
 // Chunks before sequence s.
-template <bool TREE>
+template <bool TREE, int CH>
 __device__ inline uint64_t start_of_seq(const AttendArgs& a, const Plan& p, int s, int group, int rows) {
   if (a.b.seqs == 1) return 0;
   const int per = per_entry(a);
   uint64_t c = p.before[s / per];
-  for (int i = s / per * per; i < s; ++i) c += chunks_of<TREE>(a, i, group, rows);
+  for (int i = s / per * per; i < s; ++i) c += chunks_of<TREE, CH>(a, i, group, rows);
   return c;
 }
 
 // The sequence that owns chunk c (of those that have chunks), at or after `from`.
-template <bool TREE>
+template <bool TREE, int CH>
 __device__ inline int owner(const AttendArgs& a, const Plan& p, uint64_t c, int group, int rows) {
   if (a.b.seqs == 1) return 0;
   const int per = per_entry(a);
@@ -253,7 +259,7 @@ __device__ inline int owner(const AttendArgs& a, const Plan& p, uint64_t c, int 
   int s = lo * per;
   uint64_t at = p.before[lo];
   for (;;) {
-    const uint64_t n = chunks_of<TREE>(a, s, group, rows);
+    const uint64_t n = chunks_of<TREE, CH>(a, s, group, rows);
     if (c < at + n || s + 1 >= a.b.seqs) return s;
     at += n;
     ++s;
@@ -306,16 +312,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
       if (s >= a.b.seqs) return;
     }
   } else {
-    const uint64_t total = make_plan<TREE>(a, group, ROWS, &s_plan);
-    const uint64_t nb = total < gridDim.x ? total : gridDim.x;  // no block has nothing
+    const uint64_t total = make_plan<TREE, AT_CHUNK>(a, group, ROWS, &s_plan);
+    const uint64_t nb = sharing_blocks(total, gridDim.x);
     if (blockIdx.x >= nb) return;
     c = total * blockIdx.x / nb;
     c_end = total * (blockIdx.x + 1) / nb;
-    s = __builtin_amdgcn_readfirstlane(owner<TREE>(a, s_plan, c, group, ROWS));
+    s = __builtin_amdgcn_readfirstlane(owner<TREE, AT_CHUNK>(a, s_plan, c, group, ROWS));
   }
-  uint64_t s_start = WHOLE ? 0 : start_of_seq<TREE>(a, s_plan, s, group, ROWS);
+  uint64_t s_start = WHOLE ? 0 : start_of_seq<TREE, AT_CHUNK>(a, s_plan, s, group, ROWS);
   while (c < c_end) {
-    const Seq q = seq_of<TREE>(a, s, group, ROWS);
+    const Seq q = seq_of<TREE, AT_CHUNK>(a, s, group, ROWS);
     int head, tile;
     uint32_t ch0 = 0, take = 1;
     if (WHOLE) {
@@ -737,10 +743,9 @@ __device__ void join_row(int count, int rows, int r, At at, T* out) {
 // Joins the parts that blocks left of an item, and writes the rows that see
 // nothing.  One block per (R rows, head); row tiles of a sequence are counted
 // from first * group / ROWS + s, enough for every sequence before it.
-template <int DT, int D, int RT, int R, bool TREE>
+template <int DT, int D, int ROWS, int R, bool TREE, int CH>
 __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32) {
   typedef typename ElemOf<DT>::T T;
-  constexpr int ROWS = 16 * RT;
   __shared__ Plan s_plan;
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, head = (int)blockIdx.y, group = a.q_heads / a.kv_heads;
@@ -757,7 +762,7 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     s = s_seq;
     if (s >= a.b.seqs) return;
   }
-  const Seq q = seq_of<TREE>(a, s, group, ROWS);
+  const Seq q = seq_of<TREE, CH>(a, s, group, ROWS);
   const int64_t at_tile = (int64_t)bt - base(s);
   if (at_tile < 0 || at_tile * ROWS + r0 >= (int64_t)q.n * group) return;
   const int tile = (int)at_tile;
@@ -769,8 +774,8 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     for (int i = tid & 31; i < D; i += 32) out[i] = (T)0.0f;
     return;
   }
-  const uint64_t total = make_plan<TREE>(a, group, ROWS, &s_plan), nb = total < nb32 ? total : nb32;
-  const uint64_t c0 = start_of_seq<TREE>(a, s_plan, s, group, ROWS) +
+  const uint64_t total = make_plan<TREE, CH>(a, group, ROWS, &s_plan), nb = sharing_blocks(total, nb32);
+  const uint64_t c0 = start_of_seq<TREE, CH>(a, s_plan, s, group, ROWS) +
                       ((uint64_t)head * q.tiles + tile) * q.chunks;
   const uint64_t c1 = c0 + q.chunks - 1;
   const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
@@ -791,7 +796,6 @@ template <int RT>
 constexpr int prompt_rows() {
   return 16 * RT * AT_W;
 }
-constexpr int PR_TILE = 64;         // tokens of one step
 constexpr int PR_SUB = PR_TILE / 16;
 
 // 16-byte pieces of a step in LDS, as fp16: keys [token][piece of 8 elements],
@@ -841,44 +845,137 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
   __shared__ h8 s_v[2][PR_TILE * D / 8];
   __shared__ int s_seq;
   __shared__ int16_t s_up[TREE ? EFFORT_KV_MAX_TREE : 1];
-  const int tid = (int)threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tid = (int)threadIdx.x;
   const int group = a.q_heads / a.kv_heads, shift = __builtin_ctz(a.page_tokens);
-  const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
-  const int head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
-  const int64_t bt = (int64_t)tiles - 1 - turn;  // the last rows see most: they go first
-  auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
-  if (tid == 0) s_seq = a.b.seqs;
-  __syncthreads();
-  for (int i = tid; i < a.b.seqs; i += AT_T)
-    if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
-  __syncthreads();
-  const int seq = __builtin_amdgcn_readfirstlane(s_seq);
-  if (seq >= a.b.seqs) return;
-  const int32_t first = start_of(a.b, seq), n = start_of(a.b, seq + 1) - first;
-  const int32_t row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
-  if (n <= 0 || row0 >= n * group) return;
-  const int rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
-  const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens, pos = len - n;
-  const int64_t b_min = pos + (TREE ? 0 : row0 / group), b_max = pos + (row0 + rows - 1) / group;
-  // tokens that the block's rows see
-  const int64_t from64 = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
-  int64_t to = b_max + 1 < len ? b_max + 1 : len;
-  to = to < cap ? to : cap;
-  const bool tree = TREE && is_tree(n, pos);
-  if (TREE && !tree) to = 0;
-  int32_t parent[2];
-  static_assert(EFFORT_KV_MAX_TREE <= 2 * AT_T, "two parents a thread");
-  if (tree) {  // asked for before the codes
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (tid + u * AT_T < n) parent[u] = a.parents[first + tid + u * AT_T];
+  // TREE.  Where the block stands among the items' steps, and what its rows see of the
+  // steps from that of the first new token on: in LDS, as the products leave no registers.
+  __shared__ Plan s_plan;
+  __shared__ struct {
+    uint64_t c, end, start;  // the next step and the last, and the sequence's first
+    int32_t seq, tree_of;    // the sequence, and whose parents s_up holds
+  } s_at;
+  constexpr int BITS = EFFORT_KV_MAX_TREE / PR_TILE + 1;
+  __shared__ uint64_t s_bits[TREE ? BITS : 1][TREE ? PR_ROWS : 1];
+  __shared__ int32_t s_low[TREE ? PR_ROWS : 1];
+  if (TREE) {
+    const uint64_t total = make_plan<TREE, PR_TILE>(a, group, PR_ROWS, &s_plan), nb = sharing_blocks(total, gridDim.x);
+    if (blockIdx.x >= nb) return;
+    if (tid == 0) {
+      const uint64_t c = total * blockIdx.x / nb;
+      s_at.c = c;
+      s_at.end = total * (blockIdx.x + 1) / nb;
+      s_at.seq = owner<TREE, PR_TILE>(a, s_plan, c, group, PR_ROWS);
+      s_at.start = start_of_seq<TREE, PR_TILE>(a, s_plan, s_at.seq, group, PR_ROWS);
+      s_at.tree_of = -1;
+    }
   }
-  const int32_t from = from64 < to ? (int32_t)from64 : 0, hi = from64 < to ? (int32_t)to : 0;
-  const int32_t lo = from & ~(PR_TILE - 1);
-  const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
-  const int32_t z = (int32_t)blockIdx.y;
-  const int32_t step0 = (int32_t)((int64_t)steps * z / splits), step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
+  // (TREE: over the block's items)
+  for (;;) {
+  // what an item's beginning and end compute of the thread's number alone would
+  // otherwise be kept through its steps, in registers that they do not leave
+  if (TREE) asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int head, seq;
+  int32_t first, n, row0, rows, lo, hi, from, step0, step1;
+  int64_t pos, bt = 0;
+  int32_t z = 0;
+  bool part = splits > 1;
+  if (TREE) {
+    __syncthreads();  // the last item is done with LDS
+    auto wide = [](uint64_t x) {
+      return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
+             (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+    };
+    const uint64_t c = wide(s_at.c), c_end = wide(s_at.end);
+    uint64_t start = wide(s_at.start);
+    seq = __builtin_amdgcn_readfirstlane(s_at.seq);
+    if (c >= c_end) return;
+    Seq q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
+    for (;;) {  // (what is left belongs to some sequence)
+      const uint64_t steps = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+      if (c < start + steps) break;
+      start += steps;
+      if (++seq >= a.b.seqs) return;
+      q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
+    }
+    const uint64_t in = c - start;
+    const uint32_t item = (uint32_t)(in / (uint32_t)q.chunks);
+    step0 = (int32_t)(in % (uint32_t)q.chunks);
+    head = (int)(item / (uint32_t)q.tiles);
+    const int64_t left = (int64_t)(c_end - c), to_end = q.chunks - step0;
+    step1 = step0 + (int32_t)(left < to_end ? left : to_end);
+    part = step0 > 0 || step1 < q.chunks;
+    first = q.first;
+    n = q.n;
+    pos = q.pos;
+    row0 = (int32_t)(item % (uint32_t)q.tiles) * PR_ROWS;
+    rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+    lo = q.lo;
+    hi = q.hi;
+    from = a.window && pos + 1 > a.window ? (int32_t)(pos + 1 - a.window) : 0;  // in front of hi: there are chunks
+    // the rows' masks, where the block's steps need them
+    const bool reach = lo + step1 * PR_TILE > pos;
+    if (reach || a.window) {
+      if (s_at.tree_of != seq)
+        for (int i = tid; i < n; i += AT_T) s_up[i] = up_of(a.parents[first + i], i);
+      __syncthreads();
+      for (int i = tid; i < PR_ROWS; i += AT_T) {
+        const int tok = (row0 + (i < rows ? i : rows - 1)) / group;  // rows behind the last one repeat it
+        s_low[i] = a.window ? sight_of(pos + depth_of(s_up, tok), hi, a.window).low : -1;
+      }
+      const int32_t base = (int32_t)(pos < hi ? pos : hi), base64 = base & ~(PR_TILE - 1);
+      if (reach)
+        for (int i = tid; i < PR_ROWS; i += AT_T) {
+          const int tok = (row0 + (i < rows ? i : rows - 1)) / group;
+          for (int b = 0; b < BITS && base64 + b * PR_TILE < hi; ++b)
+            s_bits[b][i] = b == 0 ? (1ull << (base - base64)) - 1 : 0ull;
+          int p = tok;
+          for (int k = 0; p >= 0 && (!a.window || k < a.window); p = s_up[p], ++k)
+            if (pos + p < hi) {
+              const int at = (int)(pos - base64) + p;
+              s_bits[at / PR_TILE][i] |= 1ull << (at % PR_TILE);
+            }
+        }
+    }
+    if (tid == 0) {
+      s_at.c = c + (uint64_t)(step1 - step0);
+      s_at.start = start;
+      s_at.seq = seq;
+      if (reach || a.window) s_at.tree_of = seq;
+    }
+  } else {
+    const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
+    head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
+    bt = (int64_t)tiles - 1 - turn;  // the last rows see most: they go first
+    auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
+    if (tid == 0) s_seq = a.b.seqs;
+    __syncthreads();
+    for (int i = tid; i < a.b.seqs; i += AT_T)
+      if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
+    __syncthreads();
+    seq = __builtin_amdgcn_readfirstlane(s_seq);
+    if (seq >= a.b.seqs) return;
+    first = start_of(a.b, seq);
+    n = start_of(a.b, seq + 1) - first;
+    row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
+    if (n <= 0 || row0 >= n * group) return;
+    rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+    const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens;
+    pos = len - n;
+    const int64_t b_min = pos + row0 / group, b_max = pos + (row0 + rows - 1) / group;
+    // tokens that the block's rows see
+    const int64_t from64 = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
+    int64_t to = b_max + 1 < len ? b_max + 1 : len;
+    to = to < cap ? to : cap;
+    from = from64 < to ? (int32_t)from64 : 0;
+    hi = from64 < to ? (int32_t)to : 0;
+    lo = from & ~(PR_TILE - 1);
+    const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
+    z = (int32_t)blockIdx.y;
+    step0 = (int32_t)((int64_t)steps * z / splits);
+    step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
+  }
   const int32_t* table = a.b.table + seq * a.b.table_stride;
 
   const int last = wave * WROWS + WROWS - 1 < rows ? wave * WROWS + WROWS - 1 : rows - 1;
@@ -1062,28 +1159,13 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
   h8 qh[RT][KS], ql[RT][KS];
   float f[RT];
   Sight see[RT];
-  Branch br[RT];
-  if (TREE) {
-    if (tree) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (tid + u * AT_T < n) s_up[tid + u * AT_T] = up_of(parent[u], tid + u * AT_T);
-    }
-    __syncthreads();
-  }
+  if (TREE) __syncthreads();  // the rows' masks are in LDS
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     int r = wave * WROWS + rt * 16 + j;
     r = row0 + (r < rows ? r : rows - 1);
     const int i = r / group;
-    if (TREE) {
-      see[rt] = sight_of(pos + (a.window && tree ? depth_of(s_up, i) : 0), hi, a.window);
-      see[rt].high = all_high;
-      br[rt].tok = i;
-      br[rt].reach = a.window ? a.window : EFFORT_KV_MAX_TREE;
-    } else {
-      see[rt] = sight_of(pos + i, hi, a.window);
-    }
+    if (!TREE) see[rt] = sight_of(pos + i, hi, a.window);
     const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
     float x[KS][8], top = 0.0f;
 #pragma unroll
@@ -1176,7 +1258,13 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           if (TREE) {
-            const uint64_t bits = line_bits(see[rt], br[rt], s_up, pos, t, hi) >> (g * 4);
+            const int row = wave * WROWS + rt * 16 + j;
+            uint64_t bits = t + PR_TILE - 1 > all_high ? s_bits[t / PR_TILE - (all_high + 1) / PR_TILE][row] : ~0ull;
+            if (a.window) {
+              const int32_t hidden = s_low[row] + 1 - t;
+              bits = hidden >= PR_TILE ? 0ull : hidden > 0 ? bits & ~0ull << hidden : bits;
+            }
+            bits >>= g * 4;
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
               sc[rt][u] *= c[rt][u];
@@ -1317,13 +1405,15 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
   // a prompt's first hundreds of tokens.
   float* rowbuf = reinterpret_cast<float*>(wave < 2 ? s_k[wave] : s_v[wave - 2]);  // 16 rows of D floats a wave
   static_assert(sizeof(s_k[0]) >= 16 * D * sizeof(float), "a buffer holds a tile of rows");
-  float* mine = parts + (((int64_t)bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
+  // TREE: slot 0 of the block for a part that does not start its item, 1 for one that does
+  float* mine = parts + (TREE ? (int64_t)blockIdx.x * 2 + (step0 == 0 ? 1 : 0)
+                              : (bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float sum = sum_of_row(l[rt]);
     const int r0 = wave * WROWS + rt * 16;
-    const float by = splits > 1 ? unit : sum == 0.0f ? 0.0f : unit / sum;
-    if (splits > 1 && g == 0 && r0 + j < rows) {
+    const float by = part ? unit : sum == 0.0f ? 0.0f : unit / sum;
+    if (part && g == 0 && r0 + j < rows) {
       mine[PR_ROWS * D + r0 + j] = m[rt];
       mine[PR_ROWS * D + PR_ROWS + r0 + j] = sum;
     }
@@ -1343,7 +1433,7 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
       const int r = i + lane / LANES, x = lane % LANES;
       const f4 y = *reinterpret_cast<const f4*>(rowbuf + piece(r, x));
       if (r0 + r >= rows) continue;
-      if (splits > 1) {
+      if (part) {
         *reinterpret_cast<f4*>(mine + (r0 + r) * D + x * 4) = y;
       } else {
         const int row = row0 + r0 + r, tok = row / group;
@@ -1353,6 +1443,8 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
         store_n<4>(out + x * 4, out_vec != 0, v);
       }
     }
+  }
+  if (!TREE) return;
   }
 }
 
@@ -1467,13 +1559,13 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const bool many = nb >= 16 * (int64_t)a.b.seqs * a.kv_heads;
   const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
   if (many)
-    hipLaunchKernelGGL((k_attend_join<DT, D, RT, 1, TREE>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
   else
-    hipLaunchKernelGGL((k_attend_join<DT, D, RT, 4, TREE>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
   return hipGetLastError();
 }
 
-template <int DT, int FMT, int D, int RT, bool TREE>
+template <int DT, int FMT, int D, int RT>
 static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream_t s) {
   float* parts = static_cast<float*>(a.ws);
   const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
@@ -1481,10 +1573,10 @@ static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream
   const int32_t tiles = (int32_t)p.tiles;
   const dim3 grid((unsigned)(p.tiles * a.kv_heads), (unsigned)p.splits);
   if (a.page_tokens >= PR_TILE)
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, TREE>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
                        out_vec);
   else
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, TREE>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
                        out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -1493,11 +1585,41 @@ static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream
   return hipGetLastError();
 }
 
+// Trees of more than 32 rows: blocks of 64 or 128 rows share the steps of all
+// sequences evenly, as in attend_rt.
+static int tree_rows(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group <= 64 * (int64_t)seqs ? 1 : 2; }
+
+template <int DT, int FMT, int D, int RT>
+static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
+  float* parts = static_cast<float*>(a.ws);
+  const int32_t out_vec = rows_aligned<4, typename ElemOf<DT>::T>(a.out, a.out_stride);
+  const int64_t nb = split_blocks(), group = a.q_heads / a.kv_heads;
+  const int64_t tiles = (int64_t)a.b.tokens * group / prompt_rows<RT>() + a.b.seqs;  // of a head, a bound
+  if (a.page_tokens >= PR_TILE)
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts, 0,
+                       1, out_vec);
+  else
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts, 0,
+                       1, out_vec);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t blocks = tiles * (prompt_rows<RT>() / 8);
+  if (blocks > 0xFFFFFF) return hipErrorInvalidValue;  // 2^32 threads of a dimension
+  const dim3 rows((unsigned)blocks, (unsigned)a.kv_heads);
+  hipLaunchKernelGGL((k_attend_join<DT, D, prompt_rows<RT>(), 8, true, PR_TILE>), rows, dim3(AT_T), 0, s, a, parts,
+                     (uint32_t)nb);
+  return hipGetLastError();
+}
+
 template <int DT, int FMT, int D, bool TREE>
 static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
+  if constexpr (TREE) {
+    return tree_rows(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads) == 1 ? tree_rt<DT, FMT, D, 1>(a, s)
+                                                                       : tree_rt<DT, FMT, D, 2>(a, s);
+  }
   const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads,
                                      (int64_t)a.b.max_pages * a.page_tokens);
-  return p.rt == 1 ? prompt_rt<DT, FMT, D, 1, TREE>(a, p, s) : prompt_rt<DT, FMT, D, 2, TREE>(a, p, s);
+  return p.rt == 1 ? prompt_rt<DT, FMT, D, 1>(a, p, s) : prompt_rt<DT, FMT, D, 2>(a, p, s);
 }
 
 template <int DT, int FMT, int D, bool TREE>

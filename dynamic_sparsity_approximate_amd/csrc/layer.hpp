@@ -91,6 +91,7 @@ hipError_t launch_append(const AppendArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_append_ex(const AppendArgs& a, int32_t dtype, hipStream_t s);
 uint64_t attend_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads);
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, hipStream_t s);
+uint64_t tree_workspace(int32_t kv_heads, int32_t dim, int32_t seqs, int64_t tokens, int32_t q_heads);
 hipError_t launch_attend_tree(const AttendArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_fork(const BookArgs& b, const int32_t* source, const int32_t* keep, hipStream_t s);
 uint64_t grow_workspace(const BookArgs& b);

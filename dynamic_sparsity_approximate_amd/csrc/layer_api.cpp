@@ -203,7 +203,8 @@ static int attention(const effort_kv_cache* cache, const effort_kv_batch* batch,
   const int64_t row = (int64_t)q_heads * cache->head_dim;
   if (!rows_ok(q_dev, q_stride, row, es) || !rows_ok(out_dev, out_stride, row, es)) return EFFORT_EINVAL;
   if (out_dev == q_dev) return EFFORT_EINVAL;
-  const uint64_t need = attend_workspace(cache->kv_heads, cache->head_dim, batch->seqs, batch->tokens, q_heads);
+  const uint64_t need = (parents_dev ? tree_workspace : attend_workspace)(
+      cache->kv_heads, cache->head_dim, batch->seqs, batch->tokens, q_heads);
   if (need && (!ws_dev || !aligned(ws_dev, 256))) return EFFORT_EINVAL;
   if (ws_bytes < need) return EFFORT_ENOSPACE;
   AttendArgs a;
@@ -228,6 +229,15 @@ static int attention(const effort_kv_cache* cache, const effort_kv_batch* batch,
   a.parents = parents_dev;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return status_of(parents_dev ? launch_attend_tree(a, dtype, s) : launch_attend(a, dtype, s));
+}
+
+int effort_kv_tree_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
+                                   int32_t q_heads, uint64_t* bytes) {
+  if (!bytes || !cache_sizes_ok(cache) || seqs < 0 || seqs > EFFORT_KV_MAX_SEQS || tokens < 0 ||
+      tokens > kMaxTokens || !heads_ok(q_heads, cache->kv_heads))
+    return EFFORT_EINVAL;
+  *bytes = tree_workspace(cache->kv_heads, cache->head_dim, seqs, tokens, q_heads);
+  return EFFORT_OK;
 }
 
 int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* batch, int32_t dtype,

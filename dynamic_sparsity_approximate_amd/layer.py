@@ -261,10 +261,11 @@ class KVCache(_Kept):
                 o, (os, oh) = out, _heads(out, "out", tokens, self.head_dim, q)
                 if oh != qh:
                     raise ValueError("out must have q's heads")
-            key = (batch.seqs, tokens, qh)
+            key = (batch.seqs, tokens, qh, batch.parents is None)
             n = self._ws_bytes.get(key)
             if n is None:
-                n = B.effort_kv_workspace_bytes(self.desc, *key)
+                need = B.effort_kv_workspace_bytes if batch.parents is None else B.effort_kv_tree_workspace_bytes
+                n = need(self.desc, *key[:3])
                 if len(self._ws_bytes) >= 256:
                     self._ws_bytes.clear()
                 self._ws_bytes[key] = n

@@ -467,7 +467,7 @@ int effort_kv_append_ex(const effort_kv_cache* cache, const effort_kv_batch* bat
                         int64_t q_stride, int32_t q_heads, void* q_out_dev, int64_t q_out_stride,
                         const void* k_dev, int64_t k_stride, const void* v_dev, int64_t v_stride, void* stream);
 
-/* Workspace bytes of effort_kv_attention (and effort_kv_attention_tree) for `seqs` sequences and `tokens` new
+/* Workspace bytes of effort_kv_attention for `seqs` sequences and `tokens` new
    tokens of q_heads query heads (a multiple of kv_heads, at most 64 times it). */
 int effort_kv_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
                               int32_t q_heads, uint64_t* bytes);
@@ -495,7 +495,10 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
    effort_kv_append_ex): a new token sees the positions in front of its
    sequence's new ones, its ancestors among these and itself; with window > 0
    only those whose position is greater than its own minus window, positions
-   being base + d.  A sequence that is no tree sees nothing: its rows become 0. */
+   being base + d.  A sequence that is no tree sees nothing: its rows become 0.
+   ws_dev: as there, of effort_kv_tree_workspace_bytes of the same arguments. */
+int effort_kv_tree_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
+                                   int32_t q_heads, uint64_t* bytes);
 int effort_kv_attention_tree(const effort_kv_cache* cache, const effort_kv_batch* batch,
                              const int32_t* parents_dev, int32_t dtype, const void* q_dev, int64_t q_stride,
                              int32_t q_heads, float scale, int32_t window, void* out_dev, int64_t out_stride,
