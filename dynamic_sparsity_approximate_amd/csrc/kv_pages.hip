@@ -139,8 +139,15 @@ __global__ __launch_bounds__(PG_T) void k_grow(BookArgs b, const int32_t* more_o
   __shared__ int32_t s_page[EFFORT_KV_MAX_SEQS];
   __shared__ uint8_t s_copy[EFFORT_KV_MAX_SEQS];
   __shared__ int32_t s_count;
-  const int tid = (int)threadIdx.x, T = b.page_tokens;
+  __shared__ int32_t s_free[EFFORT_KV_MAX_SEQS];
+  const int tid = (int)threadIdx.x, T = b.page_tokens, lane = tid & 63, wave = tid >> 6;
   const bool mine = tid < b.seqs;
+  // the first pages' counts, on their way with all that leads to what is needed
+  constexpr int U = 16;
+  uint32_t free0 = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid * U + u < b.pages && b.refs[tid * U + u] == 0) free0 |= 1u << u;
   int64_t len = 0, add = 0, beyond = 0, columns = 0;
   int32_t page = -1, first = 0;
   int part = 0;
@@ -165,24 +172,78 @@ __global__ __launch_bounds__(PG_T) void k_grow(BookArgs b, const int32_t* more_o
     s_first[tid] = first;
     s_page[tid] = page;
   }
+  auto copies_page = [&]() {  // whether this thread's sequence copies its page (s_page is complete)
+    const int32_t held = page >= 0 ? b.refs[page] : 0;
+    if (held <= 1) return false;
+    int here = 0;
+    bool later = false;
+    for (int s = 0; s < b.seqs; ++s)
+      if (s_page[s] == page) {
+        ++here;
+        later = later || s > tid;
+      }
+    return later || here < held;
+  };
+  // A column each, and pages enough among the first ones: what decoding asks for.  (A
+  // prompt's growth, or one that the pages do not suffice for, begins anew below.)
+  if (!__syncthreads_or(columns > 1 || beyond > 0)) {
+    int32_t entry = -1;
+    bool need = false, copy = false;
+    if (columns > 0) {
+      copy = copies_page();
+      if (page == -1) {
+        entry = b.table[tid * b.table_stride + first];
+        need = !(is_page(entry, b.pages) && b.refs[entry] <= 1);
+      } else {
+        entry = page;
+        need = copy;
+      }
+    }
+    const uint64_t needs = __ballot(need);
+    int run = __popc(free0);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(run, d);
+      if (lane >= d) run += o;
+    }
+    if (lane == 63) s_w[wave] = (int64_t)run << 32 | (uint32_t)__popcll(needs);
+    __syncthreads();
+    int rank = __popcll(needs & ((1ull << lane) - 1)), at = run - __popc(free0);
+    int want = 0, found = 0;
+#pragma unroll
+    for (int w = 0; w < PG_W; ++w) {
+      const int nw = (int)(uint32_t)s_w[w], fw = (int)(s_w[w] >> 32);
+      if (w < wave) rank += nw;
+      if (w < wave) at += fw;
+      want += nw;
+      found += fw;
+    }
+    if (found >= want) {
+      for (uint32_t f = free0; f && at < want; f &= f - 1) s_free[at++] = tid * U + __builtin_ctz(f);
+      __syncthreads();
+      if (need) {
+        const int32_t now = s_free[rank];
+        b.table[tid * b.table_stride + first] = now;
+        b.refs[now] = 1;
+        if (is_page(entry, b.pages)) atomicSub(b.refs + entry, 1);
+        if (copy) ws.copies[atomicAdd(&s_count, 1)] = Copy{entry, now, part, 0};
+      }
+      if (mine) b.lens[tid] = (int32_t)(len + add < 0x7FFFFFFF ? len + add : 0x7FFFFFFF);
+      __syncthreads();
+      if (tid == 0) {
+        b.info[0] = 0;
+        *ws.count = s_count;
+      }
+      return;
+    }
+    __syncthreads();
+  }
   int64_t total, missing;
   const int64_t start = scan(columns, s_w, &total);  // (its barriers publish s_page, too)
   scan(beyond, s_w, &missing);
   if (mine) {
     s_start[tid] = start;
-    bool copy = false;
-    const int32_t held = page >= 0 ? b.refs[page] : 0;
-    if (held > 1) {
-      int here = 0;
-      bool later = false;
-      for (int s = 0; s < b.seqs; ++s)
-        if (s_page[s] == page) {
-          ++here;
-          later = later || s > tid;
-        }
-      copy = later || here < held;
-    }
-    s_copy[tid] = copy;
+    s_copy[tid] = copies_page();
   }
   if (tid == 0) s_start[b.seqs] = total;
   __syncthreads();
@@ -211,7 +272,6 @@ __global__ __launch_bounds__(PG_T) void k_grow(BookArgs b, const int32_t* more_o
   scan(needed, s_w, &want);
 
   // the lowest free pages, 16 of a thread at a time
-  constexpr int U = 16;
   int64_t found = 0;
   for (int64_t p0 = 0; p0 < b.pages && found < want && missing == 0; p0 += (int64_t)PG_T * U) {
     const int64_t p = p0 + (int64_t)tid * U;
@@ -265,45 +325,57 @@ __global__ __launch_bounds__(PG_T) void k_grow(BookArgs b, const int32_t* more_o
 
 constexpr int CY_T = 256;
 
-// A wave copies one head's codes of a page, keys or values, and its scale: up to 16 KB, all
-// asked for before the first is stored.  blockIdx.y: the cache.
-template <typename Pair>
-__device__ inline void copy_planes(const CacheSet& set, int64_t count, Pair pair) {
+// A wave copies one head's codes of a page, keys or values, and its scale, 8 KB at a time.
+// Nothing of it is used again before the caches have seen much else, so that it passes them
+// by (10 copies of 62 tokens in 32 layers' caches of 8 heads of 128, 81 MB read and written:
+// 19.6 us, 4.1 TB/s; with ordinary loads and stores 26.7).  blockIdx.y: the cache.
+typedef uint32_t Piece __attribute__((ext_vector_type(4)));
+// `most`: pairs that there is room for; what pair(i) is for a later i than the last does
+// not matter.  The first pair comes with their number.
+template <typename Count, typename Pair>
+__device__ inline void copy_planes(const CacheSet& set, int64_t most, Count count, Pair pair) {
   const CacheArgs& c = set.c[blockIdx.y];
   const int lane = (int)threadIdx.x & 63;
-  const int64_t wave = ((int64_t)blockIdx.x * CY_T + threadIdx.x) >> 6, waves = (int64_t)gridDim.x * (CY_T / 64);
-  const int planes = 2 * c.heads;
+  const int64_t waves = (int64_t)gridDim.x * (CY_T / 64);
+  const uint32_t planes = 2 * (uint32_t)c.heads;
   const int64_t plane = (int64_t)set.page_tokens * c.dim;
-  for (int64_t i = wave; i < count * planes; i += waves) {
-    const int64_t at = i / planes;
+  uint32_t wave = blockIdx.x * (CY_T / 64) + (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int64_t at = wave / planes;
+  Copy p = pair(at < most ? at : most - 1);
+  const int64_t all = count() * planes;
+  for (int64_t i = wave; i < all; i += waves) {
+    if (i != wave) {
+      at = i / planes;
+      p = pair(at);
+    }
     const int ph = (int)(i - at * planes), head = ph >> 1;
-    Copy p = pair(at);
     if (!is_page(p.from, set.pages) || !is_page(p.to, set.pages) || p.from == p.to) continue;
     uint8_t* codes = (ph & 1) ? c.v : c.k;
     float* scale = (ph & 1) ? c.vs : c.ks;
-    const uint4* from = reinterpret_cast<const uint4*>(codes + ((int64_t)p.from * c.heads + head) * plane);
-    uint4* to = reinterpret_cast<uint4*>(codes + ((int64_t)p.to * c.heads + head) * plane);
+    const Piece* from = reinterpret_cast<const Piece*>(codes + ((int64_t)p.from * c.heads + head) * plane);
+    Piece* to = reinterpret_cast<Piece*>(codes + ((int64_t)p.to * c.heads + head) * plane);
     const int pieces = p.slots * c.dim / 16;  // 1024 at most
     constexpr int U = 8;
     for (int j0 = 0; j0 < pieces; j0 += 64 * U) {
-      uint4 x[U];
+      Piece x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (j0 + u * 64 + lane < pieces) x[u] = from[j0 + u * 64 + lane];
+        if (j0 + u * 64 + lane < pieces) x[u] = __builtin_nontemporal_load(from + j0 + u * 64 + lane);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (j0 + u * 64 + lane < pieces) to[j0 + u * 64 + lane] = x[u];
+        if (j0 + u * 64 + lane < pieces) __builtin_nontemporal_store(x[u], to + j0 + u * 64 + lane);
     }
     if (lane == 0) scale[(int64_t)p.to * c.heads + head] = scale[(int64_t)p.from * c.heads + head];
   }
 }
 
-__global__ __launch_bounds__(CY_T) void k_copy_grown(CacheSet set, const int32_t* count, const Copy* copies) {
-  copy_planes(set, *count, [&](int64_t i) { return copies[i]; });
+__global__ __launch_bounds__(CY_T) void k_copy_grown(CacheSet set, int32_t most, const int32_t* count,
+                                                      const Copy* copies) {
+  copy_planes(set, most, [&]() { return (int64_t)*count; }, [&](int64_t i) { return copies[i]; });
 }
 
 __global__ __launch_bounds__(CY_T) void k_copy(CacheSet set, int64_t count, const int32_t* from, const int32_t* to) {
-  copy_planes(set, count, [&](int64_t i) { return Copy{from[i], to[i], set.page_tokens, 0}; });
+  copy_planes(set, count, [&]() { return count; }, [&](int64_t i) { return Copy{from[i], to[i], set.page_tokens, 0}; });
 }
 
 // Blocks of a cache for at most `most` pages: a wave for each plane, up to what fills the chip.
@@ -342,7 +414,7 @@ hipError_t launch_grow(const BookArgs& b, const effort_kv_cache* caches, int32_t
   if (e != hipSuccess) return e;
   return each_set(caches, count, [&](const CacheSet& set) {
     hipLaunchKernelGGL(k_copy_grown, dim3(copy_blocks(set, b.seqs), (unsigned)set.count), dim3(CY_T), 0, s, set,
-                       g.count, g.copies);
+                       b.seqs, g.count, g.copies);
   });
 }
 

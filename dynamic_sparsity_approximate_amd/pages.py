@@ -27,10 +27,11 @@ class _Set:
         if not self.caches:
             raise ValueError("no cache")
         c = self.caches[0]
-        if any((o.pages, o.page_tokens, o.device) != (c.pages, c.page_tokens, c.device) for o in self.caches):
+        if any([o._alike != c._alike for o in self.caches]):
             raise ValueError("the caches must have the same pages and page_tokens and be on one device")
         self.pages, self.page_tokens, self.device = c.pages, c.page_tokens, c.device
-        self.descs, self.count = B.kv_caches([o.desc for o in self.caches]), len(self.caches)
+        self.count = len(self.caches)
+        self.descs = (B.effort_kv_cache * self.count).from_buffer_copy(b"".join([o._packed for o in self.caches]))
 
 
 def _set(caches):
