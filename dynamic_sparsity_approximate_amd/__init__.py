@@ -8,13 +8,13 @@ mixture-of-experts block); PyTorch only supplies device memory and streams.
 """
 from .binding import *  # noqa: F401,F403
 from .binding import EffortError, effort_desc, LIB_PATH  # noqa: F401
-from .chain import (LAYER_ROLES, DecodeStep, DecoderStep, DenseDecodeStep, EffortSchedule,  # noqa: F401
+from .chain import (LAYER_ROLES, BeamStep, DecodeStep, DecoderStep, DenseDecodeStep, EffortSchedule,  # noqa: F401
                     MoEFFN, route_top2)
 from .device import EffortGroup, EffortMatrix, Recorder  # noqa: F401
 from .layer import KVBatch, KVCache, norm_residual, rope_table  # noqa: F401
 from .pages import KVPages, beam_select, cache_set, kv_accept, kv_copy_pages  # noqa: F401
 
 __all__ = [n for n in dir() if n.startswith(("effort_", "dense_")) or n in
-           ("EffortError", "EffortGroup", "EffortMatrix", "LIB_PATH", "LAYER_ROLES", "DecodeStep",
+           ("EffortError", "EffortGroup", "EffortMatrix", "LIB_PATH", "LAYER_ROLES", "BeamStep", "DecodeStep",
             "DecoderStep", "DenseDecodeStep", "EffortSchedule", "KVBatch", "KVCache", "KVPages", "MoEFFN", "Recorder",
             "beam_select", "cache_set", "kv_accept", "kv_copy_pages", "norm_residual", "rope_table", "route_top2")]

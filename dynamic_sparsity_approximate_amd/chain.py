@@ -162,12 +162,17 @@ class DecoderStep:
     `norms` one (before attention, before the feed-forward block) pair of norm
     weights per layer and `head_norm` the one before the head.  `x` [tokens][dim]
     holds the embeddings of the new tokens in the order of the batch, `rope` is a
-    table of rope_table (None: no rotation).  Per layer, with the residual
-    stream r (r = x at first):
+    table of rope_table (None: no rotation), `qk_norms` one pair of weights per
+    layer (each [head_dim], one row per head, or None) with which every head of q
+    and k is normed before its rotation.  Per layer, with the residual stream r
+    (r = x at first):
       h = norm(r); q, k, v = h Wq, h Wk, h Wv; k and v appended, q and k rotated
       r += attend(q) Wo; h = norm(r); r += (silu(h W1) * h W3) W2
     and logits = norm(r) Whead.  `out[l]` keeps what layer l computed.  A matrix
     needs `batch` >= tokens; a single row goes through the multi-matrix calls.
+
+    A batch with parents takes trees of drafted tokens: row by row the logits
+    behind each token's own line.  BeamStep makes a beam search of the step.
 
     The kernels read x, the page table, the lengths and the starts at every
     step: a captured step is replayed after the caller has updated them in
@@ -176,11 +181,15 @@ class DecoderStep:
     """
 
     def __init__(self, layers, head, x, caches, batch, norms, head_norm, rope=None, interleaved: bool = False,
-                 window: int = 0, eps: float = 1e-5):
+                 window: int = 0, eps: float = 1e-5, qk_norms=None):
         import torch
 
         from .device import EffortGroup
 
+        if qk_norms is None:
+            qk_norms = [(None, None)] * len(layers)
+        if len(qk_norms) != len(layers):
+            raise ValueError("one pair of weights of the heads' norms per layer")
         if len(layers) != len(caches) or len(layers) != len(norms):
             raise ValueError("one cache and one pair of norm weights per layer")
         if x.dim() != 2 or x.dtype != torch.float32 or not x.is_contiguous() or x.shape[0] < 1:
@@ -194,6 +203,14 @@ class DecoderStep:
                 raise ValueError("a layer's matrices do not fit x, its cache or each other")
         if head.in_dim != dim:
             raise ValueError("the head does not fit x")
+        for L, c, pair in zip(layers, caches, qk_norms):
+            for w, r in zip(pair, ("wq", "wk")):
+                if w is not None and (w.shape not in ((c.head_dim,), (L[r].out_dim // c.head_dim, c.head_dim)) or
+                                      w.dtype != torch.float32 or not w.is_contiguous() or w.device != x.device):
+                    raise ValueError("weights of the heads' norms must be contiguous float32 tensors [head_dim] or "
+                                     "[heads][head_dim] on %s" % x.device)
+        if batch.parents is not None and batch.parents.shape[0] < tokens:
+            raise ValueError("%d parents for %d rows" % (batch.parents.shape[0], tokens))
         weights = [w for pair in norms for w in pair] + [head_norm]
         if any(w.shape != (dim,) or w.dtype != torch.float32 or not w.is_contiguous() for w in weights):
             raise ValueError("norm weights must be contiguous float32 tensors [dim]")
@@ -206,6 +223,7 @@ class DecoderStep:
         self.layers, self.head, self.x = layers, head, x
         self.caches, self.batch, self.norms, self.head_norm = caches, batch, norms, head_norm
         self.rope, self.interleaved, self.window, self.eps = rope, interleaved, window, eps
+        self.qk_norms = qk_norms
         # zeros: rows of no sequence are never written by the attention
         mk = lambda n: torch.zeros((tokens, n), dtype=torch.float32, device=x.device)  # noqa: E731
         self.out = []
@@ -254,13 +272,14 @@ class DecoderStep:
                 mats[0].matvec(x[0], es[0], ys[0][0], main, record=None if record is None else (record, keys[0]))
 
         r, add = None, self.x
-        for l, (c, (before_attn, before_ffn)) in enumerate(zip(self.caches, self.norms)):
+        for l, (c, (before_attn, before_ffn), (qn, kn)) in enumerate(zip(self.caches, self.norms, self.qk_norms)):
             o, (qkv, gu) = self.out[l], self.groups[l] if self.groups else (None, None)
             heads = lambda t: t.view(tokens, -1, c.head_dim)  # noqa: B023,E731
             norm_residual(add, r, pre_w=before_attn, eps=self.eps, resid_out=self.r, out=o["hq"], stream=stream)
             times(l, ("wq", "wk", "wv"), o["hq"], [o["wq"], o["wk"], o["wv"]], qkv)
             c.append(self.batch, heads(o["wk"]), heads(o["wv"]), q=heads(o["wq"]), rope=self.rope,
-                     interleaved=self.interleaved, q_out=heads(o["q"]), stream=stream)
+                     interleaved=self.interleaved, q_out=heads(o["q"]), stream=stream, q_norm=qn, k_norm=kn,
+                     eps=self.eps)
             c.attend(self.batch, heads(o["q"]), window=self.window, out=heads(o["a"]), stream=stream)
             times(l, ("wo",), o["a"], [o["wo"]])
             norm_residual(o["wo"], self.r, pre_w=before_ffn, eps=self.eps, resid_out=o["r"], out=o["hf"], stream=stream)
@@ -271,6 +290,59 @@ class DecoderStep:
         norm_residual(add, r, pre_w=self.head_norm, eps=self.eps, resid_out=self.r, out=self.h, stream=stream)
         times(None, ("head",), self.h, [self.logits])
         return self.logits
+
+
+class BeamStep:
+    """One step of beam search: a DecoderStep whose rows are the beams of some
+    prompts, one new token each, item after item; then the selection, the beams'
+    reordering (KVPages.fork), and room for their next tokens (KVPages.grow).
+
+    `pages` is a KVPages over the step's caches, page table and lengths.  Before
+    the first step the caller has put the prompts into the caches, every beam's
+    sequence holds its prompt (KVPages.fork shares it) and has room for its first
+    token, and `scores` [items][beams] are 0 for one beam of an item and -inf for
+    the others (as they are at first).  After each step `tokens`, `parents` (rows)
+    and `scores` [items][beams] say what the beams are now, `ended` which of them
+    have taken `end_token` (they stay as they are); the caller writes the tokens'
+    embeddings to the step's x.  `short` counts the pages that were missing, at
+    most, in any step: once there are any, the results mean nothing.  The step may
+    be captured once and replayed."""
+
+    def __init__(self, step, pages, beams: int, end_token: int = -1):
+        import torch
+
+        rows, b = step.x.shape[0], step.batch
+        if beams < 1 or rows % beams:
+            raise ValueError("%d rows are not some items of %d beams" % (rows, beams))
+        if b.parents is not None or b.seqs != rows:
+            raise ValueError("a beam search's batch has one sequence per row, and no trees")
+        if pages.page_table is not b.page_table or pages.kv_lens is not b.kv_lens:
+            raise ValueError("pages must be over the batch's own page table and lengths")
+        mine = {(c.k.data_ptr(), c.v.data_ptr()) for c in pages.caches.caches}
+        if any((c.k.data_ptr(), c.v.data_ptr()) not in mine for c in step.caches):
+            raise ValueError("pages must be over all the step's caches")
+        self.step, self.pages, self.end_token = step, pages, end_token
+        mk = lambda v, t: torch.full((rows // beams, beams), v, dtype=t, device=step.x.device)  # noqa: E731
+        self.scores, self.parents, self.tokens = mk(-math.inf, torch.float32), mk(-1, torch.int32), mk(-1, torch.int32)
+        self.scores[:, 0] = 0.0
+        self.ended = mk(False, torch.bool)
+        self.short = torch.zeros(1, dtype=torch.int32, device=step.x.device)
+
+    def enqueue(self, effort, stream=None):
+        """Issue the step on `stream` (None: torch's current stream); returns tokens."""
+        import torch
+
+        from .pages import beam_select
+
+        dev = self.step.x.device
+        with torch.cuda.device(dev), torch.cuda.stream(stream):  # (None changes nothing)
+            logits = self.step.enqueue(effort, stream)
+            beam_select(logits, self.scores, ended=self.ended, end_token=self.end_token,
+                        out=(self.scores, self.parents, self.tokens), stream=stream)
+            torch.eq(self.tokens, self.end_token, out=self.ended)
+            self.pages.fork(self.parents.view(-1), stream=stream)
+            torch.maximum(self.short, self.pages.grow(1, stream=stream), out=self.short)
+        return self.tokens
 
 
 class DenseDecodeStep:

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(PG_T) void k_grow(BookArgs b, const int32_t* more_o
 
   // the lowest free pages, 16 of a thread at a time
   int64_t found = 0;
-  for (int64_t p0 = 0; p0 < b.pages && found < want && missing == 0; p0 += (int64_t)PG_T * U) {
+  for (int64_t p0 = 0; p0 < b.pages && found < want; p0 += (int64_t)PG_T * U) {
     const int64_t p = p0 + (int64_t)tid * U;
     uint32_t free = 0;
 #pragma unroll

@@ -448,8 +448,8 @@ int effort_kv_append(const effort_kv_cache* cache, const effort_kv_batch* batch,
    q_norm_dev[head * q_norm_stride ..] of `dtype` (stride 0: shared by the heads,
    else at least head_dim); k alike with k_norm_dev.  A key's norm is taken in
    double like its rotation and not rounded before its code; a query's is
-   rounded to 32 bits.  A head with a NaN or an infinity is a NaN throughout,
-   and so is one of zeros when eps is 0.
+   rounded to 32 bits.  A head with a NaN is a NaN throughout, and so is one of
+   zeros when eps is 0; one with an infinity is a NaN there, and 0 elsewhere.
    Trees: parents_dev not NULL: int32 [tokens]; row q_starts[s] + i's entry is
    the number, among sequence s's new tokens, of the token that i continues;
    what is no earlier token of the sequence (-1, say) means the last committed
@@ -545,8 +545,8 @@ int effort_kv_fork(const effort_kv_book* book, const int32_t* source_dev, const 
       stays absent.
    Free pages, those of count 0, are given out in the order of sequences and
    columns, the lowest first.  If there are too few, or a sequence would grow
-   beyond its table, nothing changes and info[0] says how many pages are missing
-   (else 0): the new tokens must then not be appended.
+   beyond its table, nothing changes and info[0] says how many pages are missing,
+   columns that the table has not among them (else 0): the new tokens must then not be appended.
    caches: host array of `count` caches of the book's pages and page_tokens (0:
    no copies).  ws_dev: 256-byte aligned, of effort_kv_grow_workspace_bytes. */
 int effort_kv_grow_workspace_bytes(const effort_kv_book* book, uint64_t* bytes);
