@@ -13,6 +13,18 @@ except ImportError:  # the C binding alone works without torch
     pass
 
 
+_sizes = {}  # workspace bytes by a call's sizes
+
+
+def _bytes(need, *sizes):
+    n = _sizes.get((need, sizes))
+    if n is None:
+        if len(_sizes) >= 1024:
+            _sizes.clear()
+        n = _sizes[(need, sizes)] = need(*sizes)
+    return n
+
+
 def _vector(t, name, n, device):
     if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous int32 tensor [%d] on %s" % (name, n, device))
@@ -27,7 +39,8 @@ class _Set:
         if not self.caches:
             raise ValueError("no cache")
         c = self.caches[0]
-        if any([o._alike != c._alike for o in self.caches]):
+        alike = c._alike
+        if [o for o in self.caches if o._alike != alike]:
             raise ValueError("the caches must have the same pages and page_tokens and be on one device")
         self.pages, self.page_tokens, self.device = c.pages, c.page_tokens, c.device
         self.count = len(self.caches)
@@ -52,7 +65,7 @@ class KVPages(_Kept):
     A KVBatch over the same page_table and kv_lens sees every change.  Calls on
     one KVPages, or on several with one refs, must be ordered."""
 
-    _kept = frozenset(("caches", "page_table", "kv_lens", "refs", "info", "device", "seqs"))
+    _kept = frozenset(("caches", "page_table", "kv_lens", "refs", "info", "_missing", "device", "seqs"))
 
     def __init__(self, caches, page_table, kv_lens, refs=None):
         s = self.caches = _set(caches)
@@ -66,6 +79,7 @@ class KVPages(_Kept):
             refs = torch.bincount(held, minlength=s.pages).to(torch.int32)
         self.page_table, self.kv_lens, self.refs = page_table, kv_lens, _vector(refs, "refs", s.pages, s.device)
         self.info = torch.zeros(4, dtype=torch.int32, device=s.device)
+        self._missing = self.info[:1]
         self.device = s.device
         stride = page_table.stride(0) if self.seqs > 1 else cols
         self._book = B.effort_kv_book(self.seqs, cols, s.page_tokens, 0, s.pages, stride, page_table.data_ptr(),
@@ -102,7 +116,7 @@ class KVPages(_Kept):
             # of this call alone: other captured graphs have their own
             ws = self.info.new_empty(self._ws_bytes, dtype=torch.uint8)
             B.effort_kv_grow(self._book, self.caches.descs, self.caches.count, each, more, ws, self._ws_bytes, handle)
-            return self.info[:1]
+            return self._missing
 
         return _run(self.device, stream, call)
 
@@ -130,7 +144,7 @@ def kv_accept(caches, batch: KVBatch, leaf, lens_out=None, stream=None):
         raise ValueError("the batch is on %s, the caches on %s" % (batch.device, s.device))
     _vector(leaf, "leaf", batch.seqs, s.device)
     out = batch.kv_lens if lens_out is None else _vector(lens_out, "lens_out", batch.seqs, s.device)
-    n = B.effort_kv_accept_workspace_bytes(batch.seqs) if batch.parents is not None else 0
+    n = _bytes(B.effort_kv_accept_workspace_bytes, batch.seqs) if batch.parents is not None else 0
     # rows of the call: no more than the parents, where there are any
     tokens = batch.parents.shape[0] if batch.parents is not None else 1 << 24
 
@@ -158,19 +172,18 @@ def beam_select(logits, scores, keep=None, ended=None, end_token: int = 0, out=N
         raise ValueError("scores must be a contiguous float32 tensor [items][beams]")
     (items, beams), dev = scores.shape, scores.device
     dt = _dtype(logits, "logits")
-    if logits.dim() == 3:
-        if logits.shape[:2] != (items, beams):
-            raise ValueError("logits: shape %s, wanted [%d][%d][vocab]" % (tuple(logits.shape), items, beams))
-        strides = logits.stride()
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) == 2 and shape[0] == items * beams:
+        stride = strides[0]
+    elif len(shape) == 3 and shape[:2] == (items, beams):
         if items > 1 and beams > 1 and strides[0] != beams * strides[1]:
             raise ValueError("logits: rows must be one distance apart (strides %s)" % (strides,))
         stride = strides[1] if beams > 1 else strides[0]
-    elif logits.dim() == 2 and logits.shape[0] == items * beams:
-        stride = logits.stride(0)
     else:
-        raise ValueError("logits: shape %s, wanted [%d][vocab]" % (tuple(logits.shape), items * beams))
-    vocab = logits.shape[-1]
-    if logits.device != dev or (vocab > 1 and logits.stride(-1) != 1):
+        raise ValueError("logits: shape %s, wanted [%d][vocab] or [%d][%d][vocab]" % (
+            tuple(shape), items * beams, items, beams))
+    vocab = shape[-1]
+    if logits.device != dev or (vocab > 1 and strides[-1] != 1):
         raise ValueError("logits must be on %s, their rows contiguous" % dev)
     if items * beams <= 1:
         stride = max(vocab, 1)
@@ -180,12 +193,11 @@ def beam_select(logits, scores, keep=None, ended=None, end_token: int = 0, out=N
     keep = beams if keep is None else keep
     _i32(keep, "keep")
     _i32(end_token, "end_token")
-    n = B.effort_beam_workspace_bytes(items, beams, vocab)
+    n = _bytes(B.effort_beam_workspace_bytes, items, beams, vocab)
 
     def call(handle):
         if out is None:
-            o = (scores.new_empty((items, keep)), scores.new_empty((items, keep), dtype=torch.int32),
-                 scores.new_empty((items, keep), dtype=torch.int32))
+            o = (scores.new_empty((items, keep)), *scores.new_empty((2, items, keep), dtype=torch.int32).unbind())
         else:
             o = tuple(out)
             if [t.dtype for t in o] != [torch.float32, torch.int32, torch.int32] or \
