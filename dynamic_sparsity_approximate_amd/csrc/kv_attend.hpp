@@ -43,6 +43,10 @@ constexpr int AT_T = 256, AT_W = AT_T / 64;
 constexpr int AT_TILE = 32;              // tokens of one step of a wave
 constexpr int AT_CHUNK = AT_W * AT_TILE; // tokens of one step of a block
 constexpr int PR_TILE = 64;              // tokens of one step of a block whose waves share them
+// Steps that beginning and ending an item cost such a block where blocks share them (with
+// none, the blocks that have parts of two items end last: eight trees of 32 over up to 8192
+// tokens @@ us, 24 of up to 25 behind a window of 1000 @@).
+constexpr int PR_BEGIN = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 // Weights are held times 2^6 relative to a row's reference score, which follows
 // the row's maximum only when that is 2^8 times larger (most steps then rescale
@@ -169,6 +173,7 @@ struct Seq {
   int32_t lo, hi;     // tokens that any row sees, lo a multiple of AT_TILE at least
   int32_t tiles;      // row tiles of `rows` rows
   int32_t chunks;
+  int32_t span;       // what an item counts when blocks share them: its chunks, and its beginning
 };
 
 // Chunks of CH tokens: AT_CHUNK, or PR_TILE (then lo is a multiple of that).
@@ -184,12 +189,13 @@ __device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
   const int64_t from = a.window && q.pos + 1 > a.window ? q.pos + 1 - a.window : 0;
   const int64_t to = len < cap ? len : cap;
   q.tiles = (int32_t)(((int64_t)q.n * group + rows - 1) / rows);
-  q.chunks = 0;
+  q.chunks = q.span = 0;
   q.lo = q.hi = 0;
   if (q.n > 0 && to > from && (!TREE || is_tree(q.n, q.pos))) {
     q.lo = (int32_t)(from & ~(int64_t)(ALIGN - 1));
     q.hi = (int32_t)to;
     q.chunks = (int32_t)((to - q.lo + CH - 1) / CH);
+    q.span = q.chunks + (CH == PR_TILE ? PR_BEGIN : 0);
   }
   return q;
 }
@@ -197,11 +203,16 @@ __device__ inline Seq seq_of(const AttendArgs& a, int s, int group, int rows) {
 template <bool TREE, int CH>
 __device__ inline uint64_t chunks_of(const AttendArgs& a, int s, int group, int rows) {
   const Seq q = seq_of<TREE, CH>(a, s, group, rows);
-  return (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+  return (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.span;
 }
 
 // Blocks that share a call's chunks: no block has nothing.
 __device__ inline uint64_t sharing_blocks(uint64_t steps, uint32_t grid) { return steps < grid ? steps : grid; }
+
+// x / y; of 32 bits each, as they nearly always are, in a tenth of the instructions.
+__device__ inline uint64_t quotient(uint64_t x, uint64_t y) {
+  return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
+}
 
 // Chunks before the sequences, one entry for `per` of them (one each up to 256
 // sequences); every block computes it from the lengths, so that a captured call
@@ -776,9 +787,10 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
   }
   const uint64_t total = make_plan<TREE, CH>(a, group, ROWS, &s_plan), nb = sharing_blocks(total, nb32);
   const uint64_t c0 = start_of_seq<TREE, CH>(a, s_plan, s, group, ROWS) +
-                      ((uint64_t)head * q.tiles + tile) * q.chunks;
+                      ((uint64_t)head * q.tiles + tile) * q.span;
   const uint64_t c1 = c0 + q.chunks - 1;
-  const uint64_t b0 = ((c0 + 1) * nb - 1) / total, b1 = ((c1 + 1) * nb - 1) / total;  // blocks of its first, last chunk
+  // blocks of its first, last chunk
+  const uint64_t b0 = quotient((c0 + 1) * nb - 1, total), b1 = quotient((c1 + 1) * nb - 1, total);
   if (b0 == b1) return;
   const float* first = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
   const float* rest = parts + (b0 + 1) * 2 * (uint64_t)(ROWS * (D + 2));
@@ -861,9 +873,9 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
     const uint64_t total = make_plan<TREE, PR_TILE>(a, group, PR_ROWS, &s_plan), nb = sharing_blocks(total, gridDim.x);
     if (blockIdx.x >= nb) return;
     if (tid == 0) {
-      const uint64_t c = total * blockIdx.x / nb;
+      const uint64_t c = quotient(total * blockIdx.x, nb);
       s_at.c = c;
-      s_at.end = total * (blockIdx.x + 1) / nb;
+      s_at.end = quotient(total * (blockIdx.x + 1), nb);
       s_at.seq = owner<TREE, PR_TILE>(a, s_plan, c, group, PR_ROWS);
       s_at.start = start_of_seq<TREE, PR_TILE>(a, s_plan, s_at.seq, group, PR_ROWS);
       s_at.tree_of = -1;
@@ -893,18 +905,20 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
     if (c >= c_end) return;
     Seq q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
     for (;;) {  // (what is left belongs to some sequence)
-      const uint64_t steps = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.chunks;
+      const uint64_t steps = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.span;
       if (c < start + steps) break;
       start += steps;
       if (++seq >= a.b.seqs) return;
       q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
     }
     const uint64_t in = c - start;
-    const uint32_t item = (uint32_t)(in / (uint32_t)q.chunks);
-    step0 = (int32_t)(in % (uint32_t)q.chunks);
+    const uint32_t item = (uint32_t)quotient(in, (uint32_t)q.span);
+    const int32_t in_item = (int32_t)(in - (uint64_t)item * (uint32_t)q.span);
     head = (int)(item / (uint32_t)q.tiles);
-    const int64_t left = (int64_t)(c_end - c), to_end = q.chunks - step0;
-    step1 = step0 + (int32_t)(left < to_end ? left : to_end);
+    const int64_t left = (int64_t)(c_end - c), to_end = q.span - in_item;
+    const int32_t take = (int32_t)(left < to_end ? left : to_end);
+    step0 = in_item < q.chunks ? in_item : q.chunks;
+    step1 = in_item + take < q.chunks ? in_item + take : q.chunks;
     part = step0 > 0 || step1 < q.chunks;
     first = q.first;
     n = q.n;
@@ -916,7 +930,8 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
     from = a.window && pos + 1 > a.window ? (int32_t)(pos + 1 - a.window) : 0;  // in front of hi: there are chunks
     // the rows' masks, where the block's steps need them
     const bool reach = lo + step1 * PR_TILE > pos;
-    if (reach || a.window) {
+    const bool edge = a.window && lo + step0 * PR_TILE <= pos + n - 1 - a.window;  // some row may not see all of a step
+    if (reach || edge) {
       if (s_at.tree_of != seq)
         for (int i = tid; i < n; i += AT_T) s_up[i] = up_of(a.parents[first + i], i);
       __syncthreads();
@@ -938,12 +953,14 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
             }
         }
     }
+    __syncthreads();  // every wave has read the state
     if (tid == 0) {
-      s_at.c = c + (uint64_t)(step1 - step0);
+      s_at.c = c + (uint64_t)take;
       s_at.start = start;
       s_at.seq = seq;
-      if (reach || a.window) s_at.tree_of = seq;
+      if (reach || edge) s_at.tree_of = seq;
     }
+    if (step0 == step1) continue;  // (the rest of what its beginning counts)
   } else {
     const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
     head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
@@ -1260,7 +1277,7 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
           if (TREE) {
             const int row = wave * WROWS + rt * 16 + j;
             uint64_t bits = t + PR_TILE - 1 > all_high ? s_bits[t / PR_TILE - (all_high + 1) / PR_TILE][row] : ~0ull;
-            if (a.window) {
+            if (t <= all_low) {
               const int32_t hidden = s_low[row] + 1 - t;
               bits = hidden >= PR_TILE ? 0ull : hidden > 0 ? bits & ~0ull << hidden : bits;
             }
