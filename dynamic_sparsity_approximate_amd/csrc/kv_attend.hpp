@@ -682,12 +682,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float
 }
 
 // Joins `count` parts of a row by 256 / R threads: a group of 32 has D / 32
-// elements each of every (8 / R)-th part, four parts in flight, with the
+// elements each of every (8 / R)-th part, FLY parts in flight, with the
 // maximum and sum of what it has seen; then the groups are joined the same way.
 // `at(i)` is part i: the values of `rows` rows, their maxima, their sums.
-template <int D, int R, typename T, typename At>
+template <int D, int R, int FLY = 4, typename T, typename At>
 __device__ void join_row(int count, int rows, int r, At at, T* out) {
-  constexpr int E = D / 32, GROUPS = 8 / R, FLY = 4;
+  constexpr int E = D / 32, GROUPS = 8 / R;
   __shared__ float s_m[8], s_l[8];
   __shared__ float s_v[8][D];
   const int tid = (int)threadIdx.x, lane = tid & 31, slot = tid >> 5, k = slot % GROUPS;
@@ -755,7 +755,8 @@ __device__ void join_row(int count, int rows, int r, At at, T* out) {
 // nothing.  One block per (R rows, head); row tiles of a sequence are counted
 // from first * group / ROWS + s, enough for every sequence before it.
 template <int DT, int D, int ROWS, int R, bool TREE, int CH>
-__global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32) {
+__global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32,
+                                                      const uint64_t* before) {
   typedef typename ElemOf<DT>::T T;
   __shared__ Plan s_plan;
   __shared__ int s_seq;
@@ -785,9 +786,16 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
     for (int i = tid & 31; i < D; i += 32) out[i] = (T)0.0f;
     return;
   }
-  const uint64_t total = make_plan<TREE, CH>(a, group, ROWS, &s_plan), nb = sharing_blocks(total, nb32);
-  const uint64_t c0 = start_of_seq<TREE, CH>(a, s_plan, s, group, ROWS) +
-                      ((uint64_t)head * q.tiles + tile) * q.span;
+  uint64_t total, c0 = 0;
+  if (before && per_entry(a) == 1) {  // the plan that the other kernel left
+    total = before[AT_T];
+    c0 = before[s];
+  } else {
+    total = make_plan<TREE, CH>(a, group, ROWS, &s_plan);
+    c0 = start_of_seq<TREE, CH>(a, s_plan, s, group, ROWS);
+  }
+  const uint64_t nb = sharing_blocks(total, nb32);
+  c0 += ((uint64_t)head * q.tiles + tile) * q.span;
   const uint64_t c1 = c0 + q.chunks - 1;
   // blocks of its first, last chunk
   const uint64_t b0 = quotient((c0 + 1) * nb - 1, total), b1 = quotient((c1 + 1) * nb - 1, total);
@@ -796,7 +804,7 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
   const float* rest = parts + (b0 + 1) * 2 * (uint64_t)(ROWS * (D + 2));
   auto at = [&](int i) { return i == 0 ? first : rest + (uint64_t)(i - 1) * 2 * (ROWS * (D + 2)); };
   // a row behind the last one repeats the block's first
-  join_row<D, R>((int)(b1 - b0) + 1, ROWS, mine ? r : r0, at, out);
+  join_row<D, R, CH == PR_TILE ? 8 : 4>((int)(b1 - b0) + 1, ROWS, mine ? r : r0, at, out);
 }
 
 // ---------------------------------------------------------------- prompts
@@ -833,6 +841,12 @@ struct Staged {
   uint4 k[D / 64];
   uint32_t v[2][4];
 };
+
+// Behind the parts of a tree's blocks: the plan, for those who join them.
+template <int D>
+__host__ __device__ inline uint64_t* plan_of(float* parts, int64_t blocks, int rows) {
+  return reinterpret_cast<uint64_t*>(parts + blocks * 2 * rows * (D + 2));
+}
 
 // One block per (128 or 64 rows of a sequence, head, part of their tokens): its
 // four waves have a quarter each and share every 64-token step's keys and values, which
@@ -871,6 +885,10 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
   __shared__ int32_t s_low[TREE ? PR_ROWS : 1];
   if (TREE) {
     const uint64_t total = make_plan<TREE, PR_TILE>(a, group, PR_ROWS, &s_plan), nb = sharing_blocks(total, gridDim.x);
+    if (blockIdx.x == 0 && a.b.seqs > 1) {  // for the join
+      uint64_t* before = plan_of<D>(parts, gridDim.x, PR_ROWS);
+      for (int i = tid; i <= AT_T; i += AT_T) before[i] = s_plan.before[i];
+    }
     if (blockIdx.x >= nb) return;
     if (tid == 0) {
       const uint64_t c = quotient(total * blockIdx.x, nb);
@@ -1576,9 +1594,11 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const bool many = nb >= 16 * (int64_t)a.b.seqs * a.kv_heads;
   const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
   if (many)
-    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb,
+                       (const uint64_t*)nullptr);
   else
-    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb,
+                       (const uint64_t*)nullptr);
   return hipGetLastError();
 }
 
@@ -1624,7 +1644,7 @@ static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
   if (blocks > 0xFFFFFF) return hipErrorInvalidValue;  // 2^32 threads of a dimension
   const dim3 rows((unsigned)blocks, (unsigned)a.kv_heads);
   hipLaunchKernelGGL((k_attend_join<DT, D, prompt_rows<RT>(), 8, true, PR_TILE>), rows, dim3(AT_T), 0, s, a, parts,
-                     (uint32_t)nb);
+                     (uint32_t)nb, a.b.seqs > 1 ? plan_of<D>(parts, nb, prompt_rows<RT>()) : nullptr);
   return hipGetLastError();
 }
 
