@@ -1537,6 +1537,12 @@ static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
 // 40.9; of 896, one sequence: 17.8 and 13.9, 64: 55.1 and 48.8, so 640 there.
 static int64_t whole_tokens(int rt) { return rt == 2 ? 640 : 1024; }
 
+// Tokens that a row of the call may see: all that the host knows of lengths.
+static int64_t span_of(const AttendArgs& a) {
+  const int64_t span = (int64_t)a.b.max_pages * a.page_tokens;
+  return a.window && a.window + (int64_t)AT_CHUNK < span ? a.window + (int64_t)AT_CHUNK : span;
+}
+
 // How a prompt is shared out: 16-row tiles of a wave, blocks of rows of a head
 // (a bound), and in how many parts their tokens are taken so that as many blocks
 // as a CU holds fall to every CU.
@@ -1577,8 +1583,7 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const int64_t nb = split_blocks();
   const int64_t tiles = (int64_t)a.b.tokens * (a.q_heads / a.kv_heads) / (16 * RT) + a.b.seqs;  // of a head, a bound
   float* parts = static_cast<float*>(a.ws);
-  int64_t span = (int64_t)a.b.max_pages * a.page_tokens;
-  if (a.window && a.window + (int64_t)AT_CHUNK < span) span = a.window + (int64_t)AT_CHUNK;
+  const int64_t span = span_of(a);
   if (span <= whole_tokens(RT) && tiles <= 65535) {
     const dim3 grid((unsigned)a.kv_heads, (unsigned)tiles);
     hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true, TREE>), grid, dim3(512), 0, s, a, parts);
@@ -1623,7 +1628,15 @@ static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream
 }
 
 // Trees of more than 32 rows: blocks of 64 or 128 rows share the steps of all
-// sequences evenly, as in attend_rt.
+// sequences evenly, as in attend_rt; but over such short tables as there (whole_tokens)
+// a block of eight waves takes 16 rows each, up to three items a CU: 15 tokens of 1, 4, 8,
+// 16 sequences, 4 query heads a group, 8 heads, tables of 448 tokens, fp32: 11.6, 12.4, 14.2
+// and 24.8 us, shared 15.0, 20.2, 23.7 and 28.0; 30 tokens of 8 and 16 in bf16, of 1024:
+// 27.8 and 54.0, shared 32.9 and 40.9.
+static bool tree_whole(const AttendArgs& a) {
+  const int64_t items = ((int64_t)a.b.tokens * (a.q_heads / a.kv_heads) + 15) / 16 * a.kv_heads;
+  return span_of(a) <= whole_tokens(1) && items <= 3 * (int64_t)cu_count();
+}
 static int tree_rows(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group <= 64 * (int64_t)seqs ? 1 : 2; }
 
 template <int DT, int FMT, int D, int RT>
@@ -1651,6 +1664,7 @@ static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
 template <int DT, int FMT, int D, bool TREE>
 static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
   if constexpr (TREE) {
+    if (tree_whole(a)) return attend_rt<DT, FMT, D, 1, true>(a, s);
     return tree_rows(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads) == 1 ? tree_rt<DT, FMT, D, 1>(a, s)
                                                                        : tree_rt<DT, FMT, D, 2>(a, s);
   }

@@ -153,6 +153,8 @@ def test_what_is_no_tree_is_left_alone():
     assert np.abs(g[522:] - ref[522:]).max() <= 2.0 ** -20
     a = c.check_tree(got)
     assert (f64(a)[:522] == 0.0).all()
+    far = Tree(7, lens, new, page=16, parents=par, dim=64, room=1100, group=4)
+    assert (f64(far.check_tree(far.rand(8)))[:522] == 0.0).all()
 
 
 # ---------------------------------------------------------------- attention of trees
@@ -172,29 +174,34 @@ TREES = [
 ]
 
 
+@pytest.mark.parametrize("room", [0, 1100])  # tables of more than 1024 tokens are shared out in another way
 @pytest.mark.parametrize("heads,group,dim,page,fmt,dtype,lens,new,window", TREES)
-def test_tree_attention(heads, group, dim, page, fmt, dtype, lens, new, window):
-    c = Tree(11, lens, new, heads=heads, group=group, dim=dim, page=page, fmt=fmt, dtype=dtype, spread=3)
+def test_tree_attention(heads, group, dim, page, fmt, dtype, lens, new, window, room):
+    c = Tree(11, lens, new, heads=heads, group=group, dim=dim, page=page, fmt=fmt, dtype=dtype, spread=3, room=room)
     c.check_tree(c.rand(heads * group, 1.5), window=window)
 
 
+@pytest.mark.parametrize("room", [0, 1100])
 @pytest.mark.parametrize("new,group,dtype", [(12, 1, "f32"), (20, 3, "bf16"), (40, 4, "f16")])
-def test_chains_forests_and_lines(new, group, dtype):
+def test_chains_forests_and_lines(new, group, dtype, room):
     """A chain is causal attention; tokens of no parent see themselves alone of the new ones."""
     lens = [new + 100, new, new + 3]
-    chain = Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=[i - 1 for i in range(new)] * 3)
+    chain = Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=[i - 1 for i in range(new)] * 3,
+                 room=room)
     q = chain.rand(2 * group)
     chain.check_attend(q, got=chain.check_tree(q))
-    Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=[-1] * 3 * new).check_tree(q)
+    Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=[-1] * 3 * new, room=room).check_tree(q)
     comb = [(i - 2 if i % 2 == 0 else i - 1) if i else -1 for i in range(new)]
-    Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=comb * 3).check_tree(q, window=5)
+    Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=comb * 3, room=room).check_tree(q, window=5)
+    Tree(12, lens, [new] * 3, group=group, dtype=dtype, parents=comb * 3, room=room).check_tree(q, window=1000)
 
 
+@pytest.mark.parametrize("room", [0, 1100])
 @pytest.mark.parametrize("new,group", [(5, 2), (20, 4), (40, 4)])
-def test_poison_reaches_only_rows_that_see_it(new, group):
+def test_poison_reaches_only_rows_that_see_it(new, group, room):
     """Of a page of drafted tokens, and of a committed one behind a window."""
     lens = [64 + new, 200]
-    c = Tree(13, lens, [new, new], group=group, page=16)
+    c = Tree(13, lens, [new, new], group=group, page=16, room=room)
     for page, head in ((c.table[0, (64 + new - 1) // 16], 0), (c.table[1, (200 - new - 30) // 16], 1)):
         c.np["ks"][page, head] = np.nan
         c.cache.k_scale[int(page), head] = math.nan
@@ -207,17 +214,19 @@ def test_poison_reaches_only_rows_that_see_it(new, group):
 def test_many_sequences_and_blocks_of_several_items():
     """More sequences than the plan has entries; blocks that take parts of several items; lengths of all kinds."""
     rng = np.random.default_rng(14)
-    for seqs, new, group, page in ((300, 3, 2, 16), (40, 17, 4, 64), (70, 20, 3, 16)):
+    for seqs, new, group, page, room in ((300, 3, 2, 16, 0), (300, 12, 4, 16, 1100), (40, 17, 4, 64, 1100),
+                                         (70, 20, 3, 16, 1100), (70, 20, 3, 16, 0)):
         lens = [int(n + rng.integers(0, 300)) for n in [new] * seqs]
         lens[3] = 0
         count = [new] * seqs
         count[3], count[5] = 0, 1
-        c = Tree(14, lens, count, heads=1, group=group, page=page, dtype="bf16")
+        c = Tree(14, lens, count, heads=1, group=group, page=page, dtype="bf16", room=room)
         c.check_tree(c.rand(group))
 
 
-def test_rows_behind_the_last_sequence_stay_and_scales_are_signed():
-    c = Tree(15, [90, 50], [20, 20], group=4, parents=R.random_tree(np.random.default_rng(1), 20) * 2 + [0] * 9)
+@pytest.mark.parametrize("room", [0, 1100])
+def test_rows_behind_the_last_sequence_stay_and_scales_are_signed(room):
+    c = Tree(15, [90, 50], [20, 20], group=4, room=room, parents=R.random_tree(np.random.default_rng(1), 20) * 2 + [0] * 9)
     q = c.rand(8, rows=49)
     out = torch.full_like(q, 3.0)
     c.cache.attend(c.batch, q, out=out)

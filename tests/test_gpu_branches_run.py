@@ -233,7 +233,7 @@ def test_two_streams_and_two_graphs_have_their_own_workspaces():
     rng = np.random.default_rng(5)
     logits = [cuda(rng.standard_normal((8, 50000)).astype(np.float32)) for _ in range(2)]
     scores = [cuda(-rng.random((2, 4)).astype(np.float32)) for _ in range(2)]
-    trees = [Tree(30 + i, [300, 200], [20, 20], group=4, page=16) for i in range(2)]
+    trees = [Tree(30 + i, [300, 200], [20, 20], group=4, page=16, room=900 * (2 - i)) for i in range(2)]
     qs = [t.rand(8) for t in trees]
     pools = [Pool(6 + i, [[0, 1, -1], [0, 1, -1], [0, 1, 2]], [20, 20, 33], 30) for i in range(2)]
     work = lambda i: (*E.beam_select(logits[i], scores[i], keep=8), trees[i].cache.attend(trees[i].batch, qs[i]))  # noqa: E731
