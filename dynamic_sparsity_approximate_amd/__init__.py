@@ -3,8 +3,8 @@
 The compute path is libeffort.so (hand-written HIP kernels behind the C ABI of
 include/effort.h).  This package is its ctypes binding, a small holder for a
 prepared matrix resident in device memory, and the sequencing of chained calls
-(a decoder stack's matvecs, whole decoder layers over a paged 8-bit cache, a
-mixture-of-experts block); PyTorch only supplies device memory and streams.
+(a decoder stack's matvecs, whole decoder layers over a paged 8-bit cache, beam
+search over them, a mixture-of-experts block); PyTorch only supplies device memory and streams.
 """
 from .binding import *  # noqa: F401,F403
 from .binding import EffortError, effort_desc, LIB_PATH  # noqa: F401

@@ -7,7 +7,7 @@ sequence calls into libeffort and own the intermediate buffers; every step of
 the arithmetic, the glue included (silu(h1) * h3, the gated expert sum), runs
 in the library's kernels.  A caller that repeats a chain captures `enqueue`
 into a HIP graph.  DecodeStep takes the attention's results from outside;
-DecoderStep runs whole layers over a paged cache.
+DecoderStep runs whole layers over a paged cache, BeamStep a beam search of them.
 """
 from __future__ import annotations
 

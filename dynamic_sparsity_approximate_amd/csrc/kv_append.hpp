@@ -153,7 +153,9 @@ constexpr int AP_QH = 4;
 // before the page is known.
 // EX: with head norms or a tree, which the others need no registers for.  A key's norm
 // is taken in double like its rotation, and rounded with it: the codes are the nearest
-// ones.  A tree's depths come from its parents in LDS, asked for before the rows.
+// ones.  A tree's depths come from its parents in LDS, asked for before the rows.  The
+// prompts above with both norms: 46.5 us, the norms' sums and products in double hidden
+// behind the bytes; one token 4.8 (without norms 4.1), 12 trees of up to 16 6.0.
 template <int DT, int FMT, int IT, bool EX>
 __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token,
                                                  int32_t kv_vec, int32_t q_vec) {

@@ -24,7 +24,8 @@
 // and of those its ancestors and itself; a window counts by position, which is the first
 // new one's plus the token's depth.  Only steps that reach the new tokens know of it: a
 // lane walks from its row's token up through the parents, in LDS, and takes a bit for
-// each that lies in the step (a tree of 15 tokens or 64: 4 to 8 reads of LDS a row).
+// each that lies in the step (a tree of 15 tokens or 64: 4 to 8 reads of LDS a row);
+// blocks whose waves share steps keep the rows' bits in LDS, for want of registers.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -861,6 +862,16 @@ __host__ __device__ inline uint64_t* plan_of(float* parts, int64_t blocks, int r
 // instructions a step beside 64 products, and they are its time (two bf16
 // prompts of 4096 tokens, 32 query heads of 128, pages of 64: 334 us with it,
 // 320 with ONE, 860 TFLOP/s).
+//
+// TREE: a tree has few rows, and a batch's lengths are unequal, so that blocks (two
+// a CU) share all items' steps evenly, in order, as in k_attend_split, and
+// k_attend_join joins their parts.  Eight trees of 32 tokens, 4 query heads a
+// group, over 1365 to 8192 tokens, bf16: 50.6 us and 9.2 for the join (every
+// item in equal parts, as prompts are: 73 and 6); 64 tokens over 100003 int8 ones:
+// 152 and 9.2 (196 and 7), of which each 25000 tokens are 32, 820 TFLOP/s, and the
+// blocks' beginnings and ends 17.  The parts are as large as what is read of the
+// cache: fewer blocks, so fewer parts, cost more than they save (256 blocks: 63.0 and
+// 6.4, 206 and 6.2).
 template <int DT, int FMT, int D, bool ONE, int RT, bool TREE>
 __global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 ? 2 : 3) : DT == EFFORT_F32 && D == 128 ? 1 : 2)
 void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, int32_t out_vec) {

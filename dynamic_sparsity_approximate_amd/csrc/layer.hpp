@@ -1,5 +1,6 @@
 // layer.hpp -- argument blocks and launchers of the kernels between a decoder
-// layer's matvecs (kv_append.hip, kv_attend.hip, norm.hip).
+// layer's matvecs (kv_append.hpp, kv_attend.hpp, norm.hip), and of what several
+// continuations of a sequence need (kv_pages.hip, beam.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -1,5 +1,5 @@
-// layer_api.cpp -- C ABI of what lies between a decoder layer's matvecs:
-// argument validation and launches.  Every check happens before the first enqueue.
+// layer_api.cpp -- C ABI of what lies between a decoder layer's matvecs, and of several
+// continuations of a sequence: argument validation and launches.  Every check happens before the first enqueue.
 #include <hip/hip_runtime.h>
 #include <math.h>
 

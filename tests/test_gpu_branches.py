@@ -485,3 +485,15 @@ def test_beams_far_apart_scores():
     check_beams(cuda(x), cuda(s), keep=100)
     check_beams(cuda(x[:, :4]), cuda(s[:, :4]), keep=100)
     check_beams(cuda(x[:, :3]), cuda(s[:, :3]), keep=128)
+
+
+def test_beams_of_more_items_than_a_launch_has_blocks():
+    dev()
+    n = (1 << 21) + 3
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(n, 2, generator=g, device="cuda")
+    s, p, t = E.beam_select(x, torch.zeros(n, 1, device="cuda"))
+    assert torch.equal(p[:, 0], torch.arange(n, dtype=torch.int32, device="cuda"))
+    assert torch.equal(t[:, 0], (x[:, 1] > x[:, 0]).int())
+    want = -torch.log1p(torch.exp(-(x[:, 0] - x[:, 1]).abs().double()))
+    assert float((s[:, 0].double() - want).abs().max()) <= 2.0 ** -22 + 2.0 ** -24
