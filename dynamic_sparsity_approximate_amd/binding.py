@@ -515,8 +515,8 @@ def effort_kv_accept_workspace_bytes(seqs: int) -> int:
 
 
 def effort_kv_accept(caches, count: int, batch, parents, leaf, lens_out, ws, ws_bytes: int, stream=None):
-    _check(_lib.effort_kv_accept(caches, count, ctypes.byref(batch), _ptr(parents), _ptr(leaf), _ptr(lens_out), _ptr(ws),
-                                 ws_bytes, _stream(stream)), "effort_kv_accept")
+    _check(_lib.effort_kv_accept(caches, count, ctypes.byref(batch), _ptr(parents), _ptr(leaf), _ptr(lens_out),
+                                 _ptr(ws), ws_bytes, _stream(stream)), "effort_kv_accept")
 
 
 def effort_beam_workspace_bytes(items: int, beams: int, vocab: int) -> int:

@@ -44,7 +44,8 @@ __device__ inline float top_of(float x, float y) { return __builtin_elementwise_
 
 template <int CTRL>
 __device__ inline float dpp_top(float x) {
-  return top_of(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), CTRL, 0xF, 0xF, false)));
+  const int b = __float_as_int(x);
+  return top_of(x, __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false)));
 }
 
 constexpr float kHi = 1.4426950408889634f, kLo = 1.925963033500995e-8f;  // log2(e)
@@ -72,8 +73,8 @@ __device__ inline void load_any(const T* p, float* x) {
 // products, exact but for 2^-24 of the exponent, whose reference is a number of base 2
 // that the sum is kept with, and the instruction's ulp.
 template <int DT, int WAVE>
-__global__ __launch_bounds__(BM_T) void k_beam_read(BeamArgs a, float* maxima, Part* parts, int64_t first, int64_t waves,
-                                                    int64_t per_row, int64_t groups) {
+__global__ __launch_bounds__(BM_T) void k_beam_read(BeamArgs a, float* maxima, Part* parts, int64_t first,
+                                                    int64_t waves, int64_t per_row, int64_t groups) {
   typedef typename ElemOf<DT>::T T;
   constexpr int N = 16 / sizeof(T), LANES = BM_GROUP / N, IT = WAVE / (64 * N);  // lanes of a group
   const int lane = (int)threadIdx.x & 63;
@@ -392,7 +393,8 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     const int b = 63 - (int)(c.lo >> 52);
     a.out_scores[out + rank] = (float)number_of(c.hi);
     a.out_parents[out + rank] = (int32_t)(row0 + b);
-    a.out_tokens[out + rank] = a.ended && a.ended[row0 + b] ? a.end_token : (int32_t)(0xFFFFFu - (uint32_t)(c.lo & 0xFFFFFu));
+    const int32_t token = (int32_t)(0xFFFFFu - (uint32_t)(c.lo & 0xFFFFFu));
+    a.out_tokens[out + rank] = a.ended && a.ended[row0 + b] ? a.end_token : token;
   });
   for (int i = found + tid; i < keep; i += BP_T) {
     a.out_scores[out + i] = -INFINITY;

@@ -912,585 +912,590 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
   }
   // (TREE: over the block's items)
   for (;;) {
-  // what an item's beginning and end compute of the thread's number alone would
-  // otherwise be kept through its steps, in registers that they do not leave
-  if (TREE) asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, j = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int head, seq;
-  int32_t first, n, row0, rows, lo, hi, from, step0, step1;
-  int64_t pos, bt = 0;
-  int32_t z = 0;
-  bool part = splits > 1;
-  if (TREE) {
-    __syncthreads();  // the last item is done with LDS
-    auto wide = [](uint64_t x) {
-      return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
-             (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
-    };
-    const uint64_t c = wide(s_at.c), c_end = wide(s_at.end);
-    uint64_t start = wide(s_at.start);
-    seq = __builtin_amdgcn_readfirstlane(s_at.seq);
-    if (c >= c_end) return;
-    Seq q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
-    for (;;) {  // (what is left belongs to some sequence)
-      const uint64_t steps = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.span;
-      if (c < start + steps) break;
-      start += steps;
-      if (++seq >= a.b.seqs) return;
-      q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
-    }
-    const uint64_t in = c - start;
-    const uint32_t item = (uint32_t)quotient(in, (uint32_t)q.span);
-    const int32_t in_item = (int32_t)(in - (uint64_t)item * (uint32_t)q.span);
-    head = (int)(item / (uint32_t)q.tiles);
-    const int64_t left = (int64_t)(c_end - c), to_end = q.span - in_item;
-    const int32_t take = (int32_t)(left < to_end ? left : to_end);
-    step0 = in_item < q.chunks ? in_item : q.chunks;
-    step1 = in_item + take < q.chunks ? in_item + take : q.chunks;
-    part = step0 > 0 || step1 < q.chunks;
-    first = q.first;
-    n = q.n;
-    pos = q.pos;
-    row0 = (int32_t)(item % (uint32_t)q.tiles) * PR_ROWS;
-    rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
-    lo = q.lo;
-    hi = q.hi;
-    from = a.window && pos + 1 > a.window ? (int32_t)(pos + 1 - a.window) : 0;  // in front of hi: there are chunks
-    // the rows' masks, where the block's steps need them
-    const bool reach = lo + step1 * PR_TILE > pos;
-    const bool edge = a.window && lo + step0 * PR_TILE <= pos + n - 1 - a.window;  // some row may not see all of a step
-    if (reach || edge) {
-      if (s_at.tree_of != seq)
-        for (int i = tid; i < n; i += AT_T) s_up[i] = up_of(a.parents[first + i], i);
-      __syncthreads();
-      for (int i = tid; i < PR_ROWS; i += AT_T) {
-        const int tok = (row0 + (i < rows ? i : rows - 1)) / group;  // rows behind the last one repeat it
-        s_low[i] = a.window ? sight_of(pos + depth_of(s_up, tok), hi, a.window).low : -1;
+    // what an item's beginning and end compute of the thread's number alone would
+    // otherwise be kept through its steps, in registers that they do not leave
+    if (TREE) asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, j = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int head, seq;
+    int32_t first, n, row0, rows, lo, hi, from, step0, step1;
+    int64_t pos, bt = 0;
+    int32_t z = 0;
+    bool part = splits > 1;
+    if (TREE) {
+      __syncthreads();  // the last item is done with LDS
+      auto wide = [](uint64_t x) {
+        return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+      };
+      const uint64_t c = wide(s_at.c), c_end = wide(s_at.end);
+      uint64_t start = wide(s_at.start);
+      seq = __builtin_amdgcn_readfirstlane(s_at.seq);
+      if (c >= c_end) return;
+      Seq q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
+      for (;;) {  // (what is left belongs to some sequence)
+        const uint64_t steps = (uint64_t)q.tiles * (uint64_t)a.kv_heads * (uint64_t)q.span;
+        if (c < start + steps) break;
+        start += steps;
+        if (++seq >= a.b.seqs) return;
+        q = seq_of<TREE, PR_TILE>(a, seq, group, PR_ROWS);
       }
-      const int32_t base = (int32_t)(pos < hi ? pos : hi), base64 = base & ~(PR_TILE - 1);
-      if (reach)
+      const uint64_t in = c - start;
+      const uint32_t item = (uint32_t)quotient(in, (uint32_t)q.span);
+      const int32_t in_item = (int32_t)(in - (uint64_t)item * (uint32_t)q.span);
+      head = (int)(item / (uint32_t)q.tiles);
+      const int64_t left = (int64_t)(c_end - c), to_end = q.span - in_item;
+      const int32_t take = (int32_t)(left < to_end ? left : to_end);
+      step0 = in_item < q.chunks ? in_item : q.chunks;
+      step1 = in_item + take < q.chunks ? in_item + take : q.chunks;
+      part = step0 > 0 || step1 < q.chunks;
+      first = q.first;
+      n = q.n;
+      pos = q.pos;
+      row0 = (int32_t)(item % (uint32_t)q.tiles) * PR_ROWS;
+      rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+      lo = q.lo;
+      hi = q.hi;
+      from = a.window && pos + 1 > a.window ? (int32_t)(pos + 1 - a.window) : 0;  // in front of hi: there are chunks
+      // the rows' masks, where the block's steps need them
+      const bool reach = lo + step1 * PR_TILE > (pos < hi ? pos : hi);
+      // (edge: some row may not see all of a step)
+      const bool edge = a.window && lo + step0 * PR_TILE <= pos + n - 1 - a.window;
+      if (reach || edge) {
+        if (s_at.tree_of != seq)
+          for (int i = tid; i < n; i += AT_T) s_up[i] = up_of(a.parents[first + i], i);
+        __syncthreads();
         for (int i = tid; i < PR_ROWS; i += AT_T) {
-          const int tok = (row0 + (i < rows ? i : rows - 1)) / group;
-          for (int b = 0; b < BITS && base64 + b * PR_TILE < hi; ++b)
-            s_bits[b][i] = b == 0 ? (1ull << (base - base64)) - 1 : 0ull;
-          int p = tok;
-          for (int k = 0; p >= 0 && (!a.window || k < a.window); p = s_up[p], ++k)
-            if (pos + p < hi) {
-              const int at = (int)(pos - base64) + p;
-              s_bits[at / PR_TILE][i] |= 1ull << (at % PR_TILE);
-            }
+          const int tok = (row0 + (i < rows ? i : rows - 1)) / group;  // rows behind the last one repeat it
+          s_low[i] = a.window ? sight_of(pos + depth_of(s_up, tok), hi, a.window).low : -1;
         }
+        const int32_t base = (int32_t)(pos < hi ? pos : hi), base64 = base & ~(PR_TILE - 1);
+        if (reach)
+          for (int i = tid; i < PR_ROWS; i += AT_T) {
+            const int tok = (row0 + (i < rows ? i : rows - 1)) / group;
+            for (int b = 0; b < BITS && base64 + b * PR_TILE < hi; ++b)
+              s_bits[b][i] = b == 0 ? (1ull << (base - base64)) - 1 : 0ull;
+            int p = tok;
+            for (int k = 0; p >= 0 && (!a.window || k < a.window); p = s_up[p], ++k)
+              if (pos + p < hi) {
+                const int at = (int)(pos - base64) + p;
+                s_bits[at / PR_TILE][i] |= 1ull << (at % PR_TILE);
+              }
+          }
+      }
+      __syncthreads();  // every wave has read the state
+      if (tid == 0) {
+        s_at.c = c + (uint64_t)take;
+        s_at.start = start;
+        s_at.seq = seq;
+        if (reach || edge) s_at.tree_of = seq;
+      }
+      if (step0 == step1) continue;  // (the rest of what its beginning counts)
+    } else {
+      const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
+      head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
+      bt = (int64_t)tiles - 1 - turn;  // the last rows see most: they go first
+      auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
+      if (tid == 0) s_seq = a.b.seqs;
+      __syncthreads();
+      for (int i = tid; i < a.b.seqs; i += AT_T)
+        if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
+      __syncthreads();
+      seq = __builtin_amdgcn_readfirstlane(s_seq);
+      if (seq >= a.b.seqs) return;
+      first = start_of(a.b, seq);
+      n = start_of(a.b, seq + 1) - first;
+      row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
+      if (n <= 0 || row0 >= n * group) return;
+      rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
+      const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens;
+      pos = len - n;
+      const int64_t b_min = pos + row0 / group, b_max = pos + (row0 + rows - 1) / group;
+      // tokens that the block's rows see
+      const int64_t from64 = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
+      int64_t to = b_max + 1 < len ? b_max + 1 : len;
+      to = to < cap ? to : cap;
+      from = from64 < to ? (int32_t)from64 : 0;
+      hi = from64 < to ? (int32_t)to : 0;
+      lo = from & ~(PR_TILE - 1);
+      const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
+      z = (int32_t)blockIdx.y;
+      step0 = (int32_t)((int64_t)steps * z / splits);
+      step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
     }
-    __syncthreads();  // every wave has read the state
-    if (tid == 0) {
-      s_at.c = c + (uint64_t)take;
-      s_at.start = start;
-      s_at.seq = seq;
-      if (reach || edge) s_at.tree_of = seq;
+    const int32_t* table = a.b.table + seq * a.b.table_stride;
+
+    const int last = wave * WROWS + WROWS - 1 < rows ? wave * WROWS + WROWS - 1 : rows - 1;
+    const int front = wave * WROWS < rows ? wave * WROWS : rows - 1;
+    const int32_t all_high = TREE ? (int32_t)(pos < hi ? pos : hi) - 1 : __builtin_amdgcn_readfirstlane(
+        sight_of(pos + (row0 + front) / group, hi, a.window).high);
+    const int32_t all_low = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + last) / group, hi, a.window).low);
+
+    f4 o[RT][ND];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      m[rt] = -INFINITY;
+      l[rt] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (step0 == step1) continue;  // (the rest of what its beginning counts)
-  } else {
-    const uint32_t turn = blockIdx.x / (uint32_t)a.kv_heads;
-    head = (int)(blockIdx.x - turn * (uint32_t)a.kv_heads);
-    bt = (int64_t)tiles - 1 - turn;  // the last rows see most: they go first
-    auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / PR_ROWS + i; };
-    if (tid == 0) s_seq = a.b.seqs;
-    __syncthreads();
-    for (int i = tid; i < a.b.seqs; i += AT_T)
-      if (base(i) <= bt && bt < base(i + 1)) atomicMin(&s_seq, i);
-    __syncthreads();
-    seq = __builtin_amdgcn_readfirstlane(s_seq);
-    if (seq >= a.b.seqs) return;
-    first = start_of(a.b, seq);
-    n = start_of(a.b, seq + 1) - first;
-    row0 = (int32_t)(bt - base(seq)) * PR_ROWS;
-    if (n <= 0 || row0 >= n * group) return;
-    rows = n * group - row0 < PR_ROWS ? n * group - row0 : PR_ROWS;
-    const int64_t len = a.b.lens[seq], cap = (int64_t)a.b.max_pages * a.page_tokens;
-    pos = len - n;
-    const int64_t b_min = pos + row0 / group, b_max = pos + (row0 + rows - 1) / group;
-    // tokens that the block's rows see
-    const int64_t from64 = a.window && b_min + 1 > a.window ? b_min + 1 - a.window : 0;
-    int64_t to = b_max + 1 < len ? b_max + 1 : len;
-    to = to < cap ? to : cap;
-    from = from64 < to ? (int32_t)from64 : 0;
-    hi = from64 < to ? (int32_t)to : 0;
-    lo = from & ~(PR_TILE - 1);
-    const int32_t steps = (hi - lo + PR_TILE - 1) / PR_TILE;
-    z = (int32_t)blockIdx.y;
-    step0 = (int32_t)((int64_t)steps * z / splits);
-    step1 = (int32_t)((int64_t)steps * (z + 1) / splits);
-  }
-  const int32_t* table = a.b.table + seq * a.b.table_stride;
+    // O counts in `unit`s of the values' scale: a token of scale vs weighs w * vs /
+    // unit, with the ratio inside the exponent.  The unit follows the scales up at
+    // once, down when they are 2^10 smaller (but never to where what is there
+    // could overflow).
+    float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
+    uint32_t now_vs = 0;  // ONE: the last step's scale, log2 of its ratio to the unit, and 1 / ratio
+    float now_up = 0.0f, now_back = 1.0f;
+    auto set_unit = [&](float top) {
+      unit_top = fmaxf(unit_top, top);
+      if (top > 2.0f * unit || (top < 0x1p-10f * unit && top > 0.0f)) {
+        const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f), by = unit / now;
+        unit = now;
+        per_unit = 1.0f / now;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[rt][d] *= by;
+      }
+    };
 
-  const int last = wave * WROWS + WROWS - 1 < rows ? wave * WROWS + WROWS - 1 : rows - 1;
-  const int front = wave * WROWS < rows ? wave * WROWS : rows - 1;
-  const int32_t all_high = TREE ? (int32_t)(pos < hi ? pos : hi) - 1 : __builtin_amdgcn_readfirstlane(
-      sight_of(pos + (row0 + front) / group, hi, a.window).high);
-  const int32_t all_low = __builtin_amdgcn_readfirstlane(sight_of(pos + (row0 + last) / group, hi, a.window).low);
-
-  f4 o[RT][ND];
-  float m[RT], l[RT];
+    // page of the step at t, or of its sub-tile lane & 3; -1: none, behind the
+    // block's last step, or a sub-tile before what the rows see, whose page may have
+    // any scale
+    const int32_t stop = lo + step1 * PR_TILE < hi ? lo + step1 * PR_TILE : hi;
+    auto page_at = [&](int32_t t) {
+      const int32_t tok = ONE ? t : t + 16 * (lane & 3);
+      return tok < stop && (ONE || tok + 15 >= from) ? table[tok >> shift] : -1;
+    };
+    const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
+    const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
+    const bool v_mine = D == 128 || wave < 2;
+    const int in_page = (1 << shift) - 1;
+    // Addresses are a lane's place in page 0 plus the page times a page's bytes
+    // (pages of 16 and 32 tokens divide a step, so that a lane's slot is the same
+    // in every step); with ONE a scalar address plus a lane's constant offset.
+    // Page 0 is read where there is none, and never used.
+    const uint32_t page_bytes = (uint32_t)a.kv_heads << shift << (D == 128 ? 7 : 6);
+    const int64_t at_head = (int64_t)head << shift;
+    auto lane_base = [&](const uint8_t* c, int tok, int byte) {  // of token `tok` of a step
+      return c + (at_head + (tok & in_page)) * D + byte;
+    };
+    const uint8_t* k_base[D / 64];
+    const uint8_t* v_base[2];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = -INFINITY;
-    l[rt] = 0.0f;
+    for (int i = 0; i < D / 64; ++i) k_base[i] = lane_base(a.kc, k_tok + i * (4096 / D), k_piece * 16);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) o[rt][d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  // O counts in `unit`s of the values' scale: a token of scale vs weighs w * vs /
-  // unit, with the ratio inside the exponent.  The unit follows the scales up at
-  // once, down when they are 2^10 smaller (but never to where what is there
-  // could overflow).
-  float unit = 0.0f, per_unit = 0.0f, unit_top = 0.0f;
-  uint32_t now_vs = 0;  // ONE: the last step's scale, log2 of its ratio to the unit, and 1 / ratio
-  float now_up = 0.0f, now_back = 1.0f;
-  auto set_unit = [&](float top) {
-    unit_top = fmaxf(unit_top, top);
-    if (top > 2.0f * unit || (top < 0x1p-10f * unit && top > 0.0f)) {
-      const float now = fmaxf(fmaxf(top, unit_top * 0x1p-60f), 0x1p-100f), by = unit / now;
-      unit = now;
-      per_unit = 1.0f / now;
+    for (int u = 0; u < 2; ++u) v_base[u] = lane_base(a.vc, (v_q * 2 + u) * 16 + v_g * 4, v_el);
+    const float *ks_base = a.ks + head, *vs_base = a.vs + head;
+    auto valid = [&](int32_t page) { return (uint32_t)page < (uint32_t)a.b.pages ? (uint32_t)page : 0u; };
+    auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, uint32_t* ks, uint32_t* vs) {
+      const uint64_t own = (uint64_t)valid(pages) * (uint32_t)a.kv_heads;
+      *ks = __float_as_uint(ks_base[own]);
+      *vs = __float_as_uint(vs_base[own]);
+      if (ONE) {
+        const uint64_t at = (uint64_t)valid(pages) * page_bytes + (uint64_t)(at_head + (t & in_page)) * D;
+        const uint8_t *kp = a.kc + at, *vp = a.vc + at;
+        const uint32_t k_off = (uint32_t)(k_tok * D + k_piece * 16);
+        const uint32_t v_off = (uint32_t)((v_q * 32 + v_g * 4) * D + v_el);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+        for (int i = 0; i < D / 64; ++i) st->k[i] = *reinterpret_cast<const uint4*>(kp + (k_off + i * 4096));
+        if (v_mine) {
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[rt][d] *= by;
-    }
-  };
-
-  // page of the step at t, or of its sub-tile lane & 3; -1: none, behind the
-  // block's last step, or a sub-tile before what the rows see, whose page may have
-  // any scale
-  const int32_t stop = lo + step1 * PR_TILE < hi ? lo + step1 * PR_TILE : hi;
-  auto page_at = [&](int32_t t) {
-    const int32_t tok = ONE ? t : t + 16 * (lane & 3);
-    return tok < stop && (ONE || tok + 15 >= from) ? table[tok >> shift] : -1;
-  };
-  const int k_piece = tid & (D / 16 - 1), k_tok = tid / (D / 16);  // the first of D / 64 keys, 4096 / D tokens apart
-  const int v_el = (tid & (D / 4 - 1)) * 4, v_g = tid / (D / 4) & 3, v_q = wave / (D / 64);
-  const bool v_mine = D == 128 || wave < 2;
-  const int in_page = (1 << shift) - 1;
-  // Addresses are a lane's place in page 0 plus the page times a page's bytes
-  // (pages of 16 and 32 tokens divide a step, so that a lane's slot is the same
-  // in every step); with ONE a scalar address plus a lane's constant offset.
-  // Page 0 is read where there is none, and never used.
-  const uint32_t page_bytes = (uint32_t)a.kv_heads << shift << (D == 128 ? 7 : 6);
-  const int64_t at_head = (int64_t)head << shift;
-  auto lane_base = [&](const uint8_t* c, int tok, int byte) {  // of token `tok` of a step
-    return c + (at_head + (tok & in_page)) * D + byte;
-  };
-  const uint8_t* k_base[D / 64];
-  const uint8_t* v_base[2];
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) k_base[i] = lane_base(a.kc, k_tok + i * (4096 / D), k_piece * 16);
+            for (int r = 0; r < 4; ++r)
+              st->v[u][r] = *reinterpret_cast<const uint32_t*>(vp + (v_off + (u * 16 + r) * D));
+        }
+        return;
+      }
+      auto place = [&](int sub) {  // of the page of a sub-tile
+        return (uint64_t)valid(__builtin_amdgcn_readlane(pages, sub)) * page_bytes;
+      };
 #pragma unroll
-  for (int u = 0; u < 2; ++u) v_base[u] = lane_base(a.vc, (v_q * 2 + u) * 16 + v_g * 4, v_el);
-  const float *ks_base = a.ks + head, *vs_base = a.vs + head;
-  auto valid = [&](int32_t page) { return (uint32_t)page < (uint32_t)a.b.pages ? (uint32_t)page : 0u; };
-  auto fetch = [&](int32_t t, int32_t pages, Staged<D>* st, uint32_t* ks, uint32_t* vs) {
-    const uint64_t own = (uint64_t)valid(pages) * (uint32_t)a.kv_heads;
-    *ks = __float_as_uint(ks_base[own]);
-    *vs = __float_as_uint(vs_base[own]);
-    if (ONE) {
-      const uint64_t at = (uint64_t)valid(pages) * page_bytes + (uint64_t)(at_head + (t & in_page)) * D;
-      const uint8_t *kp = a.kc + at, *vp = a.vc + at;
-      const uint32_t k_off = (uint32_t)(k_tok * D + k_piece * 16), v_off = (uint32_t)((v_q * 32 + v_g * 4) * D + v_el);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) st->k[i] = *reinterpret_cast<const uint4*>(kp + (k_off + i * 4096));
+      for (int i = 0; i < D / 64; ++i) {
+        const int sub = D == 128 ? i * 2 + (wave >> 1) : wave;  // of token k_tok + i * 4096 / D
+        st->k[i] = *reinterpret_cast<const uint4*>(k_base[i] + place(sub));
+      }
       if (v_mine) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* from_row = v_base[u] + place(v_q * 2 + u);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(from_row + r * D);
+        }
+      }
+    };
+    auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, uint32_t vs, int buf) {
+      // nothing of this may move up to where the codes are still on their way
+      asm volatile("" : "+v"(vs));
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        asm volatile("" : "+v"(st.k[i].x), "+v"(st.k[i].y), "+v"(st.k[i].z), "+v"(st.k[i].w));
+        const int tok = k_tok + i * (4096 / D);
+        s_k[buf][key_piece<D>(tok, k_piece * 2)] = decode8<FMT>(st.k[i].x, st.k[i].y);
+        s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
+      }
+      if (!v_mine) return;
+      if (ONE)
+        ok = __builtin_amdgcn_readfirstlane(vs) != 0u ? ok : 0u;
+      else
+        ok &= (uint32_t)__ballot(vs != 0u);
+      if ((ok & ((1u << SUB) - 1)) != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
+        // values of tokens that no row sees weigh 0, so they must not be NaN;
+        // those of scale 0 are 0
+        int32_t tok0 = t + v_q * 32 + v_g * 4;
+        asm volatile("" : "+v"(tok0));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(vp + (v_off + (u * 16 + r) * D));
+          for (int r = 0; r < 4; ++r) {
+            const int32_t tok = tok0 + u * 16 + r;
+            if (!(ok >> (v_q * 2 + u) & 1) || tok >= hi || tok < from) st.v[u][r] = 0u;
+          }
       }
-      return;
-    }
-    auto place = [&](int sub) {  // of the page of a sub-tile
-      return (uint64_t)valid(__builtin_amdgcn_readlane(pages, sub)) * page_bytes;
-    };
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int sub = D == 128 ? i * 2 + (wave >> 1) : wave;  // of token k_tok + i * 4096 / D
-      st->k[i] = *reinterpret_cast<const uint4*>(k_base[i] + place(sub));
-    }
-    if (v_mine) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint8_t* from_row = v_base[u] + place(v_q * 2 + u);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) st->v[u][r] = *reinterpret_cast<const uint32_t*>(from_row + r * D);
-      }
-    }
-  };
-  auto store = [&](int32_t t, uint32_t ok, Staged<D>& st, uint32_t vs, int buf) {
-    // nothing of this may move up to where the codes are still on their way
-    asm volatile("" : "+v"(vs));
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      asm volatile("" : "+v"(st.k[i].x), "+v"(st.k[i].y), "+v"(st.k[i].z), "+v"(st.k[i].w));
-      const int tok = k_tok + i * (4096 / D);
-      s_k[buf][key_piece<D>(tok, k_piece * 2)] = decode8<FMT>(st.k[i].x, st.k[i].y);
-      s_k[buf][key_piece<D>(tok, k_piece * 2 + 1)] = decode8<FMT>(st.k[i].z, st.k[i].w);
-    }
-    if (!v_mine) return;
-    if (ONE)
-      ok = __builtin_amdgcn_readfirstlane(vs) != 0u ? ok : 0u;
-    else
-      ok &= (uint32_t)__ballot(vs != 0u);
-    if ((ok & ((1u << SUB) - 1)) != (1u << SUB) - 1 || t + PR_TILE > hi || t < from) {
-      // values of tokens that no row sees weigh 0, so they must not be NaN;
-      // those of scale 0 are 0
-      int32_t tok0 = t + v_q * 32 + v_g * 4;
-      asm volatile("" : "+v"(tok0));
+      uint32_t e[4], e2[4];  // both tokens of a pair: bytes 0 and 1, bytes 2 and 3
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int32_t tok = tok0 + u * 16 + r;
-          if (!(ok >> (v_q * 2 + u) & 1) || tok >= hi || tok < from) st.v[u][r] = 0u;
+        for (int h = 0; h < 2; ++h) {
+          e[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x05010400u);
+          e2[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x07030602u);
         }
-    }
-    uint32_t e[4], e2[4];  // both tokens of a pair: bytes 0 and 1, bytes 2 and 3
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        e[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x05010400u);
-        e2[u * 2 + h] = __builtin_amdgcn_perm(st.v[u][2 * h + 1], st.v[u][2 * h], 0x07030602u);
-      }
-    const int piece = v_q * 4 + v_g;
-    s_v[buf][value_piece<D>(v_el, piece)] =
-        join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]),
-              decode2<FMT, false>(e[3]));
-    s_v[buf][value_piece<D>(v_el + 1, piece)] =
-        join8(decode2<FMT, true>(e[0]), decode2<FMT, true>(e[1]), decode2<FMT, true>(e[2]), decode2<FMT, true>(e[3]));
-    s_v[buf][value_piece<D>(v_el + 2, piece)] = join8(decode2<FMT, false>(e2[0]), decode2<FMT, false>(e2[1]),
-                                                      decode2<FMT, false>(e2[2]), decode2<FMT, false>(e2[3]));
-    s_v[buf][value_piece<D>(v_el + 3, piece)] =
-        join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]),
-              decode2<FMT, true>(e2[3]));
-  };
-  auto there = [&](int32_t pages) {  // bit per sub-tile
-    const bool in = (uint32_t)pages < (uint32_t)a.b.pages;
-    return ONE ? (in ? (1u << SUB) - 1 : 0u) : (uint32_t)__ballot(in) & ((1u << SUB) - 1);
-  };
+      const int piece = v_q * 4 + v_g;
+      s_v[buf][value_piece<D>(v_el, piece)] =
+          join8(decode2<FMT, false>(e[0]), decode2<FMT, false>(e[1]), decode2<FMT, false>(e[2]),
+                decode2<FMT, false>(e[3]));
+      s_v[buf][value_piece<D>(v_el + 1, piece)] =
+          join8(decode2<FMT, true>(e[0]), decode2<FMT, true>(e[1]), decode2<FMT, true>(e[2]), decode2<FMT, true>(e[3]));
+      s_v[buf][value_piece<D>(v_el + 2, piece)] = join8(decode2<FMT, false>(e2[0]), decode2<FMT, false>(e2[1]),
+                                                        decode2<FMT, false>(e2[2]), decode2<FMT, false>(e2[3]));
+      s_v[buf][value_piece<D>(v_el + 3, piece)] =
+          join8(decode2<FMT, true>(e2[0]), decode2<FMT, true>(e2[1]), decode2<FMT, true>(e2[2]),
+                decode2<FMT, true>(e2[3]));
+    };
+    auto there = [&](int32_t pages) {  // bit per sub-tile
+      const bool in = (uint32_t)pages < (uint32_t)a.b.pages;
+      return ONE ? (in ? (1u << SUB) - 1 : 0u) : (uint32_t)__ballot(in) & ((1u << SUB) - 1);
+    };
 
-  // Codes of two steps are in flight: those of the next one, which go to LDS
-  // during this one, and those of the one after (short prompts have few steps
-  // and cold caches: with one step in flight they waited for memory in each).
-  // Steps alternate between two sets, in a loop unrolled by two: moving a set
-  // would wait for it.
-  struct Flight {
-    Staged<D> st;
-    uint32_t ks, vs, ok;
-  };
-  Flight even, odd;  // of the steps step0, step0 + 2, ... and the others
-  int32_t pages2 = -1;
-  // (Behind the last step it reads page 0: with a branch around the loads, the
-  // next wait for older ones would wait for these.)
-  auto fetch_at = [&](int32_t step, int32_t pages, Flight& to) {
-    fetch(lo + step * PR_TILE, pages, &to.st, &to.ks, &to.vs);
-    to.ok = there(pages);
-  };
-  even.ks = even.vs = even.ok = odd.ks = odd.vs = odd.ok = 0;
-  if (step0 < step1) {
-    const int32_t t = lo + step0 * PR_TILE;
-    const int32_t p0 = page_at(t), p1 = page_at(t + PR_TILE), p2 = page_at(t + 2 * PR_TILE);
-    fetch_at(step0, p0, even);
-    fetch_at(step0 + 1, p1, odd);
-    pages2 = p2;
-  }
-  // this wave's rows (those behind the last one repeat it)
-  h8 qh[RT][KS], ql[RT][KS];
-  float f[RT];
-  Sight see[RT];
-  if (TREE) __syncthreads();  // the rows' masks are in LDS
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    int r = wave * WROWS + rt * 16 + j;
-    r = row0 + (r < rows ? r : rows - 1);
-    const int i = r / group;
-    if (!TREE) see[rt] = sight_of(pos + i, hi, a.window);
-    const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride + (int64_t)(head * group + r - i * group) * D;
-    float x[KS][8], top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) load_n<8>(src + (k * 4 + g) * 8, a.q_vec != 0, x[k]);
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
-    // the scale's sign goes into q: what is left of it keeps the scores' order
-    top = max_of_row(top);
-    const float by = power_of_row(top);
-    f[rt] = factor_of_row(a.scale, top, by);
-    const float mul = a.scale < 0.0f ? -by : by;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] *= mul;
-      qh[rt][k] = weights8(x[k]);
-      if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
+    // Codes of two steps are in flight: those of the next one, which go to LDS
+    // during this one, and those of the one after (short prompts have few steps
+    // and cold caches: with one step in flight they waited for memory in each).
+    // Steps alternate between two sets, in a loop unrolled by two: moving a set
+    // would wait for it.
+    struct Flight {
+      Staged<D> st;
+      uint32_t ks, vs, ok;
+    };
+    Flight even, odd;  // of the steps step0, step0 + 2, ... and the others
+    int32_t pages2 = -1;
+    // (Behind the last step it reads page 0: with a branch around the loads, the
+    // next wait for older ones would wait for these.)
+    auto fetch_at = [&](int32_t step, int32_t pages, Flight& to) {
+      fetch(lo + step * PR_TILE, pages, &to.st, &to.ks, &to.vs);
+      to.ok = there(pages);
+    };
+    even.ks = even.vs = even.ok = odd.ks = odd.vs = odd.ok = 0;
+    if (step0 < step1) {
+      const int32_t t = lo + step0 * PR_TILE;
+      const int32_t p0 = page_at(t), p1 = page_at(t + PR_TILE), p2 = page_at(t + 2 * PR_TILE);
+      fetch_at(step0, p0, even);
+      fetch_at(step0 + 1, p1, odd);
+      pages2 = p2;
     }
-  }
-  if (step0 < step1) store(lo + step0 * PR_TILE, even.ok, even.st, even.vs, 0);
-  __syncthreads();
-  // the lane's pieces of a key by the product, and of a value's tokens by its
-  // half; the others lie at constant distances
-  int k_at[KS];
+    // this wave's rows (those behind the last one repeat it)
+    h8 qh[RT][KS], ql[RT][KS];
+    float f[RT];
+    Sight see[RT];
+    if (TREE) __syncthreads();  // the rows' masks are in LDS
 #pragma unroll
-  for (int k = 0; k < KS; ++k) k_at[k] = key_piece<D>(j, k * 4 + g);
-  const int v_at[2] = {value_piece<D>(j * ND, g), value_piece<D>(j * ND, 4 + g)};
-  // one step: its codes are in LDS buffer `buf` and its scales in `mine`, whose
-  // registers then take the step after the next
-  auto one_step = [&](int32_t step, int buf, Flight& mine, Flight& next) {
-    const int32_t t = lo + step * PR_TILE;
-    const uint32_t ks_l = mine.ks, vs_l = mine.vs, ok = mine.ok;
-    // the step's scales, those of sub-tile lane & 3 in each lane
-    const uint32_t there_now = ok;
-    // a poisoned page: its scores are NaN, its values count as any
-    const bool bad = ks_l >= 0x7F800000u || vs_l >= 0x7F800000u;
-    const float ks_lane = __uint_as_float(bad ? 0x7FC00000u : ks_l);  // (ONE: of the step)
-    // 0 where a sub-tile has no say in the unit (values of scale 0 are 0 in LDS)
-    const float vs_lane = (ONE ? there_now != 0 : there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
-    float v_hi = vs_lane, v_lo = vs_lane;
-    if (!ONE) {
-      v_hi = uniform(quad_max(vs_lane));
-      v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
+    for (int rt = 0; rt < RT; ++rt) {
+      int r = wave * WROWS + rt * 16 + j;
+      r = row0 + (r < rows ? r : rows - 1);
+      const int i = r / group;
+      if (!TREE) see[rt] = sight_of(pos + i, hi, a.window);
+      const T* src = static_cast<const T*>(a.q) + (first + i) * a.q_stride +
+                     (int64_t)(head * group + r - i * group) * D;
+      float x[KS][8], top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) load_n<8>(src + (k * 4 + g) * 8, a.q_vec != 0, x[k]);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
+      // the scale's sign goes into q: what is left of it keeps the scores' order
+      top = max_of_row(top);
+      const float by = power_of_row(top);
+      f[rt] = factor_of_row(a.scale, top, by);
+      const float mul = a.scale < 0.0f ? -by : by;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] *= mul;
+        qh[rt][k] = weights8(x[k]);
+        if (SPLIT) ql[rt][k] = rest8(x[k], qh[rt][k]);
+      }
     }
-    fetch_at(step + 2, pages2, mine);
-    pages2 = page_at(t + 3 * PR_TILE);
-    // Sub-tiles whose values' scales are far apart are taken one after the
-    // other: the weights of the smaller would lose bits below the larger.
-    const int passes = !ONE && v_hi > 0x1p10f * v_lo ? SUB : 1;
+    if (step0 < step1) store(lo + step0 * PR_TILE, even.ok, even.st, even.vs, 0);
+    __syncthreads();
+    // the lane's pieces of a key by the product, and of a value's tokens by its
+    // half; the others lie at constant distances
+    int k_at[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) k_at[k] = key_piece<D>(j, k * 4 + g);
+    const int v_at[2] = {value_piece<D>(j * ND, g), value_piece<D>(j * ND, 4 + g)};
+    // one step: its codes are in LDS buffer `buf` and its scales in `mine`, whose
+    // registers then take the step after the next
+    auto one_step = [&](int32_t step, int buf, Flight& mine, Flight& next) {
+      const int32_t t = lo + step * PR_TILE;
+      const uint32_t ks_l = mine.ks, vs_l = mine.vs, ok = mine.ok;
+      // the step's scales, those of sub-tile lane & 3 in each lane
+      const uint32_t there_now = ok;
+      // a poisoned page: its scores are NaN, its values count as any
+      const bool bad = ks_l >= 0x7F800000u || vs_l >= 0x7F800000u;
+      const float ks_lane = __uint_as_float(bad ? 0x7FC00000u : ks_l);  // (ONE: of the step)
+      // 0 where a sub-tile has no say in the unit (values of scale 0 are 0 in LDS)
+      const float vs_lane = (ONE ? there_now != 0 : there_now >> (lane & 3) & 1) && !bad ? __uint_as_float(vs_l) : 0.0f;
+      float v_hi = vs_lane, v_lo = vs_lane;
+      if (!ONE) {
+        v_hi = uniform(quad_max(vs_lane));
+        v_lo = uniform(-quad_max(vs_lane > 0.0f ? -vs_lane : -INFINITY));
+      }
+      fetch_at(step + 2, pages2, mine);
+      pages2 = page_at(t + 3 * PR_TILE);
+      // Sub-tiles whose values' scales are far apart are taken one after the
+      // other: the weights of the smaller would lose bits below the larger.
+      const int passes = !ONE && v_hi > 0x1p10f * v_lo ? SUB : 1;
 #pragma unroll 1
-    for (int pass = 0; pass < passes; ++pass) {
-      const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
-      // The fences keep the compiler from loading all pieces at once, for which
-      // there are no registers: those of one sub-tile are loaded while the one
-      // before is multiplied.
-      f4 sc[RT][SUB];
-      h8 kf[2][KS];
+      for (int pass = 0; pass < passes; ++pass) {
+        const uint32_t here = passes > 1 ? there_now & (1u << pass) : there_now;
+        // The fences keep the compiler from loading all pieces at once, for which
+        // there are no registers: those of one sub-tile are loaded while the one
+        // before is multiplied.
+        f4 sc[RT][SUB];
+        h8 kf[2][KS];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k]];
+        for (int k = 0; k < KS; ++k) kf[0][k] = s_k[buf][k_at[k]];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        if (u + 1 < SUB) {
+        for (int u = 0; u < SUB; ++u) {
+          if (u + 1 < SUB) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            kf[(u + 1) & 1][k] = s_k[buf][k_at[k] + (u + 1) * 16 * (D / 8)];
+            for (int k = 0; k < KS; ++k)
+              kf[(u + 1) & 1][k] = s_k[buf][k_at[k] + (u + 1) * 16 * (D / 8)];
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], qh[rt][k], sc[rt][u], 0, 0, 0);
+              if (SPLIT)
+                sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], ql[rt][k], sc[rt][u], 0, 0, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        // scores are sc * c
+        float c[RT][SUB];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) sc[rt][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+          for (int rt = 0; rt < RT; ++rt)
+            c[rt][u] = ONE ? f[rt] * ks_lane : f[rt] * lane_of(ks_lane, u);
+        if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], qh[rt][k], sc[rt][u], 0, 0, 0);
-            if (SPLIT) sc[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u & 1][k], ql[rt][k], sc[rt][u], 0, 0, 0);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // scores are sc * c
-      float c[RT][SUB];
+            if (TREE) {
+              const int row = wave * WROWS + rt * 16 + j;
+              uint64_t bits = t + PR_TILE - 1 > all_high ? s_bits[t / PR_TILE - (all_high + 1) / PR_TILE][row] : ~0ull;
+              if (t <= all_low) {
+                const int32_t hidden = s_low[row] + 1 - t;
+                bits = hidden >= PR_TILE ? 0ull : hidden > 0 ? bits & ~0ull << hidden : bits;
+              }
+              bits >>= g * 4;
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+              for (int u = 0; u < SUB; ++u) {
+                sc[rt][u] *= c[rt][u];
+                c[rt][u] = 1.0f;
+                const uint32_t of_sub = here >> u & 1 ? (uint32_t)(bits >> (16 * u)) : 0u;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          c[rt][u] = ONE ? f[rt] * ks_lane : f[rt] * lane_of(ks_lane, u);
-      if (here != (1u << SUB) - 1 || t + PR_TILE - 1 > all_high || t <= all_low) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          if (TREE) {
-            const int row = wave * WROWS + rt * 16 + j;
-            uint64_t bits = t + PR_TILE - 1 > all_high ? s_bits[t / PR_TILE - (all_high + 1) / PR_TILE][row] : ~0ull;
-            if (t <= all_low) {
-              const int32_t hidden = s_low[row] + 1 - t;
-              bits = hidden >= PR_TILE ? 0ull : hidden > 0 ? bits & ~0ull << hidden : bits;
+                for (int r = 0; r < 4; ++r)
+                  if (!(of_sub >> r & 1)) sc[rt][u][r] = -INFINITY;
+              }
+              continue;
             }
-            bits >>= g * 4;
+            int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
+            // not to be compared outside this branch: most steps hide nothing
+            asm volatile("" : "+v"(high), "+v"(low));
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
               sc[rt][u] *= c[rt][u];
               c[rt][u] = 1.0f;
-              const uint32_t of_sub = here >> u & 1 ? (uint32_t)(bits >> (16 * u)) : 0u;
+              const int32_t high_u = here >> u & 1 ? high : -PR_TILE;
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (!(of_sub >> r & 1)) sc[rt][u][r] = -INFINITY;
+                if (16 * u + r > high_u || 16 * u + r <= low) sc[rt][u][r] = -INFINITY;
             }
-            continue;
           }
-          int32_t high = see[rt].high - t - g * 4, low = see[rt].low - t - g * 4;
-          // not to be compared outside this branch: most steps hide nothing
-          asm volatile("" : "+v"(high), "+v"(low));
+        }
+        float ref[RT], top[RT];
+        bool over = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          top[rt] = -INFINITY;
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {
-            sc[rt][u] *= c[rt][u];
-            c[rt][u] = 1.0f;
-            const int32_t high_u = here >> u & 1 ? high : -PR_TILE;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (16 * u + r > high_u || 16 * u + r <= low) sc[rt][u][r] = -INFINITY;
+            float x = max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]);
+            if (!ONE) x *= c[rt][u];
+            top[rt] = max_of(top[rt], x);
           }
+          top[rt] = max_of_row(ONE ? top[rt] * c[rt][0] : top[rt]);
+          over = over || top[rt] > m[rt] + kSlack;
         }
-      }
-      float ref[RT], top[RT];
-      bool over = false;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        top[rt] = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          float x = max_of(max_of(max_of(sc[rt][u][0], sc[rt][u][1]), sc[rt][u][2]), sc[rt][u][3]);
-          if (!ONE) x *= c[rt][u];
-          top[rt] = max_of(top[rt], x);
-        }
-        top[rt] = max_of_row(ONE ? top[rt] * c[rt][0] : top[rt]);
-        over = over || top[rt] > m[rt] + kSlack;
-      }
-      if (__any(over)) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const float mn = fmaxf(top[rt], m[rt]);
-          const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-          m[rt] = mn;
-          l[rt] *= alpha;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
-        }
-      }
-      // nothing seen so far (or only NaN): the weights are 0 (or NaN)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
-      if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
-      float up_lane = 0.0f, back_lane = 1.0f;
-      if (ONE) {
-        if (__float_as_uint(vs_lane) != now_vs) {  // another scale than the last step's
-          now_vs = __float_as_uint(vs_lane);
-          set_unit(vs_lane);
-          const float rel = vs_lane > 0.0f ? vs_lane * per_unit : 1.0f;
-          now_up = uniform(__builtin_amdgcn_logf(rel));
-          now_back = uniform(__builtin_amdgcn_rcpf(rel));
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) ref[rt] += now_up;
-      } else {
-        const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
-        set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
-        const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
-        up_lane = __builtin_amdgcn_logf(rel);
-        back_lane = __builtin_amdgcn_rcpf(rel);
-      }
-      float sum[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
-      h8 ph[RT][2], pl[RT][2];
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const float up = ONE ? 0.0f : lane_of(up_lane, u), back = ONE ? 1.0f : lane_of(back_lane, u);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          float w[4];
-          const float base = ONE ? ref[rt] : ref[rt] + up;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
-          if (ONE)
-            sum[rt] += (w[0] + w[1]) + (w[2] + w[3]);
-          else
-            l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int e = (u & 1) * 4 + r;
-            ph[rt][u >> 1][e] = (_Float16)w[r];
-            if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
-          }
-        }
-      }
-      if (ONE) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      h8 vf[2][4];
-      auto load_values = [&](int i, h8* to) {  // products 4 i .. 4 i + 3 of both halves' 2 ND
-        const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-          to[d] = s_v[buf][v_at[h ^ (d0 >> 2)] + (d0 + d) * 16 * (PR_TILE / 8)];
-      };
-      load_values(0, vf[0]);
-#pragma unroll
-      for (int i = 0; i < ND / 2; ++i) {
-        if (i + 1 < ND / 2) load_values(i + 1, vf[(i + 1) & 1]);
-        __builtin_amdgcn_sched_barrier(0);
-        const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
+        if (__any(over)) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            f4& acc = o[rt][d0 + d];
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], ph[rt][h], acc, 0, 0, 0);
-            if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], pl[rt][h], acc, 0, 0, 0);
+            const float mn = fmaxf(top[rt], m[rt]);
+            const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
+            m[rt] = mn;
+            l[rt] *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[rt][d] *= alpha;
           }
+        }
+        // nothing seen so far (or only NaN): the weights are 0 (or NaN)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) ref[rt] = kWeightExp - (m[rt] == -INFINITY ? 0.0f : m[rt]);
+        if (pass == 0) store(t + PR_TILE, next.ok, next.st, next.vs, buf ^ 1);  // behind the last step: never read
+        float up_lane = 0.0f, back_lane = 1.0f;
+        if (ONE) {
+          if (__float_as_uint(vs_lane) != now_vs) {  // another scale than the last step's
+            now_vs = __float_as_uint(vs_lane);
+            set_unit(vs_lane);
+            const float rel = vs_lane > 0.0f ? vs_lane * per_unit : 1.0f;
+            now_up = uniform(__builtin_amdgcn_logf(rel));
+            now_back = uniform(__builtin_amdgcn_rcpf(rel));
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) ref[rt] += now_up;
+        } else {
+          const float vs_here = here >> (lane & 3) & 1 ? vs_lane : 0.0f;
+          set_unit(passes > 1 ? uniform(quad_max(vs_here)) : v_hi);
+          const float rel = vs_here > 0.0f ? vs_here * per_unit : 1.0f;
+          up_lane = __builtin_amdgcn_logf(rel);
+          back_lane = __builtin_amdgcn_rcpf(rel);
+        }
+        float sum[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
+        h8 ph[RT][2], pl[RT][2];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const float up = ONE ? 0.0f : lane_of(up_lane, u), back = ONE ? 1.0f : lane_of(back_lane, u);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            float w[4];
+            const float base = ONE ? ref[rt] : ref[rt] + up;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][u][r], c[rt][u], base));
+            if (ONE)
+              sum[rt] += (w[0] + w[1]) + (w[2] + w[3]);
+            else
+              l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int e = (u & 1) * 4 + r;
+              ph[rt][u >> 1][e] = (_Float16)w[r];
+              if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
+            }
+          }
+        }
+        if (ONE) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
+        }
         __builtin_amdgcn_sched_barrier(0);
+        h8 vf[2][4];
+        auto load_values = [&](int i, h8* to) {  // products 4 i .. 4 i + 3 of both halves' 2 ND
+          const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            to[d] = s_v[buf][v_at[h ^ (d0 >> 2)] + (d0 + d) * 16 * (PR_TILE / 8)];
+        };
+        load_values(0, vf[0]);
+#pragma unroll
+        for (int i = 0; i < ND / 2; ++i) {
+          if (i + 1 < ND / 2) load_values(i + 1, vf[(i + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              f4& acc = o[rt][d0 + d];
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], ph[rt][h], acc, 0, 0, 0);
+              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], pl[rt][h], acc, 0, 0, 0);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-    }
-    __syncthreads();
-  };
+      __syncthreads();
+    };
 #pragma unroll 1
-  for (int32_t step = step0; step < step1; step += 2) {
-    one_step(step, 0, even, odd);
-    if (step + 1 < step1) one_step(step + 1, 1, odd, even);
-  }
-
-  // Rows of the result: a lane has the elements (g * 4 + r) * ND + d of row j.
-  // They go through LDS, 16 rows of a wave at a time, so that memory sees whole
-  // rows: stored from here, 8 bytes of 64 places at a time, they cost as much as
-  // a prompt's first hundreds of tokens.
-  float* rowbuf = reinterpret_cast<float*>(wave < 2 ? s_k[wave] : s_v[wave - 2]);  // 16 rows of D floats a wave
-  static_assert(sizeof(s_k[0]) >= 16 * D * sizeof(float), "a buffer holds a tile of rows");
-  // TREE: slot 0 of the block for a part that does not start its item, 1 for one that does
-  float* mine = parts + (TREE ? (int64_t)blockIdx.x * 2 + (step0 == 0 ? 1 : 0)
-                              : (bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const float sum = sum_of_row(l[rt]);
-    const int r0 = wave * WROWS + rt * 16;
-    const float by = part ? unit : sum == 0.0f ? 0.0f : unit / sum;
-    if (part && g == 0 && r0 + j < rows) {
-      mine[PR_ROWS * D + r0 + j] = m[rt];
-      mine[PR_ROWS * D + PR_ROWS + r0 + j] = sum;
+    for (int32_t step = step0; step < step1; step += 2) {
+      one_step(step, 0, even, odd);
+      if (step + 1 < step1) one_step(step + 1, 1, odd, even);
     }
-    // 16-byte pieces, exchanged by the row so that neighbouring rows fall on different banks
-    auto piece = [&](int row, int x) { return row * D + ((x ^ (row & 7)) << 2); };
-    __builtin_amdgcn_wave_barrier();
+
+    // Rows of the result: a lane has the elements (g * 4 + r) * ND + d of row j.
+    // They go through LDS, 16 rows of a wave at a time, so that memory sees whole
+    // rows: stored from here, 8 bytes of 64 places at a time, they cost as much as
+    // a prompt's first hundreds of tokens.
+    float* rowbuf = reinterpret_cast<float*>(wave < 2 ? s_k[wave] : s_v[wave - 2]);  // 16 rows of D floats a wave
+    static_assert(sizeof(s_k[0]) >= 16 * D * sizeof(float), "a buffer holds a tile of rows");
+    // TREE: slot 0 of the block for a part that does not start its item, 1 for one that does
+    float* mine = parts + (TREE ? (int64_t)blockIdx.x * 2 + (step0 == 0 ? 1 : 0)
+                                : (bt * a.kv_heads + head) * splits + z) * PR_ROWS * (D + 2);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int rt = 0; rt < RT; ++rt) {
+      const float sum = sum_of_row(l[rt]);
+      const int r0 = wave * WROWS + rt * 16;
+      const float by = part ? unit : sum == 0.0f ? 0.0f : unit / sum;
+      if (part && g == 0 && r0 + j < rows) {
+        mine[PR_ROWS * D + r0 + j] = m[rt];
+        mine[PR_ROWS * D + PR_ROWS + r0 + j] = sum;
+      }
+      // 16-byte pieces, exchanged by the row so that neighbouring rows fall on different banks
+      auto piece = [&](int row, int x) { return row * D + ((x ^ (row & 7)) << 2); };
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int x = 0; x < ND / 4; ++x)
-        *reinterpret_cast<f4*>(rowbuf + piece(j, (g * 4 + r) * (ND / 4) + x)) =
-            f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]} * by;
-    __builtin_amdgcn_wave_barrier();
-    constexpr int LANES = D / 4, STEP_ROWS = 64 / LANES;  // lanes of a row
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int i = 0; i < 16; i += STEP_ROWS) {
-      const int r = i + lane / LANES, x = lane % LANES;
-      const f4 y = *reinterpret_cast<const f4*>(rowbuf + piece(r, x));
-      if (r0 + r >= rows) continue;
-      if (part) {
-        *reinterpret_cast<f4*>(mine + (r0 + r) * D + x * 4) = y;
-      } else {
-        const int row = row0 + r0 + r, tok = row / group;
-        T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride +
-                 (int64_t)(head * group + row - tok * group) * D;
-        const float v[4] = {y[0], y[1], y[2], y[3]};
-        store_n<4>(out + x * 4, out_vec != 0, v);
+        for (int x = 0; x < ND / 4; ++x)
+          *reinterpret_cast<f4*>(rowbuf + piece(j, (g * 4 + r) * (ND / 4) + x)) =
+              f4{o[rt][x * 4][r], o[rt][x * 4 + 1][r], o[rt][x * 4 + 2][r], o[rt][x * 4 + 3][r]} * by;
+      __builtin_amdgcn_wave_barrier();
+      constexpr int LANES = D / 4, STEP_ROWS = 64 / LANES;  // lanes of a row
+#pragma unroll
+      for (int i = 0; i < 16; i += STEP_ROWS) {
+        const int r = i + lane / LANES, x = lane % LANES;
+        const f4 y = *reinterpret_cast<const f4*>(rowbuf + piece(r, x));
+        if (r0 + r >= rows) continue;
+        if (part) {
+          *reinterpret_cast<f4*>(mine + (r0 + r) * D + x * 4) = y;
+        } else {
+          const int row = row0 + r0 + r, tok = row / group;
+          T* out = static_cast<T*>(a.out) + (first + tok) * a.out_stride +
+                   (int64_t)(head * group + row - tok * group) * D;
+          const float v[4] = {y[0], y[1], y[2], y[3]};
+          store_n<4>(out + x * 4, out_vec != 0, v);
+        }
       }
     }
-  }
-  if (!TREE) return;
+    if (!TREE) return;
   }
 }
 
@@ -1600,7 +1605,8 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, 8, true, TREE>), grid, dim3(512), 0, s, a, parts);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, AT_W, false, TREE>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts);
+  hipLaunchKernelGGL((k_attend_split<DT, FMT, D, RT, AT_W, false, TREE>), dim3((unsigned)nb), dim3(AT_T), 0, s, a,
+                     parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // rows of a joining block: one where an item has many parts on average, so
@@ -1610,11 +1616,11 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const bool many = nb >= 16 * (int64_t)a.b.seqs * a.kv_heads;
   const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
   if (many)
-    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb,
-                       (const uint64_t*)nullptr);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts,
+                       (uint32_t)nb, (const uint64_t*)nullptr);
   else
-    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts, (uint32_t)nb,
-                       (const uint64_t*)nullptr);
+    hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts,
+                       (uint32_t)nb, (const uint64_t*)nullptr);
   return hipGetLastError();
 }
 
@@ -1626,11 +1632,11 @@ static hipError_t prompt_rt(const AttendArgs& a, const PromptShape& p, hipStream
   const int32_t tiles = (int32_t)p.tiles;
   const dim3 grid((unsigned)(p.tiles * a.kv_heads), (unsigned)p.splits);
   if (a.page_tokens >= PR_TILE)
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
-                       out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles,
+                       p.splits, out_vec);
   else
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles, p.splits,
-                       out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, false>), grid, dim3(AT_T), 0, s, a, parts, tiles,
+                       p.splits, out_vec);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 rows((unsigned)a.kv_heads, (unsigned)(p.tiles * prompt_rows<RT>() / 8));  // splits: few tiles
@@ -1648,7 +1654,9 @@ static bool tree_whole(const AttendArgs& a) {
   const int64_t items = ((int64_t)a.b.tokens * (a.q_heads / a.kv_heads) + 15) / 16 * a.kv_heads;
   return span_of(a) <= whole_tokens(1) && items <= 3 * (int64_t)cu_count();
 }
-static int tree_rows(int32_t seqs, int64_t tokens, int32_t group) { return tokens * group <= 64 * (int64_t)seqs ? 1 : 2; }
+static int tree_rows(int32_t seqs, int64_t tokens, int32_t group) {
+  return tokens * group <= 64 * (int64_t)seqs ? 1 : 2;
+}
 
 template <int DT, int FMT, int D, int RT>
 static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
@@ -1660,8 +1668,8 @@ static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, true, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts, 0,
                        1, out_vec);
   else
-    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts, 0,
-                       1, out_vec);
+    hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts,
+                       0, 1, out_vec);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t blocks = tiles * (prompt_rows<RT>() / 8);
@@ -1700,7 +1708,8 @@ static hipError_t attend_dim(const AttendArgs& a, hipStream_t s) {
 
 template <int DT, bool TREE>
 static hipError_t attend_fmt(const AttendArgs& a, hipStream_t s) {
-  return a.format == EFFORT_KV_I8 ? attend_dim<DT, EFFORT_KV_I8, TREE>(a, s) : attend_dim<DT, EFFORT_KV_E4M3, TREE>(a, s);
+  return a.format == EFFORT_KV_I8 ? attend_dim<DT, EFFORT_KV_I8, TREE>(a, s)
+                                  : attend_dim<DT, EFFORT_KV_E4M3, TREE>(a, s);
 }
 
 template <bool TREE>

@@ -326,7 +326,8 @@ int effort_beam_select(int32_t dtype, const void* logits_dev, int64_t stride, co
   if (!dtype_ok(dtype) || !beam_sizes_ok(items, beams, vocab) || keep < 1 || keep > EFFORT_BEAM_MAX_KEEP)
     return EFFORT_EINVAL;
   if (items == 0) return EFFORT_OK;  // nothing to do: the arrays may be null
-  if (!rows_ok(logits_dev, stride, vocab, bytes_of(dtype)) || !scores_dev || !aligned(scores_dev, 4)) return EFFORT_EINVAL;
+  if (!rows_ok(logits_dev, stride, vocab, bytes_of(dtype)) || !scores_dev || !aligned(scores_dev, 4))
+    return EFFORT_EINVAL;
   for (const void* p : {(const void*)out_scores_dev, (const void*)out_parents_dev, (const void*)out_tokens_dev})
     if (!p || !aligned(p, 4)) return EFFORT_EINVAL;
   const int bad = space_of(ws_dev, ws_bytes, beam_workspace(items * beams, vocab));

@@ -174,7 +174,8 @@ class KVCache(_Kept):
                                       k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self._ws_bytes = {}
         # for calls that take many caches (pages.py): the descriptor's bytes, and what they must share
-        self._packed, self._alike = bytes(self.desc), (self.pages, self.page_tokens, self.device.index, self.device.type)
+        self._packed = bytes(self.desc)
+        self._alike = (self.pages, self.page_tokens, self.device.index, self.device.type)
 
     def __reduce__(self):
         return KVCache.wrap, (self.k, self.v, self.k_scale, self.v_scale, self.format)

@@ -202,7 +202,8 @@ def beam_select(logits, scores, keep=None, ended=None, end_token: int = 0, out=N
             o = tuple(out)
             if [t.dtype for t in o] != [torch.float32, torch.int32, torch.int32] or \
                     any(t.shape != (items, keep) or t.device != dev or not t.is_contiguous() for t in o):
-                raise ValueError("out must be contiguous float32, int32, int32 tensors [%d][%d] on %s" % (items, keep, dev))
+                raise ValueError("out must be contiguous float32, int32, int32 tensors [%d][%d] on %s" % (
+                    items, keep, dev))
         ws = scores.new_empty(n, dtype=torch.uint8) if n else None
         B.effort_beam_select(dt, logits, stride, scores, ended, end_token, items, beams, vocab, keep, *o, ws, n, handle)
         return o

@@ -235,6 +235,18 @@ def test_rows_behind_the_last_sequence_stay_and_scales_are_signed(room):
     c.check_tree(q[:40], scale=0.0)
 
 
+@pytest.mark.parametrize("lens,new,cols", [([1300, 1200, 40], [20, 20, 20], 70), ([1130, 1119], [30, 12], 70),
+                                           ([1300, 1200], [20, 40], 65), ([500, 130], [20, 40], 8)])
+def test_lengths_beyond_the_table(lens, new, cols):
+    """Tokens behind the last page of the table are not seen, new ones nor committed ones."""
+    c = Tree(16, lens, new, group=4, page=16, dtype="bf16")
+    c.table = np.ascontiguousarray(c.table[:, :cols])
+    c.batch = E.KVBatch(ints(c.table.tolist()), c.batch.kv_lens, c.batch.q_starts, parents=c.batch.parents)
+    q = c.rand(8)
+    c.check_tree(q)
+    c.check_tree(q, window=300)
+
+
 # ---------------------------------------------------------------- pages
 
 class Pool:
