@@ -128,13 +128,30 @@ __device__ inline double sum_of_lanes(double x, bool sixteen) {
   return sixteen ? dpp_add<0x140>(x) : x;  // row_mirror: the other eight
 }
 
-// 1 / rms of the head that a chunk's lanes share.  The squares of 32-bit numbers and
-// their sum fit double whatever they are: a head of the largest ones has a norm, too.
-__device__ inline double unit_of(const float* x, double per_dim, double eps, bool sixteen) {
+// The mean square, and eps, of the head that a chunk's lanes share.  The squares of 32-bit
+// numbers and their sum fit double whatever they are: a head of the largest ones has a
+// norm, too.
+__device__ inline double square_of(const float* x, double per_dim, double eps, bool sixteen) {
   double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < 2 * CP; ++j) sum = __builtin_fma((double)x[j], (double)x[j], sum);
-  return 1.0 / sqrt(__builtin_fma(sum_of_lanes(sum, sixteen), per_dim, eps));
+  return __builtin_fma(sum_of_lanes(sum, sixteen), per_dim, eps);
+}
+
+// A query's chunk normed: 1 / rms to some 2^-45 (the instruction's 2^-24 and a step of
+// Newton's; the exact root and quotient, and products in double, cost the prompts above
+// 1.7 us more), its product with the weight rounded to fp32, and the element's product
+// with that.
+__device__ inline void norm_near(float* x, const float* weight, double square) {
+  const double near = __builtin_amdgcn_rsq(square);
+  const double by = square == (double)INFINITY ? 0.0 : near * (1.5 - 0.5 * square * near * near);
+  if (__any(!(by > 0x1p-60 && by < 0x1p60))) {  // the weights might leave fp32
+#pragma unroll
+    for (int j = 0; j < 2 * CP; ++j) x[j] = (float)((double)x[j] * by * (double)weight[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2 * CP; ++j) x[j] *= (float)(by * (double)weight[j]);
+  }
 }
 
 // Query heads of a thread: they share its cosines and sines (the prompts above:
@@ -154,11 +171,12 @@ constexpr int AP_QH = 4;
 // EX: with head norms or a tree, which the others need no registers for.  A key's norm
 // is taken in double like its rotation, and rounded with it: the codes are the nearest
 // ones.  A tree's depths come from its parents in LDS, asked for before the rows.  The
-// prompts above with both norms: 46.5 us, the norms' sums and products in double hidden
-// behind the bytes; one token 4.8 (without norms 4.1), 12 trees of up to 16 6.0.
+// prompts above with both norms: 50.6 us, with caches warm 41.5 (45 with the 102 registers,
+// for four waves a SIMD, that it would take for itself; fp32 rows have no room for five); one
+// token 4.7 (without norms 4.1), 12 trees of up to 16 6.0.
 template <int DT, int FMT, int IT, bool EX>
-__global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token,
-                                                 int32_t kv_vec, int32_t q_vec) {
+__global__ __launch_bounds__(AP_T, EX && IT == 4 && DT != EFFORT_F32 ? 5 : 1)
+void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token, int32_t kv_vec, int32_t q_vec) {
   typedef typename ElemOf<DT>::T T;
   const int tid = (int)threadIdx.x;
   const int dim = a.dim, cpr_log = __builtin_ctz(dim / (2 * CP));  // chunks of a row: a power of two
@@ -231,9 +249,7 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, i
       float y[2 * CP], z[2 * CP];
       if (norm) {
         if (a.q_norm_stride) load_weights(h);
-        const double by = unit_of(x[h], per_dim, a.eps, sixteen);
-#pragma unroll
-        for (int j = 0; j < 2 * CP; ++j) x[h][j] = (float)((double)x[h][j] * by * (double)weight[j]);
+        norm_near(x[h], weight, square_of(x[h], per_dim, a.eps, sixteen));
       }
       from_order(k.rotated && inter, x[h]);
       if (k.rotated) {
@@ -336,7 +352,7 @@ __global__ __launch_bounds__(AP_T) void k_append(AppendArgs a, uint32_t first, i
   auto finish = [&](float* x, int r, const Chunk& k, double* z) {
     double by[2 * CP];
     if (EX) {
-      const double unit = norm ? unit_of(x, per_dim, a.eps, sixteen) : 1.0;
+      const double unit = norm ? 1.0 / sqrt(square_of(x, per_dim, a.eps, sixteen)) : 1.0;
 #pragma unroll
       for (int j = 0; j < 2 * CP; ++j) by[j] = norm ? (double)x[j] * unit * (double)weight[j] : (double)x[j];
     }
