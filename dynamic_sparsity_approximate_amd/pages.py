@@ -65,7 +65,7 @@ class KVPages(_Kept):
     A KVBatch over the same page_table and kv_lens sees every change.  Calls on
     one KVPages, or on several with one refs, must be ordered."""
 
-    _kept = frozenset(("caches", "page_table", "kv_lens", "refs", "info", "_missing", "device", "seqs"))
+    _kept = frozenset(("caches", "page_table", "kv_lens", "refs", "info", "_missing", "_ws", "device", "seqs"))
 
     def __init__(self, caches, page_table, kv_lens, refs=None):
         s = self.caches = _set(caches)
@@ -84,7 +84,8 @@ class KVPages(_Kept):
         stride = page_table.stride(0) if self.seqs > 1 else cols
         self._book = B.effort_kv_book(self.seqs, cols, s.page_tokens, 0, s.pages, stride, page_table.data_ptr(),
                                       kv_lens.data_ptr(), refs.data_ptr(), self.info.data_ptr())
-        self._ws_bytes = B.effort_kv_grow_workspace_bytes(self._book)
+        # calls are ordered, because of refs, so that one workspace serves them all
+        self._ws = self.info.new_empty(B.effort_kv_grow_workspace_bytes(self._book), dtype=torch.uint8)
 
     def __reduce__(self):  # copies of the tensors have other addresses
         return KVPages, (self.caches.caches, self.page_table, self.kv_lens, self.refs)
@@ -112,13 +113,10 @@ class KVPages(_Kept):
         else:
             each, more = _vector(more, "more", self.seqs, self.device), 0
 
-        def call(handle):
-            # of this call alone: other captured graphs have their own
-            ws = self.info.new_empty(self._ws_bytes, dtype=torch.uint8)
-            B.effort_kv_grow(self._book, self.caches.descs, self.caches.count, each, more, ws, self._ws_bytes, handle)
-            return self._missing
-
-        return _run(self.device, stream, call)
+        s = self.caches
+        _run(self.device, stream, lambda handle: B.effort_kv_grow(
+            self._book, s.descs, s.count, each, more, self._ws, self._ws.shape[0], handle))
+        return self._missing
 
 
 def kv_copy_pages(caches, src, dst, stream=None):

@@ -509,3 +509,41 @@ def test_beams_of_more_items_than_a_launch_has_blocks():
     assert torch.equal(t[:, 0], (x[:, 1] > x[:, 0]).int())
     want = -torch.log1p(torch.exp(-(x[:, 0] - x[:, 1]).abs().double()))
     assert float((s[:, 0].double() - want).abs().max()) <= 2.0 ** -22 + 2.0 ** -24
+
+
+def test_caches_beyond_32_bits_do_what_small_ones_do():
+    """Codes behind 4 GiB: the same pages under low and high numbers."""
+    dev()
+    high, T, heads, dim = 33000, 128, 8, 128
+    rng = np.random.default_rng(7)
+    big = E.KVCache(high + 6, heads, dim, T)
+    small = E.KVCache(8, heads, dim, T)
+    for c in ("k", "v"):
+        getattr(small, c).copy_(cuda(L.encode(rng.standard_normal((8, heads, T, dim)) * 60, "e4m3")))
+        getattr(small, c + "_scale").copy_(cuda((2.0 ** rng.integers(-8, -3, (8, heads))).astype(np.float32)))
+        getattr(big, c)[high - 2:].copy_(getattr(small, c))
+        getattr(big, c + "_scale")[high - 2:].copy_(getattr(small, c + "_scale"))
+    new, lens = 20, [T * 2 + 5, T + 30]
+    par = ints(R.random_tree(rng, new) + R.random_tree(rng, new))
+    k, v, q = (cuda(rng.standard_normal((2 * new, h, dim)).astype(np.float32)) for h in (heads, heads, 2 * heads))
+    rope = E.rope_table(10000.0, 4 * T, dim)
+    got = []
+    for c, at in ((small, 0), (big, high - 2)):
+        table = [[at + 3, at + 1, at + 6, -1], [at + 2, at + 5, -1, -1]]
+        pages = E.KVPages([c], ints(table), ints([lens[0] - new, lens[1] - new]))
+        pages.refs[:max(at, 0)] = 1  # nothing free below
+        pages.fork(ints([0, 0]))
+        assert int(pages.grow(1)) == 0  # one copies the last page, which both hold
+        copy = c.k[int(pages.page_table[0, 1])].clone()
+        assert pages.page_table[0, 1] == at and pages.page_table[1, 1] == at + 1
+        pages.page_table.copy_(ints(table))
+        pages.kv_lens.copy_(ints(lens))
+        batch = E.KVBatch(pages.page_table, pages.kv_lens, ints([0, new, 2 * new]), parents=par)
+        a = c.append(batch, k, v, q=q, rope=rope, q_norm=torch.ones(dim, device="cuda"))
+        o = c.attend(batch, a)
+        n = E.kv_accept([c], batch, ints([new - 1, new - 2]), lens_out=ints([0, 0]))
+        E.kv_copy_pages([c], ints([at + 6]), ints([at + 7]))
+        torch.cuda.synchronize()
+        got.append([copy, a, o, n] + [t[at:at + 8].clone() for t in (c.k, c.v, c.k_scale, c.v_scale)])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
