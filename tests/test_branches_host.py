@@ -252,3 +252,52 @@ def test_beam_definition_against_all_pairs():
     got = R.beams(x, s, 7)
     assert got[1][0] == (order // 11).tolist() and got[2][0] == (order % 11).tolist()
     assert np.allclose(got[0][0], y.ravel()[order])
+
+
+def test_beam_step_refuses_what_does_not_fit():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    z, i32 = torch.zeros, dict(dtype=torch.int32)
+    k, s = z(4, 2, 16, 64, dtype=torch.uint8), z(4, 2)
+    one, other = (E.KVCache.wrap(k.clone(), k.clone(), s.clone(), s.clone()) for _ in range(2))
+    table, lens = z(6, 3, **i32), z(6, **i32)
+    pages = E.KVPages([one], table, lens)
+
+    def step(rows=6, batch=None, caches=(one,)):
+        return SimpleNamespace(x=z(rows, 8), batch=batch or E.KVBatch(table, lens, z(7, **i32)), caches=list(caches))
+
+    beam = E.BeamStep(step(), pages, 3)
+    assert beam.scores.tolist() == [[0.0, -math.inf, -math.inf]] * 2 and not beam.ended.any()
+    tree = E.KVBatch(table, lens, z(7, **i32), parents=z(6, **i32))
+    wide = E.KVBatch(table[:5], lens[:5], z(6, **i32))
+    for bad in (dict(beams=4), dict(beams=0), dict(step=step(caches=[one, other])), dict(step=step(batch=tree)),
+                dict(step=step(batch=wide)), dict(step=step(rows=12)),
+                dict(step=step(batch=E.KVBatch(table.clone(), lens, z(7, **i32)))),
+                dict(step=step(batch=E.KVBatch(table, lens.clone(), z(7, **i32))))):
+        d = dict(step=step(), pages=pages, beams=3)
+        d.update(bad)
+        with pytest.raises(ValueError):
+            E.BeamStep(**d)
+
+
+def test_decoder_step_refuses_head_norms_and_trees_that_do_not_fit():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    z, i32 = torch.zeros, dict(dtype=torch.int32)
+    mat = lambda m, n: SimpleNamespace(in_dim=m, out_dim=n, batch=4, layout=z(1, dtype=torch.uint8))  # noqa: E731
+    layer = {"wq": mat(32, 128), "wk": mat(32, 64), "wv": mat(32, 64), "wo": mat(128, 32), "w1": mat(32, 48),
+             "w3": mat(32, 48), "w2": mat(48, 32)}
+    k, s = z(4, 1, 16, 64, dtype=torch.uint8), z(4, 1)
+    cache = E.KVCache.wrap(k, k.clone(), s, s.clone())
+    mk = lambda qk_norms=None, parents=None: E.DecoderStep(  # noqa: E731
+        [layer], mat(32, 10), z(3, 32), [cache], E.KVBatch(z(1, 2, **i32), z(1, **i32), z(2, **i32), parents=parents),
+        [(z(32), z(32))], z(32), qk_norms=qk_norms)
+    mk()
+    mk(qk_norms=[(z(64), z(1, 64))], parents=z(3, **i32))
+    mk(qk_norms=[(z(2, 64), None)])
+    for bad in (dict(qk_norms=[]), dict(qk_norms=[(z(63), None)]), dict(qk_norms=[(None, z(2, 64))]),
+                dict(qk_norms=[(z(64).half(), None)]), dict(qk_norms=[(z(128)[::2], None)]), dict(parents=z(2, **i32))):
+        with pytest.raises(ValueError):
+            mk(**bad)
