@@ -13,12 +13,14 @@
 // but for two exchanges across the four lanes of a row.
 // Codes become fp16 exactly (8 bits fit its 11); q is scaled per row by a power
 // of two into fp16's upper range.  fp32 rows of q, and the weights, are taken as
-// two fp16 parts each (22 bits) and the products run twice.  Only prompts with
-// 16-bit rows take the weights' upper part alone (11 bits, fewer below 2^-20 of
+// two fp16 parts each (22 bits) and the products run twice.  Only causal prompts
+// with 16-bit rows take the weights' upper part alone (11 bits, fewer below 2^-20 of
 // the reference): the other costs k_attend_split, which waits for memory, 0.2 to
 // 3 per cent, but two bf16 prompts of 4096 tokens 426 us instead of 317, for
 // errors of 2.07e-4 instead of 2.7e-4 (fp16) or 1.65e-3 instead of 1.66e-3 (bf16)
-// of the outputs, most of which is their own last rounding.
+// of the outputs, most of which is their own last rounding.  Trees keep both parts
+// whichever kernel takes them (eight trees of 32 tokens 74 us instead of 64, one of 64
+// 163 instead of 138): what a row becomes does not depend on how wide its table is.
 //
 // In a tree a new token sees the committed tokens, in front of the sequence's new ones,
 // and of those its ancestors and itself; a window counts by position, which is the first
@@ -876,8 +878,9 @@ template <int DT, int FMT, int D, bool ONE, int RT, bool TREE>
 __global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 ? 2 : 3) : DT == EFFORT_F32 && D == 128 ? 1 : 2)
 void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
-  constexpr bool SPLIT = DT == EFFORT_F32;
+  constexpr bool SPLIT = DT == EFFORT_F32, LOW = SPLIT || TREE;  // queries, weights in two parts
   constexpr int KS = D / 32, ND = D / 16, SUB = PR_SUB, PR_ROWS = prompt_rows<RT>(), WROWS = 16 * RT;
+  constexpr int VG = TREE && !SPLIT && RT == 2 ? 2 : 4;  // pieces of values that are loaded together
   __shared__ h8 s_k[2][PR_TILE * D / 8];
   __shared__ h8 s_v[2][PR_TILE * D / 8];
   __shared__ int s_seq;
@@ -1391,6 +1394,8 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
         float sum[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
+        float minus = -1.0f;
+        if (TREE) asm("" : "+s"(minus));
         h8 ph[RT][2], pl[RT][2];
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
@@ -1406,10 +1411,19 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
             else
               l[rt] = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), back, l[rt]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 4; r += 2) {
               const int e = (u & 1) * 4 + r;
-              ph[rt][u >> 1][e] = (_Float16)w[r];
-              if (SPLIT) pl[rt][u >> 1][e] = (_Float16)(w[r] - (float)ph[rt][u >> 1][e]);
+              h2 high = {(_Float16)w[r], (_Float16)w[r + 1]};
+              if (TREE) asm("" : "+v"(high));  // one conversion of both
+              ph[rt][u >> 1][e] = high[0];
+              ph[rt][u >> 1][e + 1] = high[1];
+              if (LOW) {
+                // (exact: as a product of 32 bits that takes the 16-bit number as it is)
+                const h2 low = {(_Float16)__builtin_fmaf((float)high[0], minus, w[r]),
+                                (_Float16)__builtin_fmaf((float)high[1], minus, w[r + 1])};
+                pl[rt][u >> 1][e] = low[0];
+                pl[rt][u >> 1][e + 1] = low[1];
+              }
             }
           }
         }
@@ -1418,27 +1432,27 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
           for (int rt = 0; rt < RT; ++rt) l[rt] = __builtin_fmaf(sum[rt], now_back, l[rt]);
         }
         __builtin_amdgcn_sched_barrier(0);
-        h8 vf[2][4];
-        auto load_values = [&](int i, h8* to) {  // products 4 i .. 4 i + 3 of both halves' 2 ND
-          const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+        h8 vf[2][VG];
+        auto load_values = [&](int i, h8* to) {  // products VG i .. VG i + VG - 1 of both halves' 2 ND
+          const int h = i / (ND / VG), d0 = i % (ND / VG) * VG;
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
+          for (int d = 0; d < VG; ++d)
             to[d] = s_v[buf][v_at[h ^ (d0 >> 2)] + (d0 + d) * 16 * (PR_TILE / 8)];
         };
         load_values(0, vf[0]);
 #pragma unroll
-        for (int i = 0; i < ND / 2; ++i) {
-          if (i + 1 < ND / 2) load_values(i + 1, vf[(i + 1) & 1]);
+        for (int i = 0; i < 2 * ND / VG; ++i) {
+          if (i + 1 < 2 * ND / VG) load_values(i + 1, vf[(i + 1) & 1]);
           __builtin_amdgcn_sched_barrier(0);
-          const int h = i / (ND / 4), d0 = i % (ND / 4) * 4;
+          const int h = i / (ND / VG), d0 = i % (ND / VG) * VG;
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
+          for (int part = 0; part < (LOW ? 2 : 1); ++part)  // (a product waits for the last one into its sum)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              f4& acc = o[rt][d0 + d];
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], ph[rt][h], acc, 0, 0, 0);
-              if (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], pl[rt][h], acc, 0, 0, 0);
-            }
+            for (int d = 0; d < VG; ++d)
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt)
+                o[rt][d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i & 1][d], part ? pl[rt][h] : ph[rt][h],
+                                                                       o[rt][d0 + d], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }

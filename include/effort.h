@@ -496,6 +496,7 @@ int effort_kv_attention(const effort_kv_cache* cache, const effort_kv_batch* bat
    sequence's new ones, its ancestors among these and itself; with window > 0
    only those whose position is greater than its own minus window, positions
    being base + d.  A sequence that is no tree sees nothing: its rows become 0.
+   Rows of 16 bits keep 22 bits of the weights, too, however many they are.
    ws_dev: as there, of effort_kv_tree_workspace_bytes of the same arguments. */
 int effort_kv_tree_workspace_bytes(const effort_kv_cache* cache, int32_t seqs, int64_t tokens,
                                    int32_t q_heads, uint64_t* bytes);
