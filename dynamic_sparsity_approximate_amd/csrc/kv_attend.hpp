@@ -1700,10 +1700,11 @@ static hipError_t attend_prompt(const AttendArgs& a, hipStream_t s) {
     if (tree_whole(a)) return attend_rt<DT, FMT, D, 1, true>(a, s);
     return tree_rows(a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads) == 1 ? tree_rt<DT, FMT, D, 1>(a, s)
                                                                        : tree_rt<DT, FMT, D, 2>(a, s);
+  } else {
+    const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads,
+                                       (int64_t)a.b.max_pages * a.page_tokens);
+    return p.rt == 1 ? prompt_rt<DT, FMT, D, 1>(a, p, s) : prompt_rt<DT, FMT, D, 2>(a, p, s);
   }
-  const PromptShape p = prompt_shape(a.kv_heads, D, a.b.seqs, a.b.tokens, a.q_heads / a.kv_heads,
-                                     (int64_t)a.b.max_pages * a.page_tokens);
-  return p.rt == 1 ? prompt_rt<DT, FMT, D, 1>(a, p, s) : prompt_rt<DT, FMT, D, 2>(a, p, s);
 }
 
 template <int DT, int FMT, int D, bool TREE>
