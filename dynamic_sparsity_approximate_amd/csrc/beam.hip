@@ -199,8 +199,10 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
                                                     int32_t groups, int32_t wave_size, int32_t first) {
   typedef typename ElemOf<DT>::T T;
   __shared__ Cand s_list[BP_LIST], s_best[EFFORT_BEAM_MAX_KEEP];
-  __shared__ double s_add[EFFORT_BEAM_MAX];  // score minus log of the sum; -inf: continues nothing
-  __shared__ float s_near[EFFORT_BEAM_MAX], s_reach[EFFORT_BEAM_MAX];
+  // log of a beam's sum, and its score (-inf: continues nothing).  They stay apart: next to a
+  // large log sum the score would be lost, and the log sum has to meet the logit first.
+  __shared__ double s_lse[EFFORT_BEAM_MAX];
+  __shared__ float s_near[EFFORT_BEAM_MAX], s_score[EFFORT_BEAM_MAX], s_reach[EFFORT_BEAM_MAX];
   __shared__ uint32_t s_top[BP_T / 4];
   __shared__ int s_n, s_runs;
   __shared__ int32_t s_run[BP_RUNS];
@@ -235,13 +237,15 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
     // (0 where all of the row is forbidden)
-    const double add = !__any(bad) && sum > 0.0 ? (double)a.scores[row0 + b] - (ref + log(sum)) : -INFINITY;
+    const bool some = !__any(bad) && sum > 0.0;
     if (lane == 0) {
-      s_add[b] = add;
-      s_near[b] = add > -INFINITY ? fmaxf((float)add, -3.4e38f) : -INFINITY;
+      s_lse[b] = some ? ref + log(sum) : 0.0;
+      s_near[b] = some ? (float)s_lse[b] : 0.0f;
+      s_score[b] = some ? a.scores[row0 + b] : -INFINITY;
     }
   }
   __syncthreads();
+  auto value = [&](int b, float x) { return (double)s_score[b] + ((double)x - s_lse[b]); };
 
   // Runs of neighbouring groups: those of a reading wave, or single groups where there are
   // not many runs for each that is kept.  A first bound, a little too low: of the largest
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     }
   };
   float best = -INFINITY;
-  each_run(0, n, [&](float x, int b, int) __attribute__((always_inline)) { best = fmaxf(best, x + s_near[b]); });
+  each_run(0, n, [&](float x, int b, int) __attribute__((always_inline)) { best = fmaxf(best, (x - s_near[b]) + s_score[b]); });
   best = fmaxf(best, __shfl_xor(best, 1));
   best = fmaxf(best, __shfl_xor(best, 2));
   const uint32_t top = order_of(best);
@@ -301,12 +305,13 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     // roundings, 2^-24 of each of the numbers, of any beam.  A NaN lets nothing pass.
     const bool any = least > order_of(-INFINITY);
     const float bound = fminf(__uint_as_float(least >> 31 ? least & 0x7FFFFFFFu : ~least), 3.0e38f);
-    const float add = lane < beams ? s_near[lane] : -INFINITY;
-    float most = add > -INFINITY ? fabsf(add) : 0.0f;
+    const float near = lane < beams ? s_near[lane] : 0.0f, score = lane < beams ? s_score[lane] : -INFINITY;
+    float most = score > -INFINITY ? fmaxf(fabsf(near), fabsf(score)) : 0.0f;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
-    const float at = any ? bound - add - 0x1p-20f * (fabsf(bound) + most) : -INFINITY;
-    if (lane < beams) s_reach[lane] = add > -INFINITY ? at : __uint_as_float(0x7FC00000u);
+    const float slack = 0x1p-20f * fabsf(bound) + 0x1p-20f * most;
+    const float at = any ? (bound - score - slack) + near : -INFINITY;
+    if (lane < beams) s_reach[lane] = score > -INFINITY ? at : __uint_as_float(0x7FC00000u);
   }
   __syncthreads();
 
@@ -324,7 +329,7 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
   };
   auto take = [&](float x, int b, int g) __attribute__((always_inline)) {
     if (!(x >= s_reach[b]) || x == -INFINITY) return;
-    const Cand c = {order_of(s_add[b] + (double)x), low_of(b, x, (uint32_t)g)};
+    const Cand c = {order_of(value(b, x)), low_of(b, x, (uint32_t)g)};
     if (!(c > bound)) return;
     const int at = atomicAdd(&s_n, 1);
     if (at < BP_LIST) s_list[at] = c;
@@ -377,7 +382,7 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     const int32_t v = (int32_t)(0xFFFFFu - (uint32_t)(g.lo & 0xFFFFFu)) * BM_GROUP + (tid & 31);
     if (v >= a.vocab) continue;
     const float x = (float)static_cast<const T*>(a.logits)[(row0 + b) * a.stride + v];
-    const Cand c = {order_of(s_add[b] + (double)x), low_of(b, x, (uint32_t)v)};
+    const Cand c = {order_of(value(b, x)), low_of(b, x, (uint32_t)v)};
     if (x > -INFINITY && (c.hi > low.hi || (c.hi == low.hi && c.lo >= low.lo))) s_list[atomicAdd(&s_n, 1)] = c;
   }
   // an ended beam is its own only continuation

@@ -162,7 +162,9 @@ def beam_select(logits, scores, keep=None, ended=None, end_token: int = 0, out=N
     ended[b] (bool [items][beams]) continues with itself alone, its score
     unchanged and its token `end_token`.  Tokens with a logit of -inf, beams
     whose score is not finite and rows with a NaN or +inf are no candidates;
-    where there are fewer than `keep`, the rest are -inf, -1, -1.  Returns
+    where there are fewer than `keep`, the rest are -inf, -1, -1.  (Forbid tokens
+    with -inf, not with the lowest number: a row of nothing else is no dead end,
+    and beside it the logarithm of its length is lost.)  Returns
     (scores, parents, tokens), [items][keep]: parents are rows of the logits, as
     KVPages.fork takes them.  `out`: three tensors to write to; out[0] may be
     scores itself if keep == beams."""

@@ -596,7 +596,10 @@ int effort_kv_accept(const effort_kv_cache* caches, int32_t count, const effort_
    out_parents, t in out_tokens, each [items][keep].  Scores are compared in
    double, the logarithm's sum has 2^-22 or less of error; equal scores stand in
    the order of beams, a beam's by falling logits, and equal logits by rising
-   tokens.  A beam with ended_dev[b] != 0 has one candidate: itself, with its
+   tokens.  The logarithm is rounded to double, then taken from the logit, then
+   the score is added: next to a logit of 1e9 that rounding is 2^-24, and from 1e18
+   on nothing is left of what a sum of equal logits adds, so that a row of nothing
+   but -3.4e38 continues its beam at its score.  What is forbidden should be -inf.  A beam with ended_dev[b] != 0 has one candidate: itself, with its
    score unchanged and the token end_token.  A logit of -inf is no candidate; a
    row with a NaN, +inf or nothing but -inf, or with a score that is not finite,
    has none.  Where there are fewer than `keep`, the rest are -inf, -1, -1.

@@ -1,5 +1,7 @@
 """Edges of the operators for several continuations of a sequence: what 16-bit rows of trees
-keep of their weights."""
+keep of their weights, beams whose logits are large."""
+import math
+
 import numpy as np
 import pytest
 
@@ -9,8 +11,8 @@ torch = pytest.importorskip("torch")
 import _branches as R  # noqa: E402
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
-from test_gpu_branches import Tree  # noqa: E402
-from test_gpu_layer import f64, say  # noqa: E402
+from test_gpu_branches import Tree, cuda  # noqa: E402
+from test_gpu_layer import DT, dev, f64, say  # noqa: E402
 
 
 # ---------------------------------------------------------------- trees: what 16-bit rows keep
@@ -33,3 +35,55 @@ def test_trees_keep_the_weights_of_16_bit_rows(heads, group, dim, page, fmt, len
     worst = float((np.abs(got - ref) / (tol + 1e-300)).max())
     say("worst", worst)
     assert worst <= 1.0, worst
+
+
+# ---------------------------------------------------------------- beams: large logits
+
+def check_large(x, s, keep, **kw):
+    """beam_select against its definition, whatever the logits' size."""
+    got = E.beam_select(x, s, keep=keep, **kw)
+    torch.cuda.synchronize()
+    rows, scores = f64(x), f64(s)
+    ref = R.beams(rows, scores, keep)
+    a, b = f64(got[0]), np.array(ref[0])
+    assert got[1].tolist() == ref[1] and got[2].tolist() == ref[2]
+    assert np.array_equal(np.isinf(a), np.isinf(b))
+    # the sum's error in front of the logarithm and the result's own rounding; both sides round the log sum of a
+    # row to a double, 2^-53 of it each, and the difference to it is within those roundings of itself again
+    top = np.abs(np.where(np.isfinite(rows), rows, 0.0)).max(-1)
+    near = np.where(top < 2.0 ** 60, top, 0.0)  # beyond, no log sum reaches half a step
+    own = np.take_along_axis(near, np.maximum(np.array(ref[1]) - np.arange(len(rows))[:, None] * rows.shape[1], 0), 1)
+    ok = ~np.isinf(b)
+    d = np.abs(np.where(ok, a, 0.0) - np.where(ok, b, 0.0))
+    assert (d <= 2.0 ** -22 + 2.0 ** -24 * np.abs(np.where(ok, b, 0.0)) + 2.0 ** -51 * own).all(), d.max()
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("keep", [3, 64])
+def test_beams_of_rows_of_the_lowest_number_keep_their_scores(dtype, keep):
+    """A mask of the type's lowest number that forbids every token of a beam, next to beams that continue."""
+    dev()
+    rng = np.random.default_rng(62)
+    low = torch.finfo(DT[dtype]).min
+    x = cuda(rng.standard_normal((4, 3, 3001)).astype(np.float32)).to(DT[dtype])
+    s = cuda(np.array([[-12, -11, -3], [-1, -12.5, -14], [-40, -41, -30], [-7, -8, -9]], np.float32))
+    x[0, 0] = low
+    x[1, 2] = low
+    x[2, 1] = low
+    x[3] = low
+    check_large(x, s, keep)
+
+
+def test_beams_of_the_largest_scores_and_logits():
+    """The first bound must hold where a score and a log sum of the largest size meet."""
+    dev()
+    rng = np.random.default_rng(63)
+    x = rng.standard_normal((3, 4, 2600)).astype(np.float32)
+    x[0, 0] = 3.4e38
+    x[1, 1] = -3.4e38
+    x[1, 2, 7] = 3.4e38
+    x[2, 0], x[2, 1] = -3.4e38, 3.4e38
+    s = np.array([[-3.4e38, -5, -1e30, -6], [-2, 3.4e38, -3.4e38, 1e30], [3.4e38, -3.4e38, 3e38, -3e38]], np.float32)
+    for keep in (5, 128):
+        check_large(cuda(x), cuda(s), keep)
