@@ -49,9 +49,12 @@ __device__ inline float dpp_top(float x) {
 }
 
 constexpr float kHi = 1.4426950408889634f, kLo = 1.925963033500995e-8f;  // log2(e)
-// What a wave's exponentials are relative to: about its largest number, as a power of two
-// that fp32 has; numbers whose products would overflow, and -inf and NaN, stand for themselves.
-__device__ inline bool has_power(float top) { return fabsf(top) <= 0x1p120f; }
+// What a wave's exponentials are relative to: about its largest number, as the power of two
+// whose exponent is top * kHi in fp32.  Up to 2^24 that is rounded by 1 or less, and top * kLo
+// is below 1, so that the largest's own exponential is between 1/4 and 4 (at 1e10 it would be
+// 2^500 or so, infinite).  Larger numbers, -inf and NaN stand for themselves: next to them
+// differences that are not exact in fp32 are beyond what an exponential can show.
+__device__ inline bool has_power(float top) { return fabsf(top) <= 0x1p24f; }
 __device__ inline double ref_of(float top) {
   return has_power(top) ? (double)(top * kHi) * 0.6931471805599453 : (double)top;
 }

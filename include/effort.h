@@ -599,10 +599,11 @@ int effort_kv_accept(const effort_kv_cache* caches, int32_t count, const effort_
    tokens.  The logarithm is rounded to double, then taken from the logit, then
    the score is added: next to a logit of 1e9 that rounding is 2^-24, and from 1e18
    on nothing is left of what a sum of equal logits adds, so that a row of nothing
-   but -3.4e38 continues its beam at its score.  What is forbidden should be -inf.  A beam with ended_dev[b] != 0 has one candidate: itself, with its
-   score unchanged and the token end_token.  A logit of -inf is no candidate; a
-   row with a NaN, +inf or nothing but -inf, or with a score that is not finite,
-   has none.  Where there are fewer than `keep`, the rest are -inf, -1, -1.
+   but -3.4e38 continues its beam at its score.  What is forbidden should be -inf.
+   A beam with ended_dev[b] != 0 has one candidate: itself, with its score
+   unchanged and the token end_token.  A logit of -inf is no candidate; a row with
+   a NaN, +inf or nothing but -inf, or with a score that is not finite, has none.
+   Where there are fewer than `keep`, the rest are -inf, -1, -1.
    Logits: of `dtype`, `stride` elements between rows.  EINVAL: null or misaligned
    pointers, items outside 0..2^24, beams outside 1..EFFORT_BEAM_MAX (2^24 rows
    at most), keep outside 1..EFFORT_BEAM_MAX_KEEP, vocab outside 1..2^20, a

@@ -59,6 +59,28 @@ def check_large(x, s, keep, **kw):
     return got
 
 
+PLACES = {"top": lambda v: slice(v // 3, v // 3 + 1), "all": lambda v: slice(0, v), "first 512": lambda v: slice(0, 512),
+          "a wave's 2048": lambda v: slice(2048, 4096), "the last part": lambda v: slice(v // 2048 * 2048, v)}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [4500, 45077])  # waves of 512 logits, and of 2048
+@pytest.mark.parametrize("place", list(PLACES))
+def test_beams_of_large_finite_logits(dtype, vocab, place):
+    """One logit, a row, or a part that one wave reads, far from the others: forbidden tokens, or sure ones."""
+    dev()
+    rng = np.random.default_rng(61)
+    sizes = [1e6, 2.0 ** 24, 1e8, 1e9, 5e9, 1e10, 1e12, 1e15, 1e20, 1e30, 2.0 ** 120, 3e38]
+    at = [z * sign for z in sizes for sign in (1.0, -1.0)]
+    items, nb = len(at) // 2 * 2, 4  # in beam 0 and 2: the large ones; 1 and 3: ordinary
+    x = rng.standard_normal((items, nb, vocab)) * 3
+    for i in range(items):
+        x[i, 0, PLACES[place](vocab)] = at[i]
+        x[i, 2, PLACES[place](vocab)] = at[(i + 5) % items]
+    s = rng.standard_normal((items, nb)).astype(np.float32) - 12
+    check_large(cuda(x.astype(np.float32)).to(DT[dtype]), cuda(s), 6)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("keep", [3, 64])
 def test_beams_of_rows_of_the_lowest_number_keep_their_scores(dtype, keep):
