@@ -756,16 +756,17 @@ __device__ void join_row(int count, int rows, int r, At at, T* out) {
 
 // Joins the parts that blocks left of an item, and writes the rows that see
 // nothing.  One block per (R rows, head); row tiles of a sequence are counted
-// from first * group / ROWS + s, enough for every sequence before it.
+// from first * group / ROWS + s, enough for every sequence before it.  `first`: the
+// launch's first block of a head.
 template <int DT, int D, int ROWS, int R, bool TREE, int CH>
 __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float* parts, uint32_t nb32,
-                                                      const uint64_t* before) {
+                                                      const uint64_t* before, uint32_t first) {
   typedef typename ElemOf<DT>::T T;
   __shared__ Plan s_plan;
   __shared__ int s_seq;
   const int tid = (int)threadIdx.x, head = (int)blockIdx.y, group = a.q_heads / a.kv_heads;
-  const uint32_t bt = blockIdx.x / (ROWS / R);
-  const int r0 = (int)(blockIdx.x % (ROWS / R)) * R;
+  const uint32_t block = first + blockIdx.x, bt = block / (ROWS / R);
+  const int r0 = (int)(block % (ROWS / R)) * R;
   auto base = [&](int i) { return (int64_t)start_of(a.b, i) * group / ROWS + i; };
   int s = 0;
   if (a.b.seqs > 1) {
@@ -803,9 +804,9 @@ __global__ __launch_bounds__(AT_T) void k_attend_join(AttendArgs a, const float*
   // blocks of its first, last chunk
   const uint64_t b0 = quotient((c0 + 1) * nb - 1, total), b1 = quotient((c1 + 1) * nb - 1, total);
   if (b0 == b1) return;
-  const float* first = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
+  const float* start = parts + (b0 * 2 + 1) * (uint64_t)(ROWS * (D + 2));
   const float* rest = parts + (b0 + 1) * 2 * (uint64_t)(ROWS * (D + 2));
-  auto at = [&](int i) { return i == 0 ? first : rest + (uint64_t)(i - 1) * 2 * (ROWS * (D + 2)); };
+  auto at = [&](int i) { return i == 0 ? start : rest + (uint64_t)(i - 1) * 2 * (ROWS * (D + 2)); };
   // a row behind the last one repeats the block's first
   join_row<D, R, CH == PR_TILE ? 8 : 4>((int)(b1 - b0) + 1, ROWS, mine ? r : r0, at, out);
 }
@@ -1631,10 +1632,10 @@ static hipError_t attend_rt(const AttendArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(tiles * 16 * RT / (many ? 1 : 4)), (unsigned)a.kv_heads);
   if (many)
     hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 1, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts,
-                       (uint32_t)nb, (const uint64_t*)nullptr);
+                       (uint32_t)nb, (const uint64_t*)nullptr, 0u);
   else
     hipLaunchKernelGGL((k_attend_join<DT, D, 16 * RT, 4, TREE, AT_CHUNK>), grid, dim3(AT_T), 0, s, a, parts,
-                       (uint32_t)nb, (const uint64_t*)nullptr);
+                       (uint32_t)nb, (const uint64_t*)nullptr, 0u);
   return hipGetLastError();
 }
 
@@ -1684,14 +1685,18 @@ static hipError_t tree_rt(const AttendArgs& a, hipStream_t s) {
   else
     hipLaunchKernelGGL((k_attend_prompt<DT, FMT, D, false, RT, true>), dim3((unsigned)nb), dim3(AT_T), 0, s, a, parts,
                        0, 1, out_vec);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t blocks = tiles * (prompt_rows<RT>() / 8);
-  if (blocks > 0xFFFFFF) return hipErrorInvalidValue;  // 2^32 threads of a dimension
-  const dim3 rows((unsigned)blocks, (unsigned)a.kv_heads);
-  hipLaunchKernelGGL((k_attend_join<DT, D, prompt_rows<RT>(), 8, true, PR_TILE>), rows, dim3(AT_T), 0, s, a, parts,
-                     (uint32_t)nb, a.b.seqs > 1 ? plan_of<D>(parts, nb, prompt_rows<RT>()) : nullptr);
-  return hipGetLastError();
+  const int64_t blocks = tiles * (prompt_rows<RT>() / 8);  // below 2^28: 2^30 rows, 8 of a block
+  constexpr int64_t most = 0xFFFFFFFFll / AT_T;  // a launch has less than 2^32 threads of a dimension
+  for (int64_t first = 0; first < blocks; first += most) {
+    const dim3 rows((unsigned)(blocks - first < most ? blocks - first : most), (unsigned)a.kv_heads);
+    hipLaunchKernelGGL((k_attend_join<DT, D, prompt_rows<RT>(), 8, true, PR_TILE>), rows, dim3(AT_T), 0, s, a, parts,
+                       (uint32_t)nb, a.b.seqs > 1 ? plan_of<D>(parts, nb, prompt_rows<RT>()) : nullptr, (uint32_t)first);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int DT, int FMT, int D, bool TREE>

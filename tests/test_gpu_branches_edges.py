@@ -1,5 +1,5 @@
 """Edges of the operators for several continuations of a sequence: what 16-bit rows of trees
-keep of their weights, beams whose logits are large."""
+keep of their weights, trees of very many rows, beams whose logits are large."""
 import math
 
 import numpy as np
@@ -35,6 +35,26 @@ def test_trees_keep_the_weights_of_16_bit_rows(heads, group, dim, page, fmt, len
     worst = float((np.abs(got - ref) / (tol + 1e-300)).max())
     say("worst", worst)
     assert worst <= 1.0, worst
+
+
+def test_trees_of_more_rows_than_a_launch_has_blocks():
+    """2^27 rows of a sequence that is no tree become 0, those of a tree behind them what they are alone."""
+    dev()
+    big, new, group, dim = 1 << 21, 40, 64, 64
+    c = Tree(52, [2000], [new], heads=1, group=group, dim=dim, page=64, dtype="bf16")
+    q = c.rand(group)
+    want = c.check_tree(q)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    batch = E.KVBatch(c.batch.page_table.repeat(2, 1), ints([7, 2000]), ints([0, big, big + new]),
+                      parents=torch.cat([ints([-1]).repeat(big), c.batch.parents]))
+    rows = torch.zeros(big + new, group, dim, dtype=torch.bfloat16, device="cuda")
+    rows[big:] = q
+    out = torch.full_like(rows, 3.0)
+    c.cache.attend(batch, rows, out=out)
+    assert not bool(out[:big].any())
+    # another split of the sums: both are within the bound of the 64-bit result
+    ref, tol = R.attend(c.np, c.table, c.lens, c.starts, f64(q), dim ** -0.5, 0, "e4m3", "bf16", c.parents)
+    assert (np.abs(f64(out[big:]) - ref) <= tol).all() and want.shape == q.shape
 
 
 # ---------------------------------------------------------------- beams: large logits
