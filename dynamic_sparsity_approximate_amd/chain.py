@@ -305,8 +305,9 @@ class BeamStep:
     and `scores` [items][beams] say what the beams are now, `ended` which of them
     have taken `end_token` (they stay as they are); the caller writes the tokens'
     embeddings to the step's x.  `short` counts the pages that were missing, at
-    most, in any step: once there are any, the results mean nothing.  The step may
-    be captured once and replayed."""
+    most, in any step: once there are any, the results mean nothing, and the
+    sequences stay empty, so that no page is written that somebody else may hold.
+    The step may be captured once and replayed."""
 
     def __init__(self, step, pages, beams: int, end_token: int = -1):
         import torch
@@ -342,6 +343,8 @@ class BeamStep:
             torch.eq(self.tokens, self.end_token, out=self.ended)
             self.pages.fork(self.parents.view(-1), stream=stream)
             torch.maximum(self.short, self.pages.grow(1, stream=stream), out=self.short)
+            # without room the next tokens would fall on the last ones, in pages that beams share
+            self.pages.kv_lens.mul_(self.short == 0)
         return self.tokens
 
 

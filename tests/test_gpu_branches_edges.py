@@ -1,6 +1,8 @@
 """Edges of the operators for several continuations of a sequence: what 16-bit rows of trees
-keep of their weights, trees of very many rows, beams whose logits are large."""
+keep of their weights, trees of very many rows, beams whose
+logits are large, searches without room."""
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -12,7 +14,7 @@ import _branches as R  # noqa: E402
 import _layer as L  # noqa: E402
 import dynamic_sparsity_approximate_amd as E  # noqa: E402
 from test_gpu_branches import Tree, cuda  # noqa: E402
-from test_gpu_layer import DT, dev, f64, say  # noqa: E402
+from test_gpu_layer import DT, dev, f64, ints, say  # noqa: E402
 
 
 # ---------------------------------------------------------------- trees: what 16-bit rows keep
@@ -44,7 +46,6 @@ def test_trees_of_more_rows_than_a_launch_has_blocks():
     c = Tree(52, [2000], [new], heads=1, group=group, dim=dim, page=64, dtype="bf16")
     q = c.rand(group)
     want = c.check_tree(q)
-    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
     batch = E.KVBatch(c.batch.page_table.repeat(2, 1), ints([7, 2000]), ints([0, big, big + new]),
                       parents=torch.cat([ints([-1]).repeat(big), c.batch.parents]))
     rows = torch.zeros(big + new, group, dim, dtype=torch.bfloat16, device="cuda")
@@ -129,3 +130,66 @@ def test_beams_of_the_largest_scores_and_logits():
     s = np.array([[-3.4e38, -5, -1e30, -6], [-2, 3.4e38, -3.4e38, 1e30], [3.4e38, -3.4e38, 3e38, -3e38]], np.float32)
     for keep in (5, 128):
         check_large(cuda(x), cuda(s), keep)
+
+
+# ---------------------------------------------------------------- searches
+
+class Search:
+    """A BeamStep over a step of given logits that appends a key and a value for each row."""
+
+    def __init__(self, prompt, items, beams, pages, cols, end=-1, T=16, vocab=50, seed=71):
+        dev()
+        rng = np.random.default_rng(seed)
+        rows = items * beams
+        self.cache = E.KVCache(pages, 2, 64, T)
+        self.pages = E.KVPages([self.cache], ints([[-1] * cols] * rows), ints([0] * rows))
+        batch = E.KVBatch(self.pages.page_table, self.pages.kv_lens, ints(list(range(rows + 1))))
+        self.logits = torch.zeros(rows, vocab, device="cuda")
+        self.kv = cuda(rng.standard_normal((rows, 2, 64)).astype(np.float32))
+
+        def enqueue(effort, stream=None):
+            self.cache.append(batch, self.kv, self.kv, stream=stream)
+            return self.logits
+
+        # every item's prompt in its first beam, then in all
+        assert int(self.pages.grow(ints([prompt if b % beams == 0 else 0 for b in range(rows)]))) == 0
+        first = E.KVBatch(self.pages.page_table, self.pages.kv_lens,
+                          ints([prompt * (-(-b // beams)) for b in range(rows + 1)]))
+        x = cuda(rng.standard_normal((prompt * items, 2, 64)).astype(np.float32))
+        self.cache.append(first, x, x)
+        self.pages.fork(ints([b // beams * beams for b in range(rows)]))
+        assert int(self.pages.grow(1)) == 0
+        step = SimpleNamespace(x=torch.zeros(rows, 8, device="cuda"), batch=batch, caches=[self.cache], enqueue=enqueue)
+        self.search = E.BeamStep(step, self.pages, beams, end_token=end)
+
+    def state(self):
+        torch.cuda.synchronize()
+        return [t.clone() for t in (self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale)]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_search_without_room_writes_nothing_more(captured):
+    """Beams that share their last page when the pages run out: later steps leave the cache as it is."""
+    s = Search(20, 1, 4, pages=6, cols=8)  # the prompt's full page, a copy of the other for each beam, one free
+    rng = np.random.default_rng(72)
+    run = lambda: s.search.enqueue(1.0)  # noqa: E731
+    if captured:
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            s.search.enqueue(1.0, side)
+        run = graph.replay
+    steps = 0
+    while int(s.search.short) == 0:
+        s.logits.copy_(torch.from_numpy(rng.standard_normal(s.logits.shape) * 5))
+        run()
+        steps += 1
+        assert steps < 20
+    before = s.state()
+    for _ in range(3):
+        s.kv.copy_(torch.from_numpy(rng.standard_normal(s.kv.shape) * 3))
+        run()
+        (torch.ones(1000, device="cuda") * 2).sum().item()
+        assert all(torch.equal(a, b) for a, b in zip(before, s.state()))
+        assert int(s.search.short) > 0 and not s.pages.kv_lens.any()
+    held = s.pages.page_table[(s.pages.page_table >= 0)].long().cpu()
+    assert s.pages.refs.tolist() == torch.bincount(held, minlength=6).tolist()
