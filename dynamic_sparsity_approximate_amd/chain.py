@@ -303,8 +303,9 @@ class BeamStep:
     token, and `scores` [items][beams] are 0 for one beam of an item and -inf for
     the others (as they are at first).  After each step `tokens`, `parents` (rows)
     and `scores` [items][beams] say what the beams are now, `ended` which of them
-    have taken `end_token` (they stay as they are); the caller writes the tokens'
-    embeddings to the step's x.  `short` counts the pages that were missing, at
+    have taken `end_token`: those stay as they are, end_token the last of their
+    kv_lens tokens, which they append again in each step.  The caller writes the
+    tokens' embeddings to the step's x.  `short` counts the pages that were missing, at
     most, in any step: once there are any, the results mean nothing, and the
     sequences stay empty, so that no page is written that somebody else may hold.
     The step may be captured once and replayed."""
@@ -340,6 +341,8 @@ class BeamStep:
             logits = self.step.enqueue(effort, stream)
             beam_select(logits, self.scores, ended=self.ended, end_token=self.end_token,
                         out=(self.scores, self.parents, self.tokens), stream=stream)
+            # a beam that had ended before takes its last token's room again instead of more
+            self.pages.kv_lens.sub_(self.ended.view(torch.uint8).view(-1))
             torch.eq(self.tokens, self.end_token, out=self.ended)
             self.pages.fork(self.parents.view(-1), stream=stream)
             torch.maximum(self.short, self.pages.grow(1, stream=stream), out=self.short)

@@ -193,3 +193,38 @@ def test_a_search_without_room_writes_nothing_more(captured):
         assert int(s.search.short) > 0 and not s.pages.kv_lens.any()
     held = s.pages.page_table[(s.pages.page_table >= 0)].long().cpu()
     assert s.pages.refs.tolist() == torch.bincount(held, minlength=6).tolist()
+
+
+@pytest.mark.parametrize("prompt", [14, 15, 20])  # end tokens inside a page, at its end, at its beginning
+def test_ended_beams_keep_their_length_and_room(prompt):
+    """Beams that end early stay as they are, however many steps follow; the others go on."""
+    s = Search(prompt, 2, 2, pages=20, cols=3, end=9)
+    rng = np.random.default_rng(73)
+    length, held = [prompt + 1] * 4, None
+    for step in range(40):
+        x = rng.standard_normal(s.logits.shape) * 0.1
+        x[:, 9] = -50.0
+        if step == 1:
+            x[2:, 9] = 50.0  # the second item's beams end
+        if step == 5:
+            x[:2, 9] = 50.0  # the first's
+        s.logits.copy_(torch.from_numpy(x))
+        was = s.search.ended.view(-1).tolist()
+        s.search.enqueue(1.0)
+        torch.cuda.synchronize()
+        parents = s.search.parents.view(-1).tolist()
+        length = [length[p] + (0 if was[p] else 1) for p in parents]
+        assert s.pages.kv_lens.tolist() == length
+        assert s.search.ended.view(-1).tolist() == [step >= 5, step >= 5, step >= 1, step >= 1]
+        assert int(s.search.short) == 0
+        table = s.pages.page_table[s.pages.page_table >= 0].long().cpu()
+        assert s.pages.refs.tolist() == torch.bincount(table, minlength=20).tolist()
+        if step >= 7:  # nothing changes any more: not the tables but for a last page, not what they stand for
+            now = []
+            for b in range(4):
+                pos = torch.arange(length[b] - 1)
+                at = s.pages.page_table[b].cpu()[pos // 16].long()
+                now.append(s.cache.k.cpu()[at, :, pos % 16].clone())
+            assert held is None or all(torch.equal(a, b) for a, b in zip(held, now))
+            held = now
+    assert length == [prompt + 7, prompt + 7, prompt + 3, prompt + 3]
