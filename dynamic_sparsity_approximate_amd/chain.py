@@ -337,6 +337,8 @@ class BeamStep:
         from .pages import beam_select
 
         dev = self.step.x.device
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
         with torch.cuda.device(dev), torch.cuda.stream(stream):  # (None changes nothing)
             logits = self.step.enqueue(effort, stream)
             beam_select(logits, self.scores, ended=self.ended, end_token=self.end_token,

@@ -228,3 +228,18 @@ def test_ended_beams_keep_their_length_and_room(prompt):
             assert held is None or all(torch.equal(a, b) for a, b in zip(held, now))
             held = now
     assert length == [prompt + 7, prompt + 7, prompt + 3, prompt + 3]
+
+
+def test_a_search_on_a_streams_handle():
+    """`stream` as everywhere else: None, a stream, or its handle."""
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side, side.cuda_stream):
+        s = Search(20, 1, 3, pages=20, cols=8)
+        s.logits.copy_(torch.from_numpy(np.random.default_rng(74).standard_normal(s.logits.shape)))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            s.search.enqueue(1.0, stream)
+        got.append([s.search.scores, s.search.tokens, s.pages.kv_lens, s.pages.page_table] + s.state())
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
