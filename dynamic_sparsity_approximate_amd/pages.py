@@ -143,8 +143,8 @@ def kv_accept(caches, batch: KVBatch, leaf, lens_out=None, stream=None):
     _vector(leaf, "leaf", batch.seqs, s.device)
     out = batch.kv_lens if lens_out is None else _vector(lens_out, "lens_out", batch.seqs, s.device)
     n = _bytes(B.effort_kv_accept_workspace_bytes, batch.seqs) if batch.parents is not None else 0
-    # rows of the call: no more than the parents, where there are any
-    tokens = batch.parents.shape[0] if batch.parents is not None else 1 << 24
+    # rows of the call: as many as a call may have, and no more than the parents, where there are any
+    tokens = 1 << 24 if batch.parents is None else min(1 << 24, batch.parents.shape[0])
 
     def call(handle):
         ws = leaf.new_empty(n, dtype=torch.uint8) if n else None

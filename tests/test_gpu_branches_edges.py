@@ -243,3 +243,16 @@ def test_a_search_on_a_streams_handle():
         got.append([s.search.scores, s.search.tokens, s.pages.kv_lens, s.pages.page_table] + s.state())
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+# ---------------------------------------------------------------- paths: more parents than rows
+
+def test_accept_with_more_parents_than_a_call_has_rows():
+    """`parents` may be longer than the rows, by any number: a buffer for the largest batch."""
+    c = Tree(55, [70, 40], [9, 12], page=16, parents=R.random_tree(np.random.default_rng(2), 9) * 2 + [0, 1, 2])
+    long = torch.full(((1 << 24) + 5,), -1, dtype=torch.int32, device="cuda")
+    long[:21] = c.batch.parents
+    batch = E.KVBatch(c.batch.page_table, c.batch.kv_lens, c.batch.q_starts, parents=long)
+    got = E.kv_accept([c.cache], batch, ints([8, 11]), lens_out=ints([0, 0]))
+    assert got.tolist() == R.accept([c.np], "e4m3", c.table, c.lens, c.starts, 21, c.parents, [8, 11])
+    c.check_cache()
