@@ -138,14 +138,27 @@ __device__ inline double square_of(const float* x, double per_dim, double eps, b
   return __builtin_fma(sum_of_lanes(sum, sixteen), per_dim, eps);
 }
 
+// Whether weights are neither 0 nor between 2^-60 and 2^60 in size.
+__device__ inline bool are_wide(const float* weight) {
+  uint32_t off = 0;
+#pragma unroll
+  for (int j = 0; j < 2 * CP; ++j) {
+    const uint32_t b = __float_as_uint(weight[j]) & 0x7FFFFFFFu, o = b ? b - (67u << 23) : 0;
+    off = o > off ? o : off;
+  }
+  return off >= 120u << 23;  // exponents 67 to 186, less 127
+}
+
 // A query's chunk normed: 1 / rms to some 2^-45 (the instruction's 2^-24 and a step of
 // Newton's; the exact root and quotient, and products in double, cost the prompts above
 // 1.7 us more), its product with the weight rounded to fp32, and the element's product
-// with that.
-__device__ inline void norm_near(float* x, const float* weight, double square) {
+// with that.  Where 1 / rms is beyond 2^60 or below 2^-60, or a weight is (`wide`), the
+// product with the weight might leave fp32's normal numbers and the result not: then all
+// is done in double.
+__device__ inline void norm_near(float* x, const float* weight, bool wide, double square) {
   const double near = __builtin_amdgcn_rsq(square);
   const double by = square == (double)INFINITY ? 0.0 : near * (1.5 - 0.5 * square * near * near);
-  if (__any(!(by > 0x1p-60 && by < 0x1p60))) {  // the weights might leave fp32
+  if (wide || __any(!(by > 0x1p-60 && by < 0x1p60))) {
 #pragma unroll
     for (int j = 0; j < 2 * CP; ++j) x[j] = (float)((double)x[j] * by * (double)weight[j]);
   } else {
@@ -239,8 +252,10 @@ void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token, in
     if (k.rotated) load_rope(rope + pos * half + k.pair, cs);
     const bool norm = EX && a.q_norm != nullptr;
     float weight[2 * CP];
+    bool wide = false;
     auto load_weights = [&](int h) {
       load_chunk(static_cast<const T*>(a.q_norm) + at(h) / (uint32_t)dim * a.q_norm_stride, k, false, 1, weight);
+      wide = __any(are_wide(weight));
     };
     if (norm && a.q_norm_stride == 0) load_weights(0);
 #pragma unroll
@@ -249,7 +264,7 @@ void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token, in
       float y[2 * CP], z[2 * CP];
       if (norm) {
         if (a.q_norm_stride) load_weights(h);
-        norm_near(x[h], weight, square_of(x[h], per_dim, a.eps, sixteen));
+        norm_near(x[h], weight, wide, square_of(x[h], per_dim, a.eps, sixteen));
       }
       from_order(k.rotated && inter, x[h]);
       if (k.rotated) {
