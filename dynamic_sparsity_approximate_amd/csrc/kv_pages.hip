@@ -23,7 +23,7 @@ __device__ inline bool is_page(int32_t p, int64_t pages) { return p >= 0 && p < 
 // ---------------------------------------------------------------- fork
 
 // Entries of a block's columns of all sequences, in LDS.
-constexpr int FK_ENTRIES = 16384, FK_COLS = 64;
+constexpr int FK_ENTRIES = 16384, FK_COLS = 64, FK_BLOCKS = 1 << 16;
 
 // New entry (s, c) is the old (source[s], c) where that is in front of the new end, so that
 // columns are independent: a block reads its columns of every sequence before it writes any.
@@ -33,7 +33,6 @@ __global__ __launch_bounds__(PG_T) void k_fork(BookArgs b, const int32_t* source
   __shared__ int32_t s_src[EFFORT_KV_MAX_SEQS], s_len[EFFORT_KV_MAX_SEQS];
   __shared__ int s_last;
   const int tid = (int)threadIdx.x, cols = 1 << cols_log, n = b.seqs << cols_log;
-  const int32_t col0 = (int32_t)blockIdx.x << cols_log;
   if (tid < b.seqs) {
     const int32_t src = source[tid];
     const bool ok = src >= 0 && src < b.seqs;
@@ -42,22 +41,25 @@ __global__ __launch_bounds__(PG_T) void k_fork(BookArgs b, const int32_t* source
     s_src[tid] = ok ? src : -1;
     s_len[tid] = len < 0 ? 0 : len;
   }
-  for (int i = tid; i < n; i += PG_T) {
-    const int32_t c = col0 + (i & (cols - 1));
-    s_old[i] = c < b.max_pages ? b.table[(i >> cols_log) * b.table_stride + c] : -1;
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += PG_T) {
-    const int s = i >> cols_log, c = i & (cols - 1);
-    if (col0 + c >= b.max_pages) continue;
-    int32_t now = -1;
-    if (s_src[s] >= 0 && (int64_t)(col0 + c) * b.page_tokens < s_len[s]) now = s_old[(s_src[s] << cols_log) + c];
-    if (!is_page(now, b.pages)) now = -1;
-    const int32_t old = s_old[i];
-    if (now == old) continue;
-    b.table[s * b.table_stride + col0 + c] = now;
-    if (is_page(old, b.pages)) atomicSub(b.refs + old, 1);
-    if (now >= 0) atomicAdd(b.refs + now, 1);
+  for (int32_t col0 = (int32_t)blockIdx.x << cols_log; col0 < b.max_pages; col0 += (int32_t)gridDim.x << cols_log) {
+    for (int i = tid; i < n; i += PG_T) {
+      const int32_t c = col0 + (i & (cols - 1));
+      s_old[i] = c < b.max_pages ? b.table[(i >> cols_log) * b.table_stride + c] : -1;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += PG_T) {
+      const int s = i >> cols_log, c = i & (cols - 1);
+      if (col0 + c >= b.max_pages) continue;
+      int32_t now = -1;
+      if (s_src[s] >= 0 && (int64_t)(col0 + c) * b.page_tokens < s_len[s]) now = s_old[(s_src[s] << cols_log) + c];
+      if (!is_page(now, b.pages)) now = -1;
+      const int32_t old = s_old[i];
+      if (now == old) continue;
+      b.table[s * b.table_stride + col0 + c] = now;
+      if (is_page(old, b.pages)) atomicSub(b.refs + old, 1);
+      if (now >= 0) atomicAdd(b.refs + now, 1);
+    }
+    __syncthreads();
   }
   if (tid == 0) {
     s_last = 1;
@@ -75,8 +77,10 @@ __global__ __launch_bounds__(PG_T) void k_fork(BookArgs b, const int32_t* source
 hipError_t launch_fork(const BookArgs& b, const int32_t* source, const int32_t* keep, hipStream_t s) {
   int cols_log = 0;
   while ((1 << cols_log) < FK_COLS && (b.seqs << (cols_log + 1)) <= FK_ENTRIES) ++cols_log;
-  const unsigned blocks = (unsigned)((b.max_pages + (1 << cols_log) - 1) >> cols_log);
-  hipLaunchKernelGGL(k_fork, dim3(blocks), dim3(PG_T), 0, s, b, source, keep, cols_log);
+  const int64_t blocks = ((int64_t)b.max_pages + (1 << cols_log) - 1) >> cols_log;
+  // tables of more columns than blocks: a launch has less than 2^32 threads
+  const unsigned grid = (unsigned)(blocks < FK_BLOCKS ? blocks : FK_BLOCKS);
+  hipLaunchKernelGGL(k_fork, dim3(grid), dim3(PG_T), 0, s, b, source, keep, cols_log);
   return hipGetLastError();
 }
 

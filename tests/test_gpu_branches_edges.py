@@ -245,6 +245,42 @@ def test_a_search_on_a_streams_handle():
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
 
 
+# ---------------------------------------------------------------- pages: wide tables
+
+@pytest.mark.parametrize("seqs,cols", [(3, (1 << 22) + 77), (513, 1 << 26)])
+def test_fork_of_tables_with_very_many_columns(seqs, cols):
+    """More columns than a launch has blocks for; of the widest tables, more than it has threads for."""
+    dev()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * seqs * cols + (8 << 30):
+        pytest.skip("the table needs %d GB" % (4 * seqs * cols >> 30))
+    cache = E.KVCache(40, 1, 64, 16)
+    table = torch.full((seqs, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, :7] = ints([5, 6, 7, 8, 9, 10, 11])
+    at = [0, 64, 1 << 20, (1 << 22) - 1, 1 << 22, cols - 1]  # entries of others, near and far
+    for i, c in enumerate(at):
+        table[1 + i % 2, c] = 20 + i
+    refs = torch.zeros(40, dtype=torch.int32, device="cuda")
+    refs[5:12] = 1
+    refs[20:20 + len(at)] = 1
+    pages = E.KVPages([cache], table, ints([100] + [16 * cols] * 2 + [0] * (seqs - 3)), refs=refs)
+    pages.fork(ints([0, 0, 2] + [0] * (seqs - 3)))
+    want = torch.full((seqs, 8), -1, dtype=torch.int32)
+    want[:, :7] = torch.arange(5, 12)
+    want[2] = -1
+    assert torch.equal(table[:, :8].cpu(), want)
+    assert not (table[1, 8:] >= 0).any()  # the second follows the first, the third itself
+    assert [int(table[2, c]) for c in at] == [20 + i if i % 2 else -1 for i in range(len(at))]
+    held = [0] * 40
+    held[5:12] = [seqs - 1] * 7
+    for i in range(1, len(at), 2):
+        held[20 + i] = 1
+    assert refs.tolist() == held
+    assert pages.kv_lens.tolist() == [100, 100, 16 * cols] + [100] * (seqs - 3)
+    del table, pages
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- paths: more parents than rows
 
 def test_accept_with_more_parents_than_a_call_has_rows():
