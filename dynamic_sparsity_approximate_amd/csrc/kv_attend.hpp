@@ -876,7 +876,8 @@ __host__ __device__ inline uint64_t* plan_of(float* parts, int64_t blocks, int r
 // cache: fewer blocks, so fewer parts, cost more than they save (256 blocks: 63.0 and
 // 6.4, 206 and 6.2).
 template <int DT, int FMT, int D, bool ONE, int RT, bool TREE>
-__global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 ? 2 : 3) : DT == EFFORT_F32 && D == 128 ? 1 : 2)
+__global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 || (TREE && D == 128) ? 2 : 3)
+                                           : DT == EFFORT_F32 && D == 128 ? 1 : 2)
 void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, int32_t out_vec) {
   typedef typename ElemOf<DT>::T T;
   constexpr bool SPLIT = DT == EFFORT_F32, LOW = SPLIT || TREE;  // queries, weights in two parts
