@@ -1,5 +1,5 @@
 // beam.hip -- beam search's selection: of an item's beams b and their continuations t the
-// `keep` best by score[b] + logit[b][t] - log(sum over t of exp(logit[b][t])).
+// `keep` best by score[b] + (logit[b][t] - log(sum over t of exp(logit[b][t]))).
 //
 // One pass reads the logits (k_beam_read): a wave has BM_WAVE neighbouring logits of a row
 // and leaves their maximum, the sum of their exponentials, and the maximum of every BM_GROUP
@@ -194,8 +194,8 @@ __device__ inline void rank_list(const Cand* list, int n, int keep, Put put) {
   }
 }
 
-// Bound by its chain of steps: 32 items of 8 beams of 100003 logits, 16 kept, take 10.0 us,
-// one of 4 beams of 32000 8.3 (about 3 the sums, 1 each the bound, the runs, the groups and
+// Bound by its chain of steps: 32 items of 8 beams of 100003 logits, 16 kept, take 9.8 us,
+// one of 4 beams of 32000 8.7 (about 3 the sums, 1 each the bound, the runs, the groups and
 // the elements); looking at all groups instead of runs first, 20.8 and 9.4.
 template <int DT>
 __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* maxima, const Part* parts, int32_t per_row,

@@ -186,7 +186,9 @@ constexpr int AP_QH = 4;
 // ones.  A tree's depths come from its parents in LDS, asked for before the rows.  The
 // prompts above with both norms: 50.6 us, with caches warm 41.5 (45 with the 102 registers,
 // for four waves a SIMD, that it would take for itself; fp32 rows have no room for five); one
-// token 4.7 (without norms 4.1), 12 trees of up to 16 6.0.
+// token 4.7 (without norms 4.1), 12 trees of up to 16 6.0.  By pages of 16, 32, 64 and 128
+// tokens such prompts take 61, 50, 49 and 63 us (those of 128 have eight chunks a thread,
+// 150 registers, three waves a SIMD), fp32 ones 85, 78, 76 and 78.
 template <int DT, int FMT, int IT, bool EX>
 __global__ __launch_bounds__(AP_T, EX && IT == 4 && DT != EFFORT_F32 ? 5 : 1)
 void k_append(AppendArgs a, uint32_t first, int32_t units, int32_t per_token, int32_t kv_vec, int32_t q_vec) {

@@ -19,8 +19,8 @@
 // 3 per cent, but two bf16 prompts of 4096 tokens 426 us instead of 317, for
 // errors of 2.07e-4 instead of 2.7e-4 (fp16) or 1.65e-3 instead of 1.66e-3 (bf16)
 // of the outputs, most of which is their own last rounding.  Trees keep both parts
-// whichever kernel takes them (eight trees of 32 tokens 74 us instead of 64, one of 64
-// 163 instead of 138): what a row becomes does not depend on how wide its table is.
+// whichever kernel takes them (eight trees of up to 32 tokens 64.5 us instead of 58.6, one
+// of 64 171 instead of 146): what a row becomes does not depend on how wide its table is.
 //
 // In a tree a new token sees the committed tokens, in front of the sequence's new ones,
 // and of those its ancestors and itself; a window counts by position, which is the first
@@ -48,7 +48,7 @@ constexpr int AT_CHUNK = AT_W * AT_TILE; // tokens of one step of a block
 constexpr int PR_TILE = 64;              // tokens of one step of a block whose waves share them
 // Steps that beginning and ending an item cost such a block where blocks share them (with
 // none, the blocks that have parts of two items end last: eight trees of 32 over up to 8192
-// tokens 57.2 us instead of 50.6, 24 of up to 25 behind a window of 1000 24.1 instead of 20.6).
+// tokens 61.8 us instead of 56.1, 24 of up to 25 behind a window of 1000 24.8 instead of 20.8).
 constexpr int PR_BEGIN = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 // Weights are held times 2^6 relative to a row's reference score, which follows
@@ -296,7 +296,8 @@ __device__ inline int owner(const AttendArgs& a, const Plan& p, uint64_t c, int 
 // Bound by memory once there are some ten chunks for each block: 64 sequences of
 // 4000 to 16384 int8 tokens are read at 5.2 TB/s, one of 200003 e4m3 tokens at
 // 5.0, 16 of 1000 to 8192 at 4.1 (with the join 3.6).
-// `RT`: 16-row tiles of an item, `NW`: waves of a block.
+// `RT`: 16-row tiles of an item, `NW`: waves of a block.  (Trees of fp32 rows, RT 2, 128
+// elements, shared: 6 to 8 registers are in scratch memory.)
 template <int DT, int FMT, int D, int RT, int NW, bool WHOLE, bool TREE>
 __global__ __launch_bounds__(64 * NW, 2) void k_attend_split(AttendArgs a, float* parts) {
   typedef typename ElemOf<DT>::T T;
@@ -869,12 +870,16 @@ __host__ __device__ inline uint64_t* plan_of(float* parts, int64_t blocks, int r
 // TREE: a tree has few rows, and a batch's lengths are unequal, so that blocks (two
 // a CU) share all items' steps evenly, in order, as in k_attend_split, and
 // k_attend_join joins their parts.  Eight trees of 32 tokens, 4 query heads a
-// group, over 1365 to 8192 tokens, bf16: 50.6 us and 9.2 for the join (every
-// item in equal parts, as prompts are: 73 and 6); 64 tokens over 100003 int8 ones:
-// 152 and 9.2 (196 and 7), of which each 25000 tokens are 32, 820 TFLOP/s, and the
-// blocks' beginnings and ends 17.  The parts are as large as what is read of the
-// cache: fewer blocks, so fewer parts, cost more than they save (256 blocks: 63.0 and
-// 6.4, 206 and 6.2).
+// group, over 1365 to 8192 tokens, bf16: 56.1 us and 9.2 for the join; 64 tokens over
+// 100003 int8 ones: 156 and 9.0, of which each 25000 tokens are 37, 700 TFLOP/s
+// without the products of the weights' low parts.  (With the weights in one part 50.6;
+// with every item in equal parts, as prompts are, that was 73 and 6.)  The parts are as
+// large as what is read of the cache: fewer blocks, so fewer parts, cost more than
+// they save (256 blocks: 66.8 and 6.4, 215 and 6.2).
+// The instances of two row tiles a wave, 128 elements and 16-bit rows keep 3 to 5 registers
+// of what an item begins with in scratch memory where ONE.  Those of fp32 rows leave room for one
+// block a CU only, so that their blocks run in two rounds (eight trees of 32 over 8192
+// tokens each: 120 us the call, bf16 74).
 template <int DT, int FMT, int D, bool ONE, int RT, bool TREE>
 __global__ __launch_bounds__(AT_T, RT == 1 ? (DT == EFFORT_F32 || (TREE && D == 128) ? 2 : 3)
                                            : DT == EFFORT_F32 && D == 128 ? 1 : 2)
@@ -1566,7 +1571,9 @@ static int64_t split_blocks() { return 2 * (int64_t)cu_count(); }
 // rows: 8.1 and 11.2 us at 250 tokens of one sequence, 12.2 and 11.1 at 1000;
 // 10.4 and 17.2 at 500 of 16, 32.2 and 36.5 at 1000 of 64.  Two row tiles (5
 // tokens behind a window of 512, 8 sequences): 14.9 and 22.9, of 64: 42.2 and
-// 40.9; of 896, one sequence: 17.8 and 13.9, 64: 55.1 and 48.8, so 640 there.
+// 40.9; of 896, one sequence: 17.8 and 13.9, 64: 55.1 and 48.8, so 640 there.  (A window
+// counts with the 128 tokens that its rows' own positions may add, see span_of: those
+// of 897 to 1024 tokens are shared out, too.)
 static int64_t whole_tokens(int rt) { return rt == 2 ? 640 : 1024; }
 
 // Tokens that a row of the call may see: all that the host knows of lengths.
@@ -1670,6 +1677,9 @@ static bool tree_whole(const AttendArgs& a) {
   const int64_t items = ((int64_t)a.b.tokens * (a.q_heads / a.kv_heads) + 15) / 16 * a.kv_heads;
   return span_of(a) <= whole_tokens(1) && items <= 3 * (int64_t)cu_count();
 }
+// Blocks of 64 rows where a tree fits one, bf16, 4 query heads a group: 16 tokens of 8
+// sequences over 8192 51.4 us, of one over 100000 72.9, with 128 rows 68.0 and 98.2; of 128 rows
+// where it does not: 20 and 32 tokens of 8 sequences 69.4 and 73.8, with 64 84.7 and 85.7.
 static int tree_rows(int32_t seqs, int64_t tokens, int32_t group) {
   return tokens * group <= 64 * (int64_t)seqs ? 1 : 2;
 }
