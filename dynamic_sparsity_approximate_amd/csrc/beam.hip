@@ -51,8 +51,8 @@ __device__ inline float dpp_top(float x) {
 constexpr float kHi = 1.4426950408889634f, kLo = 1.925963033500995e-8f;  // log2(e)
 // What a wave's exponentials are relative to: about its largest number, as the power of two
 // whose exponent is top * kHi in fp32.  Up to 2^24 that is rounded by 1 or less, and top * kLo
-// is below 1, so that the largest's own exponential is between 1/4 and 4 (at 1e10 it would be
-// 2^500 or so, infinite).  Larger numbers, -inf and NaN stand for themselves: next to them
+// is below 1, so that the largest's own exponential is between 1/4 and 4 (at -1e10 it would be
+// 2^247, infinite).  Larger numbers, -inf and NaN stand for themselves: next to them
 // differences that are not exact in fp32 are beyond what an exponential can show.
 __device__ inline bool has_power(float top) { return fabsf(top) <= 0x1p24f; }
 __device__ inline double ref_of(float top) {
@@ -281,7 +281,9 @@ __global__ __launch_bounds__(BP_T) void k_beam_pick(BeamArgs a, const float* max
     }
   };
   float best = -INFINITY;
-  each_run(0, n, [&](float x, int b, int) __attribute__((always_inline)) { best = fmaxf(best, (x - s_near[b]) + s_score[b]); });
+  each_run(0, n, [&](float x, int b, int) __attribute__((always_inline)) {
+    best = fmaxf(best, (x - s_near[b]) + s_score[b]);
+  });
   best = fmaxf(best, __shfl_xor(best, 1));
   best = fmaxf(best, __shfl_xor(best, 2));
   const uint32_t top = order_of(best);

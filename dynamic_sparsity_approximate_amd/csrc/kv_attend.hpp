@@ -20,7 +20,7 @@
 // errors of 2.07e-4 instead of 2.7e-4 (fp16) or 1.65e-3 instead of 1.66e-3 (bf16)
 // of the outputs, most of which is their own last rounding.  Trees keep both parts
 // whichever kernel takes them (eight trees of up to 32 tokens 64.5 us instead of 58.6, one
-// of 64 171 instead of 146): what a row becomes does not depend on how wide its table is.
+// of 64 171 instead of 146): what a row keeps does not depend on how wide its table is.
 //
 // In a tree a new token sees the committed tokens, in front of the sequence's new ones,
 // and of those its ancestors and itself; a window counts by position, which is the first
@@ -1401,6 +1401,8 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
         float sum[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sum[rt] = 0.0f;
+        // A number that the compiler does not know, for products that it would make subtractions of:
+        // those take 16-bit numbers after a conversion only.
         float minus = -1.0f;
         if (TREE) asm("" : "+s"(minus));
         h8 ph[RT][2], pl[RT][2];
@@ -1425,7 +1427,7 @@ void k_attend_prompt(AttendArgs a, float* parts, int32_t tiles, int32_t splits, 
               ph[rt][u >> 1][e] = high[0];
               ph[rt][u >> 1][e + 1] = high[1];
               if (LOW) {
-                // (exact: as a product of 32 bits that takes the 16-bit number as it is)
+                // (exact: what is left off has no more bits than w)
                 const h2 low = {(_Float16)__builtin_fmaf((float)high[0], minus, w[r]),
                                 (_Float16)__builtin_fmaf((float)high[1], minus, w[r + 1])};
                 pl[rt][u >> 1][e] = low[0];

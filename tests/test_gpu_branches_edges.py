@@ -298,8 +298,8 @@ def test_accept_with_more_parents_than_a_call_has_rows():
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("heads", [False, True])  # weights of each head, or shared
-@pytest.mark.parametrize("size,weight", [(2.0 ** 58, 1e-25), (2.0 ** -58, 1e30), (1.0, 1e-37), (1.0, 1e36), (2.0 ** 55, 1e-36),
-                                         (2.0 ** -50, 1e37), (1.0, 0.0)])
+@pytest.mark.parametrize("size,weight", [(2.0 ** 58, 1e-25), (2.0 ** -58, 1e30), (1.0, 1e-37), (1.0, 1e36),
+                                         (2.0 ** 55, 1e-36), (2.0 ** -50, 1e37), (1.0, 0.0)])
 def test_head_norms_with_weights_of_any_size(size, weight, heads, dtype):
     """The weight's product with 1 / rms may leave fp32 where the normed element does not."""
     lens, new = [40, 7], [21, 7]
@@ -309,7 +309,8 @@ def test_head_norms_with_weights_of_any_size(size, weight, heads, dtype):
     w[..., ::3] *= weight
     w = cuda(w.astype(np.float32)).to(DT[dtype])
     got = c.cache.append(c.batch, k, v, q=q, q_norm=w, eps=0.0)
-    ref, qsize = R.append(c.np, c.table, lens, c.starts, f64(q), f64(k), f64(v), None, False, "e4m3", None, f64(w), None, 0.0)
+    ref, qsize = R.append(c.np, c.table, lens, c.starts, f64(q), f64(k), f64(v), None, False, "e4m3", None, f64(w), None,
+                          0.0)
     # 1 / rms, its product with the weight, that with the element, and the result: four roundings to fp32 at most
     # (2^-22 in all), and one to the result's type; the least numbers are 2^-149 apart in fp32, 2^-133 in bf16, and
     # a rounding among them is off by half of that: the element's in fp32 and the result's
